@@ -18,13 +18,14 @@ _VARIANT = os.environ.get("SLA_LIBRARY_VARIANT", "")
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                          f"libsla{'_' + _VARIANT if _VARIANT else ''}.so")
 
-SLA_F64, SLA_F32 = 0, 1
+SLA_F64, SLA_F32, SLA_BF16, SLA_F16 = 0, 1, 2, 3
 SLA_OK, SLA_ERR_INVALID, SLA_ERR_CUDA, SLA_ERR_OOM, SLA_ERR_TIMEOUT, SLA_ERR_UNSUPPORTED = range(6)
 SLA_CONVERGED, SLA_NOT_CONVERGED, SLA_BREAKDOWN, SLA_NONFINITE, SLA_FIXED_DONE, SLA_TIMED_OUT = range(6)
 SLA_FLAG_VALIDATE, SLA_FLAG_SYMMETRIC, SLA_FLAG_BUILD_TRANSPOSE = 1, 2, 4
 SLA_STRATEGY_AUTO, SLA_STRATEGY_GRID, SLA_STRATEGY_BLOCK, SLA_STRATEGY_CLUSTER = 0, 1, 2, 3
 SLA_OP_SPMV, SLA_OP_CG, SLA_OP_ADJOINT, SLA_OP_GRAD = 0, 1, 2, 3
 SLA_GRAD_ACCUMULATE, SLA_GRAD_SHIFT_SHARED = 1, 2
+SLA_NORM_L2, SLA_NORM_MAX = 0, 1
 
 STATUS_NAMES = {0: "converged", 1: "not_converged", 2: "breakdown", 3: "nonfinite",
                 4: "fixed_done", 5: "timed_out"}
@@ -63,6 +64,18 @@ class sla_csr_props(ctypes.Structure):
                 ("interleaved", ctypes.c_int32)]
 
 
+class sla_attn_opts(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("scale", ctypes.c_double),
+                ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("do_stride", ctypes.c_int64 * 3)]
+
+
+class sla_tensor(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("dtype", ctypes.c_int64)]
+
+
 _P = ctypes.c_void_p
 _I32, _I64, _U32, _F64, _SZ = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_double, ctypes.c_size_t
 
@@ -91,6 +104,14 @@ _SIGNATURES = {
     "sla_edges_workspace_bytes": ([_P], _SZ),
     "sla_laplacian_grad_values": ([_P, _P, _P, _P, _I32, _P, _SZ, _P], _I32),
     "sla_laplacian_grad": ([_P, _P, _P, _P, _P, _I32, _P, _SZ, _P], _I32),
+    "sla_attention_prepare": ([_P, _I32, _P], _I32),
+    "sla_attention_workspace_bytes": ([_P, ctypes.POINTER(sla_attn_opts), _I32], _SZ),
+    "sla_attention": ([_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(sla_attn_opts), _P, _SZ, _P], _I32),
+    "sla_attention_grad": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(sla_attn_opts),
+                            _P, _SZ, _P], _I32),
+    "sla_norm_workspace_bytes": ([_I32], _SZ),
+    "sla_global_norm": ([_I32, _P, _I32, _P, _I32, _P, _SZ, _P], _I32),
+    "sla_clip_norm": ([_I32, _P, _I32, _F64, _P, _I32, _P, _SZ, _P], _I32),
     "sla_debug_bounds_report": ([ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(_I32), ctypes.POINTER(_I64),
                                  _I32], _I32),
     "sla_last_error_string": ([], ctypes.c_char_p),
@@ -320,3 +341,61 @@ def sla_laplacian_grad(e, lam, x, dw, dshift, flags, ws, stream=None) -> None:
     _check("sla_laplacian_grad", lib().sla_laplacian_grad(
         e, _ptr(lam), _ptr(x), _ptr(dw), _ptr(dshift), int(flags), _ptr(ws),
         0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+TENSOR_DTYPES = {torch.float64: SLA_F64, torch.float32: SLA_F32, torch.bfloat16: SLA_BF16,
+                 torch.float16: SLA_F16}
+
+
+def sla_attention_prepare(h, backward=0, stream=None) -> None:
+    _check("sla_attention_prepare", lib().sla_attention_prepare(h, int(backward), _stream(stream)))
+
+
+def make_attn_opts(dtype, heads, kv_heads, dim, scale, q_stride, k_stride, v_stride,
+                   do_stride=(0, 0, 0)) -> sla_attn_opts:
+    st = ctypes.c_int64 * 3
+    return sla_attn_opts(TENSOR_DTYPES[dtype], int(heads), int(kv_heads), int(dim), float(scale),
+                         st(*q_stride), st(*k_stride), st(*v_stride), st(*do_stride))
+
+
+def sla_attention_workspace_bytes(h, opts, backward=0) -> int:
+    return int(lib().sla_attention_workspace_bytes(h, ctypes.byref(opts), int(backward)))
+
+
+def sla_attention(h, q, k, v, vals, out, out_wide, lse, opts, ws, stream=None) -> None:
+    """q, k and v with the strides of opts (their last dimension contiguous)."""
+    _check("sla_attention", lib().sla_attention(
+        h, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(vals), _ptr(out), _ptr(out_wide), _ptr(lse),
+        ctypes.byref(opts), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def sla_attention_grad(h, q, k, v, vals, out, lse, dout, dq, dk, dv, dvals, opts, ws, stream=None) -> None:
+    """q, k, v and dout with the strides of opts (their last dimension contiguous)."""
+    _check("sla_attention_grad", lib().sla_attention_grad(
+        h, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(vals), _ptr(out), _ptr(lse), dout.data_ptr(),
+        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dvals), ctypes.byref(opts), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def sla_norm_workspace_bytes(n) -> int:
+    return int(lib().sla_norm_workspace_bytes(n))
+
+
+def tensor_list(src, dst=None):
+    """Host array of sla_tensor (four 64-bit words each) for dense tensors, and its length."""
+    words = []
+    for a, b in zip(src, dst if dst is not None else src):
+        words += (a.data_ptr(), b.data_ptr(), a.numel(), TENSOR_DTYPES[a.dtype])
+    return (ctypes.c_int64 * max(len(words), 1))(*words), len(words) // 4
+
+
+def sla_global_norm(n, tensors, kind, norm, ws, stream=None) -> None:
+    _check("sla_global_norm", lib().sla_global_norm(
+        n, tensors, int(kind), _ptr(norm), TENSOR_DTYPES[norm.dtype], _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)))
+
+
+def sla_clip_norm(n, tensors, kind, max_norm, norm, ws, stream=None) -> None:
+    _check("sla_clip_norm", lib().sla_clip_norm(
+        n, tensors, int(kind), float(max_norm), _ptr(norm), TENSOR_DTYPES[norm.dtype], _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)))

@@ -159,6 +159,60 @@ class CSR:
         return _Solve.apply(self, values, b, opts)
 
 
+    # --------------------------------------------------------- attention
+    def prepare_attention(self, backward: bool = False) -> None:
+        """Build the work plan of ``attention`` (and, with ``backward``, A^T's
+        pattern and plan) now instead of at the first call: needed before the
+        calls are captured into a CUDA graph.  Synchronises the host."""
+        with torch.cuda.device(self.device):
+            L.sla_attention_prepare(self.handle, backward)
+
+    def attention(self, q, k, v, values=None, *, scale: float | None = None) -> torch.Tensor:
+        """Attention over the pattern: row i of A is a query that attends to the
+        columns stored in that row,
+
+            s_t = scale * q_i . k_j + values_t,  o_i = sum_t softmax(s)_t v_j,
+
+        differentiable in q, k, v and values.  q: [B, n_rows, H, D], k and v:
+        [B, n_cols, K, D] (without the leading dimension when B == 1), of one type
+        among float64, float32, bfloat16 and float16 (which need not be A's), D at
+        most 256, H a multiple of K (query head h reads key head h // (H // K)).
+        values [B, nnz] (A's dtype, shared by the heads) are added to the scores;
+        an entry whose value is -inf is left out, whatever its k and v hold.  A
+        row with no entry left gives zeros.  scale defaults to D ** -0.5.  The
+        last dimension is copied if it is not contiguous; other strides are used
+        as they are.  Returns o shaped like q.  Sums have a fixed order: equal
+        calls give equal bits.
+        """
+        q4, k4, v4 = self._heads(q, self.n_rows, "q"), self._heads(k, self.n_cols, "k"), \
+            self._heads(v, self.n_cols, "v")
+        if not (q4.dtype == k4.dtype == v4.dtype) or q4.dtype not in L.TENSOR_DTYPES:
+            raise TypeError("q, k and v must share one type: float64, float32, bfloat16 or float16")
+        if k4.shape != v4.shape or k4.shape[3] != q4.shape[3]:
+            raise ValueError(f"k {tuple(k4.shape)} and v {tuple(v4.shape)} must have one shape, with q's "
+                             f"last dimension ({q4.shape[3]})")
+        if k4.shape[2] == 0 or q4.shape[2] == 0 or q4.shape[2] % k4.shape[2]:
+            raise ValueError(f"q's {q4.shape[2]} heads are not a multiple of k's {k4.shape[2]}")
+        if not 1 <= q4.shape[3] <= 256:
+            raise ValueError(f"heads of {q4.shape[3]} elements (1 to 256)")
+        if values is not None:
+            self._values(values)
+        scale = q4.shape[3] ** -0.5 if scale is None else float(scale)
+        if not math.isfinite(scale):
+            raise ValueError("scale must be finite")
+        return _Attention.apply(self, q4, k4, v4, values, scale).reshape(q.shape)
+
+    def _heads(self, x, n, name):
+        want = (self.batch, n)
+        if x.dim() == 3 and self.batch == 1:
+            x = x.unsqueeze(0)
+        if x.dim() != 4 or tuple(x.shape[:2]) != want:
+            raise ValueError(f"{name} must be [{want[0]}, {want[1]}, heads, dim] (got {tuple(x.shape)})")
+        if x.device != self.device:
+            raise TypeError(f"{name} must be on {self.device}")
+        return x
+
+
 class CSRList(CSR):
     """Independent square systems with their own patterns (torch-sla's
     SparseTensorList, technical summary, "Methodology" 1), held as one
@@ -257,6 +311,49 @@ class _Solve(torch.autograd.Function):
         gv = A.grad_values(lam, x).reshape(values.shape) if ctx.needs_input_grad[1] else None
         gb = lam.reshape(gx.shape) if ctx.needs_input_grad[2] else None
         return None, gv, gb, None
+
+
+def _unit_stride(x: torch.Tensor) -> torch.Tensor:
+    return x if x.stride(-1) == 1 or x.numel() == 0 else x.contiguous()
+
+
+class _Attention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, A: CSR, q, k, v, values, scale):
+        q, k, v = _unit_stride(q), _unit_stride(k), _unit_stride(v)
+        B, n, H, D = q.shape
+        vals = None if values is None else A._values(values)
+        out = torch.empty(B, n, H, D, dtype=q.dtype, device=A.device)
+        lse = torch.empty(B, n, H, dtype=torch.float64 if q.dtype == torch.float64 else torch.float32,
+                          device=A.device)
+        train = any(ctx.needs_input_grad)
+        wide = torch.empty(B, n, H, D, dtype=torch.float32, device=A.device) \
+            if train and q.element_size() == 2 else None
+        with torch.cuda.device(A.device):
+            L.sla_attention_prepare(A.handle, train)
+            opts = L.make_attn_opts(q.dtype, H, k.shape[2], D, scale, q.stride()[:3], k.stride()[:3],
+                                    v.stride()[:3])
+            ws = _workspace(L.sla_attention_workspace_bytes(A.handle, opts, 0), A.device)
+            L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts, ws)
+        ctx.A, ctx.scale = A, scale
+        ctx.save_for_backward(q, k, v, values, out if wide is None else wide, lse)
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, go):
+        A = ctx.A
+        q, k, v, values, out, lse = ctx.saved_tensors
+        go = _unit_stride(go)
+        vals = None if values is None else A._values(values)
+        new = lambda need, t: torch.empty(t.shape, dtype=t.dtype, device=A.device) if need else None  # noqa: E731
+        dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[1:5], (q, k, v, values)))
+        with torch.cuda.device(A.device):
+            opts = L.make_attn_opts(q.dtype, q.shape[2], k.shape[2], q.shape[3], ctx.scale, q.stride()[:3],
+                                    k.stride()[:3], v.stride()[:3], go.stride()[:3])
+            ws = _workspace(L.sla_attention_workspace_bytes(A.handle, opts, 1), A.device)
+            L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals, opts, ws)
+        return None, dq, dk, dv, dvals, None
 
 
 class EdgeLaplacian:
@@ -482,3 +579,101 @@ class _Newton(torch.autograd.Function):
         it = iter(got)
         grads = [next(it) if need else None for need in needs]
         return (None, None, None, None, None, *grads)
+
+
+# ------------------------------------------------- norms of many tensors ----
+def _norm_kind(norm_type) -> int:
+    if norm_type == 2:
+        return L.SLA_NORM_L2
+    if norm_type == math.inf:
+        return L.SLA_NORM_MAX
+    raise ValueError(f"norm_type must be 2 or inf (got {norm_type})")
+
+
+def _one_device(tensors):
+    for t in tensors:
+        if t.device.type != "cuda" or t.device != tensors[0].device:
+            raise ValueError("the tensors must be on one CUDA device")
+        if t.dtype not in L.TENSOR_DTYPES:
+            raise TypeError(f"unsupported dtype {t.dtype} (float64, float32, bfloat16 or float16)")
+    return tensors[0].device
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """The elements fill one range of memory, in whatever order."""
+    return t.is_contiguous() or torch.ops.aten.is_non_overlapping_and_dense(t)
+
+
+def _norm_buffers(tensors, device):
+    wide = any(t.dtype == torch.float64 for t in tensors)
+    return (torch.empty((), dtype=torch.float64 if wide else torch.float32, device=device),
+            _workspace(L.sla_norm_workspace_bytes(len(tensors)), device))
+
+
+@torch.no_grad()
+def global_norm(tensors, norm_type: float = 2.0) -> torch.Tensor:
+    """The norm of all elements of all tensors: sqrt(sum x^2), or max |x| for
+    norm_type inf.  A 0-dim tensor, float64 if any tensor is, else float32;
+    squares are summed in 64 bits in a fixed order.  No host synchronisation.
+    """
+    tensors = list(tensors)
+    kind = _norm_kind(norm_type)
+    if not tensors:
+        return torch.zeros(())
+    device = _one_device(tensors)
+    src = [t if _dense(t) else t.contiguous() for t in tensors]
+    with torch.cuda.device(device):
+        norm, ws = _norm_buffers(tensors, device)
+        words, n = L.tensor_list(src)
+        L.sla_global_norm(n, words, kind, norm, ws)
+    return norm
+
+
+@torch.no_grad()
+def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out=None):
+    """(clipped, norm): every tensor times min(1, max_norm / (norm + 1e-6)), with
+    the norm of all of them together.  ``out``: the tensors to write (shapes and
+    types of the inputs; ``out=tensors`` clips in place), new ones by default.
+    The outputs may share memory with their own input only.  A NaN makes every
+    output NaN; an infinity makes the factor 0.  No host synchronisation.
+    """
+    tensors = list(tensors)
+    kind = _norm_kind(norm_type)
+    max_norm = float(max_norm)
+    if not (max_norm >= 0.0 and math.isfinite(max_norm)):
+        raise ValueError(f"max_norm must be finite and not negative (got {max_norm})")
+    if out is None:
+        outs = None
+    else:
+        outs = list(out)
+        if len(outs) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype or o.device != t.device
+                                            for o, t in zip(outs, tensors)):
+            raise ValueError("out must match the tensors in number, shapes, types and device")
+    if not tensors:
+        return [], torch.zeros(())
+    device = _one_device(tensors)
+    src = [t if _dense(t) else t.contiguous() for t in tensors]
+    if outs is None:
+        outs = [torch.empty_like(t) for t in src]
+        dst = outs
+    else:
+        # an output laid out otherwise than its input is written by way of a copy
+        dst = [o if o.stride() == s.stride() and _dense(o) else torch.empty_like(s) for o, s in zip(outs, src)]
+    with torch.cuda.device(device):
+        norm, ws = _norm_buffers(tensors, device)
+        words, n = L.tensor_list(src, dst)
+        L.sla_clip_norm(n, words, kind, max_norm, norm, ws)
+    for o, d in zip(outs, dst):
+        if o is not d:
+            o.copy_(d)
+    return outs, norm
+
+
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0) -> torch.Tensor:
+    """Clip the parameters' gradients in place to a global norm; returns the norm
+    before clipping.  Parameters without a gradient are skipped.  Two parameters
+    that share one gradient tensor are an error.  No host synchronisation."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    return clip_by_global_norm(grads, max_norm, norm_type=norm_type, out=grads)[1]

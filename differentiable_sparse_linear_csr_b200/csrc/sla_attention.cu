@@ -1,0 +1,862 @@
+// Attention over a CSR pattern: row i of the pattern is a query that attends to
+// the columns stored in that row, with the stored values (one per entry) added
+// to the scores.  The autograd companion of the matrix product on the same
+// handle: the forward gathers k and v by A's columns, the backward gathers by
+// A's rows and, for the keys' gradients, by A^T's (no atomics: every sum has a
+// fixed order).  Formulas: sla_attention.cuh.
+#include "sla_attention.cuh"
+
+#include <algorithm>
+#include <climits>
+#include <new>
+
+namespace sla {
+
+// ----------------------------------------------------------------- plan ----
+namespace {
+
+__global__ void unit_len_kernel(int n_rows, int rows, int n_units, const int32_t *__restrict__ rowptr,
+                                unsigned *len) {
+    const int u = blockIdx.x * blockDim.x + threadIdx.x;
+    if (u > n_units) return;
+    int m = 0;
+    if (u < n_units)
+        for (int64_t i = (int64_t)u * rows; i < min((int64_t)n_rows, ((int64_t)u + 1) * rows); ++i)
+            m = max(m, rowptr[i + 1] - rowptr[i]);
+    len[u] = (unsigned)m;
+}
+
+// Segments, slots (segments of split units) and split units of every unit.
+__global__ void unit_split_kernel(int n_units, int seg_len, const unsigned *__restrict__ len, unsigned *nseg,
+                                  unsigned *slots, unsigned *multi) {
+    const int u = blockIdx.x * blockDim.x + threadIdx.x;
+    if (u > n_units) return;
+    unsigned n = 0;
+    if (u < n_units) n = max(1u, (len[u] + seg_len - 1) / seg_len);
+    nseg[u] = n;
+    slots[u] = n > 1 ? n : 0;
+    multi[u] = n > 1 ? 1 : 0;
+}
+
+__global__ void unit_fill_kernel(int n_units, const unsigned *__restrict__ item0, const unsigned *__restrict__ slot0,
+                                 const unsigned *__restrict__ multi0, int32_t *item_unit, int32_t *item_seg,
+                                 int32_t *item_slot, int32_t *multi_unit, int32_t *multi_slot) {
+    const int u = blockIdx.x * blockDim.x + threadIdx.x;
+    if (u > n_units) return;
+    if (u == n_units) {
+        multi_slot[multi0[u]] = (int32_t)slot0[u];
+        return;
+    }
+    const unsigned i0 = item0[u], n = item0[u + 1] - i0;
+    for (unsigned k = 0; k < n; ++k) {
+        item_unit[i0 + k] = u;
+        item_seg[i0 + k] = (int32_t)k;
+        item_slot[i0 + k] = n > 1 ? (int32_t)(slot0[u] + k) : -1;
+    }
+    if (n > 1) {
+        multi_unit[multi0[u]] = u;
+        multi_slot[multi0[u]] = (int32_t)slot0[u];
+    }
+}
+
+void free_plan(AttnPlan *p) {
+    cudaFree(p->item_unit);
+    cudaFree(p->item_seg);
+    cudaFree(p->item_slot);
+    cudaFree(p->multi_unit);
+    cudaFree(p->multi_slot);
+    *p = AttnPlan();
+}
+
+struct DeviceScratch {
+    std::vector<void *> held;
+    ~DeviceScratch() {
+        for (void *p : held) cudaFree(p);
+    }
+    template <typename U>
+    U *get(size_t count) {
+        void *p = nullptr;
+        if (cudaMalloc(&p, std::max<size_t>(count, 1) * sizeof(U)) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        held.push_back(p);
+        return static_cast<U *>(p);
+    }
+};
+
+bool alloc_i32(int32_t **p, size_t count) {
+    if (cudaMalloc(p, std::max<size_t>(count, 1) * sizeof(int32_t)) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
+
+inline unsigned blocks_of(int64_t n, int t = 256) { return (unsigned)((n + t - 1) / t); }
+
+sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s) {
+    const int n = transposed ? h->n_cols : h->n_rows;
+    const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr;
+    p->rows = rows;
+    p->n_units = (n + rows - 1) / rows;
+    const int U = p->n_units;
+    if (U == 0) {
+        p->built = true;
+        return SLA_OK;
+    }
+    DeviceScratch tmp;
+    unsigned *len = tmp.get<unsigned>(U + 1), *sum = tmp.get<unsigned>(U + 1), *nseg = tmp.get<unsigned>(U + 1),
+             *slots = tmp.get<unsigned>(U + 1), *multi = tmp.get<unsigned>(U + 1);
+    void *ws = tmp.get<char>(scan_ws_bytes(U + 1));
+    if (!len || !sum || !nseg || !slots || !multi || !ws) {
+        set_error("attention plan: out of device memory");
+        return SLA_ERR_OOM;
+    }
+    unit_len_kernel<<<blocks_of(U + 1), 256, 0, s>>>(n, rows, U, rowptr, len);
+    SLA_CHECK_LAUNCH();
+    sla_status st = exclusive_scan(len, sum, U + 1, ws, s);
+    if (st != SLA_OK) return st;
+    unsigned total = 0;
+    SLA_CHECK_CUDA(cudaMemcpyAsync(&total, sum + U, sizeof total, cudaMemcpyDeviceToHost, s));
+    SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+    // Enough segments to fill the GPU when there are few units (8 an SM), none
+    // shorter than 64 entries: a shorter one spends more on its partial result
+    // than on its entries.
+    const int64_t want = ((int64_t)total + h->num_sms * 8 - 1) / ((int64_t)h->num_sms * 8);
+    p->seg_len = (int32_t)std::max<int64_t>(64, (want + 15) / 16 * 16);
+    unit_split_kernel<<<blocks_of(U + 1), 256, 0, s>>>(U, p->seg_len, len, nseg, slots, multi);
+    SLA_CHECK_LAUNCH();
+    unsigned *vec[3] = {nseg, slots, multi};
+    unsigned tot[3] = {0, 0, 0};
+    for (int i = 0; i < 3; ++i) {
+        st = exclusive_scan(vec[i], vec[i], U + 1, ws, s);
+        if (st != SLA_OK) return st;
+        SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[i], vec[i] + U, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
+    }
+    SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+    p->n_items = (int32_t)tot[0];
+    p->n_slots = (int32_t)tot[1];
+    p->n_multi = (int32_t)tot[2];
+    if (p->n_multi > 0) {
+        if (!alloc_i32(&p->item_unit, tot[0]) || !alloc_i32(&p->item_seg, tot[0]) ||
+            !alloc_i32(&p->item_slot, tot[0]) || !alloc_i32(&p->multi_unit, tot[2]) ||
+            !alloc_i32(&p->multi_slot, (size_t)tot[2] + 1)) {
+            set_error("attention plan: out of device memory");
+            return SLA_ERR_OOM;
+        }
+        unit_fill_kernel<<<blocks_of(U + 1), 256, 0, s>>>(U, nseg, slots, multi, p->item_unit, p->item_seg,
+                                                          p->item_slot, p->multi_unit, p->multi_slot);
+        SLA_CHECK_LAUNCH();
+    }
+    SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+    p->built = true;
+    return SLA_OK;
+}
+
+}  // namespace
+
+sla_status ensure_attn_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s) {
+    if (p->built) return SLA_OK;
+    const sla_status st = build_plan(h, p, rows, transposed, s);
+    if (st != SLA_OK) free_plan(p);
+    return st;
+}
+
+void free_attn_plans(Csr *h) {
+    if (!h->attn) return;
+    for (AttnPlan &p : h->attn->row) free_plan(&p);
+    delete h->attn;
+    h->attn = nullptr;
+}
+
+// ---------------------------------------------------------- row kernels ----
+// A group of L lanes takes one (system, item, head); lane l holds the elements
+// (i * L + l) * VEC + e of the head.  Neighbouring groups take neighbouring
+// heads, so a warp reads consecutive memory of a gathered row.  The entries of
+// the item are walked kStep at a time with their loads issued together.
+// Bound by the gathers: 2 * dim elements an entry and head.
+namespace {
+
+constexpr int kAttnThreads = 128;
+
+template <int L>
+__device__ __forceinline__ unsigned group_mask() {
+    if constexpr (L == 32) return 0xffffffffu;
+    else return ((1u << L) - 1u) << ((threadIdx.x & 31) & ~(L - 1));
+}
+
+template <int L, typename A>
+__device__ __forceinline__ A group_sum(A v, unsigned mask) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+    return v;
+}
+
+struct Item { int64_t b; int row, t0, t1, slot; };
+
+__device__ __forceinline__ Item load_item(const AttnArgs &a, int64_t b, int64_t it) {
+    Item r;
+    r.b = b;
+    r.row = a.item_unit ? __ldg(a.item_unit + it) : (int)it;
+    r.t0 = __ldg(a.rowptr + r.row);
+    r.t1 = __ldg(a.rowptr + r.row + 1);
+    r.slot = -1;
+    if (a.item_unit) {
+        const int64_t begin = (int64_t)r.t0 + (int64_t)__ldg(a.item_seg + it) * a.seg_len;
+        const int64_t end = begin + a.seg_len;
+        r.slot = __ldg(a.item_slot + it);
+        r.t0 = (int)begin;
+        r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);
+    }
+    return r;
+}
+
+// The vectors of one head this lane holds.
+template <typename T, int VEC, int L, int NV>
+struct Frag {
+    using A = typename AccOf<T>::type;
+    A x[NV][VEC];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[i][e] = (A)0;
+    }
+    template <typename I>
+    __device__ __forceinline__ void load(const I *p, int dim, int lane, bool on) {
+        zero();
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int d = (i * L + lane) * VEC;
+            if (on && d < dim) {
+                const Pack<I, VEC> r = load_pack<I, VEC>(p + d);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[i][e] = to_acc(r.e[e]);
+            }
+        }
+    }
+    __device__ __forceinline__ A dot(const Frag &y) const {
+        A s = (A)0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) s = fma(x[i][e], y.x[i][e], s);
+        return s;
+    }
+    __device__ __forceinline__ void axpy(A w, const Frag &y) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[i][e] = fma(w, y.x[i][e], x[i][e]);
+    }
+    __device__ __forceinline__ void scale(A w) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[i][e] *= w;
+    }
+    template <typename O>
+    __device__ __forceinline__ void store(O *p, int dim, int lane) const {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int d = (i * L + lane) * VEC;
+            if (d < dim) {
+                if constexpr (sizeof(O) * VEC == 32) {
+                    Pack<O, VEC> r;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) r.e[e] = from_acc<O>(x[i][e]);
+                    reinterpret_cast<uint4 *>(p + d)[0] = reinterpret_cast<uint4 *>(&r)[0];
+                    reinterpret_cast<uint4 *>(p + d)[1] = reinterpret_cast<uint4 *>(&r)[1];
+                } else if constexpr (sizeof(O) * VEC == 16) {
+                    Pack<O, VEC> r;
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) r.e[e] = from_acc<O>(x[i][e]);
+                    *reinterpret_cast<uint4 *>(p + d) = *reinterpret_cast<uint4 *>(&r);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) p[d + e] = from_acc<O>(x[i][e]);
+                }
+            }
+        }
+    }
+};
+
+template <typename T, int VEC, int L, int NV>
+__global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const AttnArgs a) {
+    using A = typename AccOf<T>::type;
+    using F = Frag<T, VEC, L, NV>;
+    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
+    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
+    const int lane = threadIdx.x & (L - 1);
+    const unsigned mask = group_mask<L>();
+    if (g >= (int64_t)a.batch * a.n_items * a.heads) return;
+    const int h = (int)(g % a.heads);
+    const Item it = load_item(a, g / a.heads / a.n_items, g / a.heads % a.n_items);
+    const int kh = h / (a.heads / a.kv_heads);
+    F q, acc;
+    q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane, true);
+    acc.zero();
+    const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
+    const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
+    const A scale = (A)a.scale, none = neg_inf<A>();
+    A m = none, l = (A)0;
+    for (int t = it.t0; t < it.t1; t += kStep) {
+        F kf[kStep], vf[kStep];
+        A s[kStep];
+        bool on[kStep];
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            on[u] = t + u < it.t1;
+            A w = (A)0;
+            int64_t c = 0;
+            if (on[u]) {
+                c = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_cols, kBndColumn);
+                w = load_value<A>(a.vals, a.vals_f64, it.b * a.nnz + t + u);
+                on[u] = w != none;     // a value of -inf leaves the entry out
+            }
+            s[u] = w;
+            kf[u].load(kb + c * a.ks[1], a.dim, lane, on[u]);
+            vf[u].load(vb + c * a.vs[1], a.dim, lane, on[u]);
+        }
+        A top = m;
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            const A d = group_sum<L>(q.dot(kf[u]), mask);
+            s[u] = on[u] ? fma(d, scale, s[u]) : none;
+            top = fmax(top, s[u]);
+        }
+        const A ref = top == none ? (A)0 : top;
+        const A fix = exp_acc(m - ref);
+        acc.scale(fix);
+        l *= fix;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            const A p = exp_acc(s[u] - ref);
+            l += p;
+            acc.axpy(p, vf[u]);
+        }
+    }
+    if (it.slot < 0) {
+        const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
+        acc.scale(l > (A)0 || l != l ? (A)1 / l : (A)0);   // no entry left: zeros
+        acc.store(static_cast<T *>(a.out) + at * a.dim, a.dim, lane);
+        if (a.wide) acc.store(static_cast<A *>(a.wide) + at * a.dim, a.dim, lane);
+        if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+    } else {
+        A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * (a.dim + 2);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int d = (i * L + lane) * VEC + e;
+                if (d < a.dim) p[d] = acc.x[i][e];
+            }
+        if (lane == 0) {
+            p[a.dim] = m;
+            p[a.dim + 1] = l;
+        }
+    }
+}
+
+// Joins the segments of split rows: one warp a (system, split unit, row, head).
+template <typename T>
+__global__ void __launch_bounds__(kAttnThreads)
+attn_join_kernel(const AttnArgs a, int rows, int n_multi, const int32_t *__restrict__ multi_unit,
+                 const int32_t *__restrict__ multi_slot) {
+    using A = typename AccOf<T>::type;
+    const int64_t w = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (w >= (int64_t)a.batch * n_multi * rows * a.heads) return;
+    const int h = (int)(w % a.heads), r = (int)(w / a.heads % rows);
+    const int mu = (int)(w / a.heads / rows % n_multi);
+    const int b = (int)(w / a.heads / rows / n_multi);
+    const int64_t row = (int64_t)__ldg(multi_unit + mu) * rows + r;
+    if (row >= a.n_rows) return;
+    const int s0 = __ldg(multi_slot + mu), n = __ldg(multi_slot + mu + 1) - s0;
+    const int64_t step = (int64_t)rows * a.heads * (a.dim + 2);
+    const A *p = static_cast<const A *>(a.part) + part_index(s0, a.n_slots, b, rows, r, a.heads, h) * (a.dim + 2);
+    const A none = neg_inf<A>();
+    A m = none;
+    for (int s = lane; s < n; s += 32) m = fmax(m, p[s * step + a.dim]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const A ref = m == none ? (A)0 : m;
+    A l = (A)0;
+    for (int s = lane; s < n; s += 32) l += p[s * step + a.dim + 1] * exp_acc(p[s * step + a.dim] - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const A inv = l > (A)0 || l != l ? (A)1 / l : (A)0;
+    const int64_t at = ((int64_t)b * a.n_rows + row) * a.heads + h;
+    for (int d = lane; d < a.dim; d += 32) {
+        A x = (A)0;
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) x += p[s * step + d] * exp_acc(p[s * step + a.dim] - ref);
+        static_cast<T *>(a.out)[at * a.dim + d] = from_acc<T>(x * inv);
+        if (a.wide) static_cast<A *>(a.wide)[at * a.dim + d] = x * inv;
+    }
+    if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+}
+
+// Gradients by A's rows: p and ds of every entry and head, and dq.
+template <typename T, int VEC, int L, int NV>
+__global__ void __launch_bounds__(kAttnThreads) attn_bwd_rows_kernel(const AttnArgs a) {
+    using A = typename AccOf<T>::type;
+    using F = Frag<T, VEC, L, NV>;
+    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
+    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
+    const int lane = threadIdx.x & (L - 1);
+    const unsigned mask = group_mask<L>();
+    if (g >= (int64_t)a.batch * a.n_items * a.heads) return;
+    const int h = (int)(g % a.heads);
+    const Item it = load_item(a, g / a.heads / a.n_items, g / a.heads % a.n_items);
+    const int kh = h / (a.heads / a.kv_heads);
+    const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
+    F q, go, acc;
+    q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane, true);
+    go.load(static_cast<const T *>(a.dout) + it.b * a.ds[0] + it.row * a.ds[1] + h * a.ds[2], a.dim, lane, true);
+    acc.load(static_cast<const A *>(a.o) + at * a.dim, a.dim, lane, true);
+    const A delta = group_sum<L>(go.dot(acc), mask);
+    const A lse = static_cast<const A *>(a.lse)[at];
+    acc.zero();
+    const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
+    const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
+    const A scale = (A)a.scale, none = neg_inf<A>();
+    A *pds = static_cast<A *>(a.pds);
+    for (int t = it.t0; t < it.t1; t += kStep) {
+        F kf[kStep], vf[kStep];
+        A s[kStep];
+        bool on[kStep];
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            on[u] = t + u < it.t1;
+            A w = (A)0;
+            int64_t c = 0;
+            if (on[u]) {
+                c = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_cols, kBndColumn);
+                w = load_value<A>(a.vals, a.vals_f64, it.b * a.nnz + t + u);
+                on[u] = w != none && lse != none;
+            }
+            s[u] = w;
+            kf[u].load(kb + c * a.ks[1], a.dim, lane, on[u]);
+            vf[u].load(vb + c * a.vs[1], a.dim, lane, on[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+            const A d = group_sum<L>(q.dot(kf[u]), mask);
+            const A dp = group_sum<L>(go.dot(vf[u]), mask);
+            const A p = on[u] ? exp_acc(fma(d, scale, s[u]) - lse) : (A)0;
+            const A ds = on[u] ? p * (dp - delta) : (A)0;
+            acc.axpy(ds, kf[u]);
+            if (pds && lane == 0 && t + u < it.t1) {
+                A *e = pds + ((it.b * a.nnz + t + u) * a.heads + h) * 2;
+                e[0] = p;
+                e[1] = ds;
+            }
+        }
+    }
+    acc.scale(scale);
+    if (!a.dq) return;
+    if (it.slot < 0) {
+        acc.store(static_cast<T *>(a.dq) + at * a.dim, a.dim, lane);
+    } else {
+        A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * a.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int d = (i * L + lane) * VEC + e;
+                if (d < a.dim) p[d] = acc.x[i][e];
+            }
+    }
+}
+
+// Gradients by A^T's rows, from the stored p and ds: dk and dv.  Partial sums
+// of a split row: dk then dv.
+template <typename T, int VEC, int L, int NV>
+__global__ void __launch_bounds__(kAttnThreads) attn_bwd_cols_kernel(const AttnArgs a) {
+    using A = typename AccOf<T>::type;
+    using F = Frag<T, VEC, L, NV>;
+    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
+    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
+    const int lane = threadIdx.x & (L - 1);
+    if (g >= (int64_t)a.batch * a.n_items * a.kv_heads) return;
+    const int kh = (int)(g % a.kv_heads), share = a.heads / a.kv_heads;
+    const Item it = load_item(a, g / a.kv_heads / a.n_items, g / a.kv_heads % a.n_items);
+    F dk, dv;
+    dk.zero();
+    dv.zero();
+    const A *pds = static_cast<const A *>(a.pds);
+    for (int h = kh * share; h < (kh + 1) * share; ++h) {
+        const T *qb = static_cast<const T *>(a.q) + it.b * a.qs[0] + h * a.qs[2];
+        const T *gb = static_cast<const T *>(a.dout) + it.b * a.ds[0] + h * a.ds[2];
+        for (int t = it.t0; t < it.t1; t += kStep) {
+            F qf[kStep], gf[kStep];
+            A p[kStep], ds[kStep];
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                int64_t i = 0;
+                p[u] = ds[u] = (A)0;
+                if (t + u < it.t1) {
+                    i = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_rows, kBndColumn);
+                    const int64_t e = SLA_IDX((int64_t)__ldg(a.perm + t + u), a.nnz, kBndEntry);
+                    const A *x = pds + ((it.b * a.nnz + e) * a.heads + h) * 2;
+                    p[u] = x[0];
+                    ds[u] = x[1];
+                }
+                const bool on = p[u] != (A)0;      // an entry that was left out has no part
+                qf[u].load(qb + i * a.qs[1], a.dim, lane, on);
+                gf[u].load(gb + i * a.ds[1], a.dim, lane, on);
+            }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u) {
+                dk.axpy(ds[u], qf[u]);
+                dv.axpy(p[u], gf[u]);
+            }
+        }
+    }
+    dk.scale((A)a.scale);
+    if (it.slot < 0) {
+        const int64_t at = ((it.b * a.n_cols + it.row) * a.kv_heads + kh) * a.dim;
+        if (a.dk) dk.store(static_cast<T *>(a.dk) + at, a.dim, lane);
+        if (a.dv) dv.store(static_cast<T *>(a.dv) + at, a.dim, lane);
+    } else {
+        A *p = static_cast<A *>(a.part) +
+               part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.kv_heads, kh) * 2 * a.dim;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int d = (i * L + lane) * VEC + e;
+                if (d < a.dim) {
+                    p[d] = dk.x[i][e];
+                    p[a.dim + d] = dv.x[i][e];
+                }
+            }
+    }
+}
+
+// out0 (and out1) of split rows: the segments' sums added in order, `width`
+// elements a partial, the first `dim` for out0, the next for out1.
+template <typename T>
+__global__ void __launch_bounds__(kAttnThreads)
+attn_join_sums_kernel(const typename AccOf<T>::type *__restrict__ part, int n_rows, int batch, int n_slots, int rows,
+                      int heads, int dim, int width, int n_multi, const int32_t *__restrict__ multi_unit,
+                      const int32_t *__restrict__ multi_slot, T *out0, T *out1) {
+    using A = typename AccOf<T>::type;
+    const int64_t w = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (w >= (int64_t)batch * n_multi * rows * heads) return;
+    const int h = (int)(w % heads), r = (int)(w / heads % rows);
+    const int mu = (int)(w / heads / rows % n_multi);
+    const int b = (int)(w / heads / rows / n_multi);
+    const int64_t row = (int64_t)__ldg(multi_unit + mu) * rows + r;
+    if (row >= n_rows) return;
+    const int s0 = __ldg(multi_slot + mu), n = __ldg(multi_slot + mu + 1) - s0;
+    const int64_t step = (int64_t)rows * heads * width;
+    const A *p = part + part_index(s0, n_slots, b, rows, r, heads, h) * width;
+    const int64_t at = (((int64_t)b * n_rows + row) * heads + h) * dim;
+    for (int d = lane; d < width; d += 32) {
+        A x = (A)0;
+#pragma unroll 4
+        for (int s = 0; s < n; ++s) x += p[s * step + d];
+        T *out = d < dim ? out0 : out1;
+        if (out) out[at + (d < dim ? d : d - dim)] = from_acc<T>(x);
+    }
+}
+
+// dvals_t = sum over the heads of ds_t, in the values' type.
+template <typename A, typename V>
+__global__ void __launch_bounds__(256)
+attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__restrict__ dvals) {
+    const int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (t >= count) return;
+    A x = (A)0;
+    for (int h = 0; h < heads; ++h) x += pds[(t * heads + h) * 2 + 1];
+    dvals[t] = (V)x;
+}
+
+// -------------------------------------------------------------- launches ----
+enum { kFwd, kBwdRows, kBwdCols };
+
+template <typename T, int VEC, int L, int NV>
+sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
+    const int64_t groups = (int64_t)a.batch * a.n_items * (what == kBwdCols ? a.kv_heads : a.heads);
+    const int64_t blocks = (groups * L + kAttnThreads - 1) / kAttnThreads;
+    SLA_REQUIRE(blocks < INT_MAX, "sla_attention: too many rows, systems and heads");
+    if (blocks == 0) return SLA_OK;
+    if (what == kFwd) attn_fwd_rows_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
+    else if (what == kBwdRows) attn_bwd_rows_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
+    else attn_bwd_cols_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
+// Lanes and vectors a lane by the head's width: the fewest lanes (fewest
+// shuffles a score) that keep at most 2 vectors a lane.
+template <typename T>
+sla_status launch_rows_of(int what, const AttnArgs &a, bool vec, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (vec) {
+        const int n = a.dim / V;
+        if (n <= 4) return launch_rows<T, V, 4, 1>(what, a, s);
+        if (n <= 8) return launch_rows<T, V, 4, 2>(what, a, s);
+        if (n <= 16) return launch_rows<T, V, 8, 2>(what, a, s);
+        if (n <= 32) return launch_rows<T, V, 16, 2>(what, a, s);
+        if (n <= 64) return launch_rows<T, V, 32, 2>(what, a, s);
+        return launch_rows<T, V, 32, 4>(what, a, s);
+    }
+    if (a.dim <= 64) return launch_rows<T, 1, 32, 2>(what, a, s);
+    return launch_rows<T, 1, 32, 8>(what, a, s);
+}
+
+bool on_16_bytes(const void *p, const int64_t st[3], size_t size) {
+    if ((uintptr_t)p & 15) return false;
+    for (int i = 0; i < 3; ++i)
+        if ((st[i] * (int64_t)size) & 15) return false;
+    return true;
+}
+
+template <typename T>
+sla_status join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int heads, int width, void *out0, void *out1,
+                     cudaStream_t s) {
+    if (p.n_multi == 0) return SLA_OK;
+    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * heads;
+    attn_join_sums_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(
+        static_cast<const typename AccOf<T>::type *>(a.part), n_rows, a.batch, p.n_slots, p.rows, heads, a.dim, width,
+        p.n_multi, p.multi_unit, p.multi_slot, static_cast<T *>(out0), static_cast<T *>(out1));
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
+void use_plan(AttnArgs &a, const AttnPlan &p) {
+    a.n_units = p.n_units;
+    a.n_items = p.n_items;
+    a.n_slots = p.n_slots;
+    a.seg_len = p.seg_len;
+    a.item_unit = p.item_unit;
+    a.item_seg = p.item_seg;
+    a.item_slot = p.item_slot;
+}
+
+size_t acc_size(int32_t dt) { return dt == SLA_F64 ? 8 : 4; }
+
+template <typename T>
+sla_status attn_forward(const Csr *h, AttnArgs a, cudaStream_t s) {
+    const AttnPlan &p = h->attn->row[0];
+    use_plan(a, p);
+    a.rowptr = h->rowptr;
+    a.colind = h->colind;
+    const int V = 16 / sizeof(T);
+    const bool vec = a.dim % V == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) && on_16_bytes(a.k, a.ks, sizeof(T)) &&
+                     on_16_bytes(a.v, a.vs, sizeof(T)) && (((uintptr_t)a.out | (uintptr_t)a.wide) & 15) == 0;
+    sla_status st = launch_rows_of<T>(kFwd, a, vec, s);
+    if (st != SLA_OK || p.n_multi == 0) return st;
+    const int64_t warps = (int64_t)a.batch * p.n_multi * a.heads;
+    attn_join_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(a, 1, p.n_multi, p.multi_unit,
+                                                                                    p.multi_slot);
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
+template <typename T>
+sla_status attn_backward(const Csr *h, AttnArgs a, cudaStream_t s) {
+    using A = typename AccOf<T>::type;
+    const AttnPlan &p = h->attn->row[0];
+    const int V = 16 / sizeof(T);
+    const int64_t dense[3] = {(int64_t)a.dim, (int64_t)a.dim, (int64_t)a.dim};
+    const bool vec = a.dim % V == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) && on_16_bytes(a.k, a.ks, sizeof(T)) &&
+                     on_16_bytes(a.v, a.vs, sizeof(T)) && on_16_bytes(a.dout, a.ds, sizeof(T)) &&
+                     on_16_bytes(a.o, dense, sizeof(A)) && on_16_bytes(a.dq, dense, sizeof(T)) &&
+                     on_16_bytes(a.dk, dense, sizeof(T)) && on_16_bytes(a.dv, dense, sizeof(T));
+    use_plan(a, p);
+    a.rowptr = h->rowptr;
+    a.colind = h->colind;
+    sla_status st = launch_rows_of<T>(kBwdRows, a, vec, s);
+    if (st != SLA_OK) return st;
+    if (a.dq && (st = join_sums<T>(a, p, a.n_rows, a.heads, a.dim, a.dq, nullptr, s)) != SLA_OK) return st;
+    const int64_t entries = (int64_t)a.batch * a.nnz;
+    if (a.dvals && entries > 0) {
+        if (a.vals_f64)
+            attn_dvals_kernel<A, double><<<blocks_of(entries), 256, 0, s>>>(
+                entries, a.heads, static_cast<const A *>(a.pds), static_cast<double *>(a.dvals));
+        else
+            attn_dvals_kernel<A, float><<<blocks_of(entries), 256, 0, s>>>(
+                entries, a.heads, static_cast<const A *>(a.pds), static_cast<float *>(a.dvals));
+        SLA_CHECK_LAUNCH();
+    }
+    if (!a.dk && !a.dv) return SLA_OK;
+    const AttnPlan &pt = h->attn->row[1];
+    use_plan(a, pt);
+    a.rowptr = h->rowptrT;
+    a.colind = h->colindT;
+    a.perm = h->permT;
+    st = launch_rows_of<T>(kBwdCols, a, vec, s);
+    if (st != SLA_OK) return st;
+    return join_sums<T>(a, pt, a.n_cols, a.kv_heads, 2 * a.dim, a.dk, a.dv, s);
+}
+
+// Workspace: (p, ds) of every entry and head (backward), then the partial sums.
+size_t attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
+    const size_t acc = acc_size(o->dtype), B = (size_t)h->batch;
+    const AttnPlan &p = h->attn->row[0], &pt = h->attn->row[1];
+    if (!backward) return align_up(B * p.n_slots * o->heads * (size_t)(o->dim + 2) * acc);
+    const size_t rows = B * p.n_slots * o->heads * (size_t)o->dim * acc;
+    const size_t cols = B * pt.n_slots * o->kv_heads * 2 * (size_t)o->dim * acc;
+    return align_up(B * (size_t)h->nnz * o->heads * 2 * acc) + align_up(std::max(rows, cols));
+}
+
+sla_status check_opts(const char *fn, const Csr *h, const sla_attn_opts *o) {
+    SLA_REQUIRE(h != nullptr, "%s: NULL handle", fn);
+    SLA_REQUIRE(o != nullptr, "%s: NULL options", fn);
+    SLA_REQUIRE(o->dtype >= SLA_F64 && o->dtype <= SLA_F16, "%s: bad dtype %d", fn, o->dtype);
+    SLA_REQUIRE(o->heads >= 1 && o->kv_heads >= 1 && o->heads % o->kv_heads == 0 && o->heads <= 65536,
+                "%s: heads must be a positive multiple of kv_heads (%d, %d)", fn, o->heads, o->kv_heads);
+    SLA_REQUIRE(o->dim >= 1 && o->dim <= 256, "%s: dim must be in [1, 256] (got %d)", fn, o->dim);
+    SLA_REQUIRE(o->scale == o->scale && o->scale <= DBL_MAX && o->scale >= -DBL_MAX, "%s: scale is not finite", fn);
+    int dev = -1;
+    SLA_CHECK_CUDA(cudaGetDevice(&dev));
+    SLA_REQUIRE(dev == h->device, "%s: the handle lives on device %d, the current device is %d", fn, h->device, dev);
+    return SLA_OK;
+}
+
+sla_status prepare(Csr *h, bool backward, cudaStream_t s) {
+    const bool ready = h->attn && h->attn->row[0].built && (!backward || (h->has_transpose && h->attn->row[1].built));
+    if (ready) return SLA_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
+        cudaGetLastError();
+        set_error("sla_attention: the plan is built on first use, which a stream capture cannot hold; call "
+                  "sla_attention_prepare before capturing");
+        return SLA_ERR_UNSUPPORTED;
+    }
+    if (!h->attn) {
+        h->attn = new (std::nothrow) AttnPlans();
+        if (!h->attn) {
+            set_error("sla_attention_prepare: out of memory");
+            return SLA_ERR_OOM;
+        }
+    }
+    sla_status st = ensure_attn_plan(h, &h->attn->row[0], 1, false, s);
+    if (st != SLA_OK || !backward) return st;
+    st = ensure_transpose(h, s);
+    if (st == SLA_OK) st = ensure_attn_plan(h, &h->attn->row[1], 1, true, s);
+    return st;
+}
+
+AttnArgs make_args(const Csr *h, const sla_attn_opts *o, const void *q, const void *k, const void *v,
+                   const void *vals) {
+    AttnArgs a{};
+    a.n_rows = h->n_rows;
+    a.n_cols = h->n_cols;
+    a.batch = h->batch;
+    a.nnz = h->nnz;
+    a.heads = o->heads;
+    a.kv_heads = o->kv_heads;
+    a.dim = o->dim;
+    a.scale = o->scale;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.vals = vals;
+    a.vals_f64 = h->dtype == SLA_F64;
+    for (int i = 0; i < 3; ++i) {
+        a.qs[i] = o->q_stride[i];
+        a.ks[i] = o->k_stride[i];
+        a.vs[i] = o->v_stride[i];
+        a.ds[i] = o->do_stride[i];
+    }
+    return a;
+}
+
+}  // namespace
+}  // namespace sla
+
+using namespace sla;
+
+extern "C" sla_status sla_attention_prepare(sla_csr_t hh, int32_t backward, void *stream) {
+    SLA_RANGE("sla_attention_prepare");
+    clear_error();
+    Csr *h = reinterpret_cast<Csr *>(hh);
+    SLA_REQUIRE(h != nullptr, "sla_attention_prepare: NULL handle");
+    int dev = -1;
+    SLA_CHECK_CUDA(cudaGetDevice(&dev));
+    SLA_REQUIRE(dev == h->device, "sla_attention_prepare: the handle lives on device %d, the current device is %d",
+                h->device, dev);
+    return prepare(h, backward != 0, as_stream(stream));
+}
+
+extern "C" size_t sla_attention_workspace_bytes(sla_csr_t hh, const sla_attn_opts *o, int32_t backward) {
+    const Csr *h = reinterpret_cast<const Csr *>(hh);
+    if (!h || !o || !h->attn || !h->attn->row[0].built || (backward && !h->attn->row[1].built)) return 0;
+    if (o->dtype < SLA_F64 || o->dtype > SLA_F16 || o->heads < 1 || o->kv_heads < 1 || o->dim < 1) return 0;
+    return attn_ws(h, o, backward != 0);
+}
+
+extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, const void *v, const void *vals,
+                                    void *out, void *out_wide, void *lse, const sla_attn_opts *o, void *ws,
+                                    size_t ws_bytes, void *stream) {
+    SLA_RANGE("sla_attention");
+    clear_error();
+    Csr *h = reinterpret_cast<Csr *>(hh);
+    sla_status st = check_opts("sla_attention", h, o);
+    if (st != SLA_OK) return st;
+    if (h->n_rows == 0) return SLA_OK;
+    SLA_REQUIRE(q && out && lse && (h->n_cols == 0 || (k && v)), "sla_attention: NULL pointer");
+    cudaStream_t s = as_stream(stream);
+    st = prepare(h, false, s);
+    if (st != SLA_OK) return st;
+    const size_t need = attn_ws(h, o, false);
+    SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention: workspace too small (%zu < %zu)", ws_bytes, need);
+    SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention: workspace must be 256-byte aligned");
+    AttnArgs a = make_args(h, o, q, k, v, vals);
+    a.out = out;
+    a.wide = o->dtype == SLA_BF16 || o->dtype == SLA_F16 ? out_wide : nullptr;
+    a.lse = lse;
+    a.part = ws;
+    switch (o->dtype) {
+        case SLA_F64: return attn_forward<double>(h, a, s);
+        case SLA_F32: return attn_forward<float>(h, a, s);
+        case SLA_BF16: return attn_forward<__nv_bfloat16>(h, a, s);
+        default: return attn_forward<__half>(h, a, s);
+    }
+}
+
+extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void *k, const void *v, const void *vals,
+                                         const void *out, const void *lse, const void *dout, void *dq, void *dk,
+                                         void *dv, void *dvals, const sla_attn_opts *o, void *ws, size_t ws_bytes,
+                                         void *stream) {
+    SLA_RANGE("sla_attention_grad");
+    clear_error();
+    Csr *h = reinterpret_cast<Csr *>(hh);
+    sla_status st = check_opts("sla_attention_grad", h, o);
+    if (st != SLA_OK) return st;
+    SLA_REQUIRE(!dvals || vals, "sla_attention_grad: dvals without vals");
+    SLA_REQUIRE(h->n_rows == 0 || (q && out && lse && dout), "sla_attention_grad: NULL pointer");
+    SLA_REQUIRE(h->n_cols == 0 || (k && v), "sla_attention_grad: NULL pointer");
+    cudaStream_t s = as_stream(stream);
+    if (!dq && !dk && !dv && !dvals) return SLA_OK;
+    st = prepare(h, true, s);
+    if (st != SLA_OK) return st;
+    const size_t need = attn_ws(h, o, true);
+    SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention_grad: workspace too small (%zu < %zu)", ws_bytes,
+                need);
+    SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention_grad: workspace must be 256-byte aligned");
+    AttnArgs a = make_args(h, o, q, k, v, vals);
+    a.o = out;
+    a.lse = const_cast<void *>(lse);
+    a.dout = dout;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    a.dvals = dvals;
+    Carver c(ws);
+    a.pds = c.take<char>((size_t)h->batch * h->nnz * o->heads * 2 * acc_size(o->dtype));
+    if (!dk && !dv && !dvals) a.pds = nullptr;
+    a.part = c.base ? c.base + c.off : nullptr;
+    switch (o->dtype) {
+        case SLA_F64: return attn_backward<double>(h, a, s);
+        case SLA_F32: return attn_backward<float>(h, a, s);
+        case SLA_BF16: return attn_backward<__nv_bfloat16>(h, a, s);
+        default: return attn_backward<__half>(h, a, s);
+    }
+}

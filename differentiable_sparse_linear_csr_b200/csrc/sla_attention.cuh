@@ -1,0 +1,121 @@
+// Internals shared by the attention kernels: parameters, the plan that splits a
+// pattern's rows into work items, element loads and the partial results of
+// split rows.
+//
+//   s_t = scale * q_i . k_j + vals_t      for entry t = (i, j) of row i
+//   p_t = exp(s_t - lse_i),  lse_i = log sum_t exp(s_t),  o_i = sum_t p_t v_j
+// and backwards, with D_i = do_i . o_i:
+//   ds_t = p_t (do_i . v_j - D_i),  dq_i = scale sum_t ds_t k_j,
+//   dk_j = scale sum_t ds_t q_i,    dv_j = sum_t p_t do_i,  dvals_t = sum_heads ds_t.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cfloat>
+#include <vector>
+
+#include "sla_common.cuh"
+
+namespace sla {
+
+// Work items of one direction of a pattern: a unit is `rows` consecutive rows;
+// a unit whose longest row has more than seg_len entries is split into several
+// items (segments), whose partial results a second kernel joins.  Null item
+// arrays: item == unit, one segment each.
+struct AttnPlan {
+    bool built = false;
+    int32_t rows = 1, n_units = 0, n_items = 0, n_slots = 0, n_multi = 0, seg_len = 0;
+    int32_t *item_unit = nullptr, *item_seg = nullptr, *item_slot = nullptr;   // [n_items]
+    int32_t *multi_unit = nullptr;                                             // [n_multi]
+    int32_t *multi_slot = nullptr;                                             // [n_multi + 1]
+};
+
+struct AttnPlans {
+    AttnPlan row[2];                 // one row a unit: A, A^T
+};
+
+// What every kernel gets (strides in elements, heads of `dim` consecutive elements).
+struct AttnArgs {
+    int32_t n_rows, n_cols, batch, heads, kv_heads, dim;
+    int64_t nnz;
+    double scale;
+    const int32_t *rowptr, *colind, *perm;
+    int32_t n_units, n_items, n_slots, seg_len;
+    const int32_t *item_unit, *item_seg, *item_slot;
+    const void *q, *k, *v, *o, *dout;
+    int64_t qs[3], ks[3], vs[3], ds[3];    // system, row, head
+    const void *vals;
+    int32_t vals_f64;
+    void *out, *wide, *lse;                // forward (wide: out before its rounding, or null)
+    void *dq, *dk, *dv, *dvals;            // backward
+    void *pds;                             // [B][nnz][heads] pairs (p, ds)
+    void *part;                            // partial sums of split rows
+};
+
+// Accumulator type of a storage type: 32 bits for 16- and 32-bit types.
+template <typename T> struct AccOf { using type = float; };
+template <> struct AccOf<double> { using type = double; };
+
+__device__ __forceinline__ double to_acc(double x) { return x; }
+__device__ __forceinline__ float to_acc(float x) { return x; }
+__device__ __forceinline__ float to_acc(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_acc(__half x) { return __half2float(x); }
+template <typename T, typename A> __device__ __forceinline__ T from_acc(A x) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(x);
+    else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
+    else return (T)x;
+}
+
+// N consecutive elements, by 16-byte loads when they fill one or two.
+template <typename T, int N> struct alignas(sizeof(T) * N) Pack { T e[N]; };
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_pack(const T *p) {
+    Pack<T, N> r;
+    if constexpr (sizeof(T) * N == 16) {
+        *reinterpret_cast<uint4 *>(&r) = __ldg(reinterpret_cast<const uint4 *>(p));
+    } else if constexpr (sizeof(T) * N == 32) {
+        reinterpret_cast<uint4 *>(&r)[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        reinterpret_cast<uint4 *>(&r)[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.e[i] = p[i];
+    }
+    return r;
+}
+
+__device__ __forceinline__ float exp_acc(float x) { return exp2f(x * 1.4426950408889634f); }
+__device__ __forceinline__ double exp_acc(double x) { return exp(x); }
+__device__ __forceinline__ float log_acc(float x) { return logf(x); }
+__device__ __forceinline__ double log_acc(double x) { return log(x); }
+template <typename A> __device__ __forceinline__ A neg_inf();
+template <> __device__ __forceinline__ float neg_inf<float>() { return __int_as_float(0xff800000); }
+template <> __device__ __forceinline__ double neg_inf<double>() { return __longlong_as_double(0xfff0000000000000ll); }
+
+// A stored value as a score term.  A finite 64-bit value beyond the 32-bit
+// range stays finite, so that only -inf removes an entry.
+template <typename A>
+__device__ __forceinline__ A load_value(const void *vals, int f64, int64_t t) {
+    if (!vals) return (A)0;
+    if (!f64) return (A)__ldg(static_cast<const float *>(vals) + t);
+    const double x = __ldg(static_cast<const double *>(vals) + t);
+    if constexpr (sizeof(A) == 8) {
+        return x;
+    } else {
+        if (isinf(x)) return (float)x;
+        return x > FLT_MAX ? FLT_MAX : (x < -FLT_MAX ? -FLT_MAX : (float)x);
+    }
+}
+
+// Partial result of one segment: `dim` sums, then the running maximum and sum.
+// Rows of a unit and heads are the fastest indices.
+__host__ __device__ __forceinline__ int64_t part_index(int64_t slot, int32_t n_slots, int b, int rows, int r,
+                                                       int heads, int h) {
+    return (((int64_t)b * n_slots + slot) * rows + r) * heads + h;
+}
+
+sla_status ensure_attn_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s);
+void free_attn_plans(Csr *h);
+
+}  // namespace sla

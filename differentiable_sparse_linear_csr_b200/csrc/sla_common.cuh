@@ -82,6 +82,7 @@ constexpr int kRowBlock = 256;
 constexpr int kCgThreads = 512;
 
 // ---------------------------------------------------------------- handle ----
+struct AttnPlans;                      // sla_attention.cuh
 struct Csr {
     int32_t n_rows = 0, n_cols = 0;
     int64_t nnz = 0;
@@ -143,6 +144,7 @@ struct Csr {
     // Grid of the pipelined one-thread-row SpMV (blocks resident at once; 0
     // until first used).
     int32_t pipe_grid_spmv = 0;
+    AttnPlans *attn = nullptr;         // owned: work items of the attention kernels (null until used)
 };
 
 inline size_t dtype_size(sla_dtype dt) { return dt == SLA_F64 ? 8 : 4; }
@@ -177,6 +179,8 @@ sla_status build_sell(Csr *h, bool sort_ok, cudaStream_t s);
 sla_status cg_tile_deps(Csr *h, cudaStream_t s);   // in sla_cg.cu
 // vals_sell[b][slot] = vals[b][sell_map[slot]] (0 for padding), every system.
 sla_status sell_values(const Csr *h, const void *vals, void *vals_sell, cudaStream_t s);
+
+void free_attn_plans(Csr *h);          // in sla_attention.cu
 
 // Diagonal positions of a square pattern (kernel; enqueue only).
 sla_status diag_positions(int32_t n, const int32_t *rowptr, const int32_t *colind,

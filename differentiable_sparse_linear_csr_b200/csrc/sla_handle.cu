@@ -469,6 +469,7 @@ extern "C" sla_status sla_csr_destroy(sla_csr_t hh) {
     cudaFree(h->dep_hi);
     cudaFree(h->seg);
     cudaFree(h->seg_order);
+    free_attn_plans(h);
     delete h;
     return SLA_OK;
 }

@@ -58,7 +58,9 @@ extern "C" {
 
 typedef struct sla_csr_s *sla_csr_t;
 
-typedef enum { SLA_F64 = 0, SLA_F32 = 1 } sla_dtype;
+/* A handle's values are SLA_F64 or SLA_F32; the 16-bit types are for the tensors
+ * of sla_attention and sla_clip_norm. */
+typedef enum { SLA_F64 = 0, SLA_F32 = 1, SLA_BF16 = 2, SLA_F16 = 3 } sla_dtype;
 
 /* Call-level status. */
 typedef enum {
@@ -425,6 +427,96 @@ sla_status sla_laplacian_grad_values(sla_edges_t e, const void *G, void *dw, voi
 sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, void *dw,
                               void *dshift, int32_t flags, void *ws, size_t ws_bytes,
                               void *stream);
+
+/*
+ * Attention over a handle's pattern.  The pages have no counterpart: it is the
+ * layer that learns on the graphs and meshes whose matrices the other calls
+ * solve, and stands beside `.matvec`: row i (a query) takes a weighted mean of
+ * the v rows of the columns stored in row i.  For system b, head h (key head
+ * g = h / (heads / kv_heads)) and entry t = (i, j):
+ *   s_t = scale * (q_i . k_j) + vals_t;   p = softmax of s over the row's entries;
+ *   o_i = sum_t p_t v_j;                  lse_i = log sum_t exp(s_t).
+ * vals (the handle's dtype, [B][nnz]) is shared by the heads; NULL means 0.  An
+ * entry whose value is -inf is left out: its k and v are not used (they may be
+ * anything, NaN included).  A row without entries, or with none left, gives
+ * o_i = 0 and lse_i = -inf.  The pattern may be rectangular (queries over the
+ * states of another length), of one row, or a list handle's.
+ *
+ * q: [B][n_rows][heads][dim], k and v: [B][n_cols][kv_heads][dim], of opts.dtype
+ * (any sla_dtype, whatever the handle's), with the strides of opts; the last
+ * dimension is contiguous.  out [B][n_rows][heads][dim] (opts.dtype) and lse
+ * [B][n_rows][heads] (double for SLA_F64, else float) are contiguous.
+ * out_wide: NULL, or for 16-bit types a float array like out that receives o
+ * before its rounding (ignored for the others).  Sums,
+ * maxima and weights are held in 32 bits (64 for SLA_F64) and every sum has a
+ * fixed order: equal calls give equal bits.
+ *
+ * sla_attention_grad needs lse and the unrounded o of the forward call (out, or
+ * out_wide for 16-bit types: the difference below would keep only the rounded
+ * o's digits) and dout = dL/dout:
+ *   ds_t = p_t (dout_i . v_j - dout_i . o_i);   dq_i = scale sum_t ds_t k_j;
+ *   dk_j = scale sum_t ds_t q_i;  dv_j = sum_t p_t dout_i  (over the heads that
+ *   share the key head);  dvals_t = sum_heads ds_t (0 for entries left out).
+ * dq, dk, dv (contiguous, opts.dtype) and dvals (the handle's dtype) are
+ * overwritten; any may be NULL.
+ *
+ * Both need a plan of the pattern (and the gradients A^T's pattern), which the
+ * first call builds (host synchronisation, device memory owned by the handle)
+ * and which a stream capture cannot hold (SLA_ERR_UNSUPPORTED): call
+ * sla_attention_prepare before capturing, and before asking for the workspace
+ * size (0 until then).  Workspaces are 256-byte aligned; calls in flight at the
+ * same time need distinct ones.
+ */
+typedef struct {
+    int32_t dtype;            /* sla_dtype of q, k, v, out and their gradients */
+    int32_t heads;            /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;         /* key and value heads */
+    int32_t dim;              /* elements of one head, 1 to 256 */
+    double scale;             /* factor of the scores, finite */
+    int64_t q_stride[3];      /* elements between systems, rows and heads of q */
+    int64_t k_stride[3];
+    int64_t v_stride[3];
+    int64_t do_stride[3];     /* of dout (sla_attention_grad) */
+} sla_attn_opts;
+sla_status sla_attention_prepare(sla_csr_t h, int32_t backward, void *stream);
+size_t sla_attention_workspace_bytes(sla_csr_t h, const sla_attn_opts *opts, int32_t backward);
+sla_status sla_attention(sla_csr_t h, const void *q, const void *k, const void *v, const void *vals,
+                         void *out, void *out_wide, void *lse, const sla_attn_opts *opts, void *ws,
+                         size_t ws_bytes, void *stream);
+sla_status sla_attention_grad(sla_csr_t h, const void *q, const void *k, const void *v,
+                              const void *vals, const void *out, const void *lse, const void *dout,
+                              void *dq, void *dk, void *dv, void *dvals, const sla_attn_opts *opts,
+                              void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Global norm of many tensors and their scaling to a bound.  The pages have no
+ * counterpart: it is the step between the gradients (sla_grad_values,
+ * sla_laplacian_grad, sla_attention_grad) and an optimizer:
+ *   norm = sqrt(sum over all tensors and elements of x^2)   (SLA_NORM_L2)
+ *        = max |x|                                          (SLA_NORM_MAX)
+ *   dst = src * f,   f = min(1, max_norm / (norm + 1e-6)).
+ * list: host array, read during the call only (the kernels get the addresses
+ * as arguments, so a captured call keeps them).  Squares are summed in 64 bits
+ * in a fixed order; norm (device, SLA_F64 or SLA_F32) is rounded once.  f is
+ * applied in 64 bits to SLA_F64 tensors, else in 32.  dst may be src (in place;
+ * f == 1 then writes nothing); any other sharing of memory between an output
+ * and another tensor is SLA_ERR_INVALID.  A NaN among the elements gives a NaN
+ * norm and f; an infinite one gives norm = inf and f = 0.  An empty list has
+ * norm 0.  sla_global_norm does not read dst.  ws: device, 256-byte aligned,
+ * >= sla_norm_workspace_bytes(n).
+ */
+typedef struct {
+    const void *src;          /* device, `count` consecutive elements */
+    void *dst;                /* device; unused by sla_global_norm */
+    int64_t count;            /* may be 0 */
+    int64_t dtype;            /* sla_dtype */
+} sla_tensor;
+enum { SLA_NORM_L2 = 0, SLA_NORM_MAX = 1 };
+size_t sla_norm_workspace_bytes(int32_t n);
+sla_status sla_global_norm(int32_t n, const sla_tensor *list, int32_t kind, void *norm,
+                           int32_t norm_dtype, void *ws, size_t ws_bytes, void *stream);
+sla_status sla_clip_norm(int32_t n, const sla_tensor *list, int32_t kind, double max_norm, void *norm,
+                         int32_t norm_dtype, void *ws, size_t ws_bytes, void *stream);
 
 /*
  * Bounds record of the bounds-checking build (libsla_debug_bounds.so, compiled
