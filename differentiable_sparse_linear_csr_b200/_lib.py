@@ -104,7 +104,7 @@ _SIGNATURES = {
     "sla_edges_workspace_bytes": ([_P], _SZ),
     "sla_laplacian_grad_values": ([_P, _P, _P, _P, _I32, _P, _SZ, _P], _I32),
     "sla_laplacian_grad": ([_P, _P, _P, _P, _P, _I32, _P, _SZ, _P], _I32),
-    "sla_attention_prepare": ([_P, _I32, _P], _I32),
+    "sla_attention_prepare": ([_P, ctypes.POINTER(sla_attn_opts), _I32, _P], _I32),
     "sla_attention_workspace_bytes": ([_P, ctypes.POINTER(sla_attn_opts), _I32], _SZ),
     "sla_attention": ([_P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(sla_attn_opts), _P, _SZ, _P], _I32),
     "sla_attention_grad": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.POINTER(sla_attn_opts),
@@ -347,8 +347,9 @@ TENSOR_DTYPES = {torch.float64: SLA_F64, torch.float32: SLA_F32, torch.bfloat16:
                  torch.float16: SLA_F16}
 
 
-def sla_attention_prepare(h, backward=0, stream=None) -> None:
-    _check("sla_attention_prepare", lib().sla_attention_prepare(h, int(backward), _stream(stream)))
+def sla_attention_prepare(h, opts=None, backward=0, stream=None) -> None:
+    _check("sla_attention_prepare", lib().sla_attention_prepare(
+        h, None if opts is None else ctypes.byref(opts), int(backward), _stream(stream)))
 
 
 def make_attn_opts(dtype, heads, kv_heads, dim, scale, q_stride, k_stride, v_stride,

@@ -165,7 +165,7 @@ class CSR:
         pattern and plan) now instead of at the first call: needed before the
         calls are captured into a CUDA graph.  Synchronises the host."""
         with torch.cuda.device(self.device):
-            L.sla_attention_prepare(self.handle, backward)
+            L.sla_attention_prepare(self.handle, None, backward)
 
     def attention(self, q, k, v, values=None, *, scale: float | None = None) -> torch.Tensor:
         """Attention over the pattern: row i of A is a query that attends to the
@@ -179,9 +179,9 @@ class CSR:
         most 256, H a multiple of K (query head h reads key head h // (H // K)).
         values [B, nnz] (A's dtype, shared by the heads) are added to the scores;
         an entry whose value is -inf is left out, whatever its k and v hold.  A
-        row with no entry left gives zeros.  scale defaults to D ** -0.5.  The
-        last dimension is copied if it is not contiguous; other strides are used
-        as they are.  Returns o shaped like q.  Sums have a fixed order: equal
+        row with no entry left gives zeros.  scale defaults to D ** -0.5.  A tensor's
+        last dimension is copied if it is not contiguous, and in 16 bits a tensor
+        whose rows do not start on 16 bytes; other strides are used as they are.  Returns o shaped like q.  Sums have a fixed order: equal
         calls give equal bits.
         """
         q4, k4, v4 = self._heads(q, self.n_rows, "q"), self._heads(k, self.n_cols, "k"), \
@@ -313,14 +313,20 @@ class _Solve(torch.autograd.Function):
         return None, gv, gb, None
 
 
-def _unit_stride(x: torch.Tensor) -> torch.Tensor:
-    return x if x.stride(-1) == 1 or x.numel() == 0 else x.contiguous()
+def _head_layout(x: torch.Tensor) -> torch.Tensor:
+    """x as the kernels read it: the last dimension contiguous and, in 16 bits,
+    the other strides and the address on 16 bytes; a copy if it is not."""
+    st = x.stride()
+    if st[3] != 1 or (x.element_size() == 2 and ((st[0] | st[1] | st[2]) & 7 or x.data_ptr() & 15)
+                      and x.shape[3] % 8 == 0):
+        x = x.clone(memory_format=torch.contiguous_format)
+    return x
 
 
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, A: CSR, q, k, v, values, scale):
-        q, k, v = _unit_stride(q), _unit_stride(k), _unit_stride(v)
+        q, k, v = _head_layout(q), _head_layout(k), _head_layout(v)
         B, n, H, D = q.shape
         vals = None if values is None else A._values(values)
         out = torch.empty(B, n, H, D, dtype=q.dtype, device=A.device)
@@ -330,9 +336,9 @@ class _Attention(torch.autograd.Function):
         wide = torch.empty(B, n, H, D, dtype=torch.float32, device=A.device) \
             if train and q.element_size() == 2 else None
         with torch.cuda.device(A.device):
-            L.sla_attention_prepare(A.handle, train)
             opts = L.make_attn_opts(q.dtype, H, k.shape[2], D, scale, q.stride()[:3], k.stride()[:3],
                                     v.stride()[:3])
+            L.sla_attention_prepare(A.handle, opts, train)
             ws = _workspace(L.sla_attention_workspace_bytes(A.handle, opts, 0), A.device)
             L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts, ws)
         ctx.A, ctx.scale = A, scale
@@ -344,7 +350,7 @@ class _Attention(torch.autograd.Function):
     def backward(ctx, go):
         A = ctx.A
         q, k, v, values, out, lse = ctx.saved_tensors
-        go = _unit_stride(go)
+        go = _head_layout(go)
         vals = None if values is None else A._values(values)
         new = lambda need, t: torch.empty(t.shape, dtype=t.dtype, device=A.device) if need else None  # noqa: E731
         dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[1:5], (q, k, v, values)))

@@ -8,7 +8,9 @@
 
 #include <algorithm>
 #include <climits>
+#include <initializer_list>
 #include <new>
+#include <utility>
 
 namespace sla {
 
@@ -65,35 +67,14 @@ void free_plan(AttnPlan *p) {
     cudaFree(p->item_slot);
     cudaFree(p->multi_unit);
     cudaFree(p->multi_slot);
+    cudaFree(p->chunk_ptr);
+    cudaFree(p->cols);
+    cudaFree(p->bits);
+    cudaFree(p->row_start);
     *p = AttnPlan();
 }
 
-struct DeviceScratch {
-    std::vector<void *> held;
-    ~DeviceScratch() {
-        for (void *p : held) cudaFree(p);
-    }
-    template <typename U>
-    U *get(size_t count) {
-        void *p = nullptr;
-        if (cudaMalloc(&p, std::max<size_t>(count, 1) * sizeof(U)) != cudaSuccess) {
-            cudaGetLastError();
-            return nullptr;
-        }
-        held.push_back(p);
-        return static_cast<U *>(p);
-    }
-};
-
-bool alloc_i32(int32_t **p, size_t count) {
-    if (cudaMalloc(p, std::max<size_t>(count, 1) * sizeof(int32_t)) == cudaSuccess) return true;
-    cudaGetLastError();
-    return false;
-}
-
-inline unsigned blocks_of(int64_t n, int t = 256) { return (unsigned)((n + t - 1) / t); }
-
-sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s) {
+sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, int level, cudaStream_t s) {
     const int n = transposed ? h->n_cols : h->n_rows;
     const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr;
     p->rows = rows;
@@ -118,10 +99,12 @@ sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream
     unsigned total = 0;
     SLA_CHECK_CUDA(cudaMemcpyAsync(&total, sum + U, sizeof total, cudaMemcpyDeviceToHost, s));
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
-    // Enough segments to fill the GPU when there are few units (8 an SM), none
+    // Enough segments to fill the GPU (16 an SM) when there are few units, none
     // shorter than 64 entries: a shorter one spends more on its partial result
-    // than on its entries.
-    const int64_t want = ((int64_t)total + h->num_sms * 8 - 1) / ((int64_t)h->num_sms * 8);
+    // than on its entries.  A level counts on 8 times as many systems and heads
+    // as the one before, so it splits 8 times less.
+    const int64_t fill = std::max<int64_t>(1, (int64_t)h->num_sms * 16 >> (3 * level));
+    const int64_t want = ((int64_t)total + fill - 1) / fill;
     p->seg_len = (int32_t)std::max<int64_t>(64, (want + 15) / 16 * 16);
     unit_split_kernel<<<blocks_of(U + 1), 256, 0, s>>>(U, p->seg_len, len, nseg, slots, multi);
     SLA_CHECK_LAUNCH();
@@ -137,9 +120,9 @@ sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream
     p->n_slots = (int32_t)tot[1];
     p->n_multi = (int32_t)tot[2];
     if (p->n_multi > 0) {
-        if (!alloc_i32(&p->item_unit, tot[0]) || !alloc_i32(&p->item_seg, tot[0]) ||
-            !alloc_i32(&p->item_slot, tot[0]) || !alloc_i32(&p->multi_unit, tot[2]) ||
-            !alloc_i32(&p->multi_slot, (size_t)tot[2] + 1)) {
+        if (!alloc_array(&p->item_unit, tot[0]) || !alloc_array(&p->item_seg, tot[0]) ||
+            !alloc_array(&p->item_slot, tot[0]) || !alloc_array(&p->multi_unit, tot[2]) ||
+            !alloc_array(&p->multi_slot, (size_t)tot[2] + 1)) {
             set_error("attention plan: out of device memory");
             return SLA_ERR_OOM;
         }
@@ -147,23 +130,53 @@ sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream
                                                           p->item_slot, p->multi_unit, p->multi_slot);
         SLA_CHECK_LAUNCH();
     }
+    if (rows == kTileRows) {
+        st = build_tiles(p, n, rowptr, transposed ? h->colindT : h->colind, s);
+        if (st != SLA_OK) return st;
+    }
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
     p->built = true;
     return SLA_OK;
 }
 
+sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
+    AttnPlan *p = &(tiled ? h->attn->tile : h->attn->row)[transposed][level];
+    if (p->built) return SLA_OK;
+    sla_status st = SLA_ERR_OOM;
+    try {
+        st = build_plan(h, p, tiled ? kTileRows : 1, transposed, level, s);
+    } catch (const std::bad_alloc &) {
+        set_error("sla_attention_prepare: out of host memory");
+    }
+    if (st != SLA_OK) {
+        cudaStreamSynchronize(s);
+        free_plan(p);
+    }
+    return st;
+}
+
 }  // namespace
 
-sla_status ensure_attn_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s) {
-    if (p->built) return SLA_OK;
-    const sla_status st = build_plan(h, p, rows, transposed, s);
-    if (st != SLA_OK) free_plan(p);
-    return st;
+void use_plan(AttnArgs &a, const AttnPlan &p) {
+    a.n_items = p.n_items;
+    a.n_slots = p.n_slots;
+    a.seg_len = p.seg_len;
+    a.item_unit = p.item_unit;
+    a.item_seg = p.item_seg;
+    a.item_slot = p.item_slot;
+    a.chunk_ptr = p.chunk_ptr;
+    a.cols = p.cols;
+    a.bits = p.bits;
+    a.row_start = p.row_start;
 }
 
 void free_attn_plans(Csr *h) {
     if (!h->attn) return;
-    for (AttnPlan &p : h->attn->row) free_plan(&p);
+    for (int t = 0; t < 2; ++t)
+        for (int l = 0; l < kAttnLevels; ++l) {
+            free_plan(&h->attn->row[t][l]);
+            free_plan(&h->attn->tile[t][l]);
+        }
     delete h->attn;
     h->attn = nullptr;
 }
@@ -564,7 +577,19 @@ attn_join_sums_kernel(const typename AccOf<T>::type *__restrict__ part, int n_ro
     }
 }
 
-// dvals_t = sum over the heads of ds_t, in the values' type.
+// dvals_t = sum over the heads of ds_t, in the values' type; the same from
+// [B][heads][nnz].
+template <typename V>
+__global__ void __launch_bounds__(256)
+attn_dvals_heads_kernel(int64_t count, int64_t nnz, int heads, const float *__restrict__ ds, V *__restrict__ dvals) {
+    const int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (t >= count) return;
+    const float *p = ds + t / nnz * nnz * heads + t % nnz;
+    float x = 0.0f;
+    for (int h = 0; h < heads; ++h) x += p[h * nnz];
+    dvals[t] = (V)x;
+}
+
 template <typename A, typename V>
 __global__ void __launch_bounds__(256)
 attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__restrict__ dvals) {
@@ -574,6 +599,32 @@ attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__rest
     for (int h = 0; h < heads; ++h) x += pds[(t * heads + h) * 2 + 1];
     dvals[t] = (V)x;
 }
+
+}  // namespace
+
+template <typename T>
+sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s) {
+    if (p.n_multi == 0) return SLA_OK;
+    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * a.heads;
+    attn_join_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit,
+                                                                                    p.multi_slot);
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
+template <typename T>
+sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int heads, int width, void *out0, void *out1,
+                          cudaStream_t s) {
+    if (p.n_multi == 0) return SLA_OK;
+    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * heads;
+    attn_join_sums_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(
+        static_cast<const typename AccOf<T>::type *>(a.part), n_rows, a.batch, p.n_slots, p.rows, heads, a.dim, width,
+        p.n_multi, p.multi_unit, p.multi_slot, static_cast<T *>(out0), static_cast<T *>(out1));
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
+namespace {
 
 // -------------------------------------------------------------- launches ----
 enum { kFwd, kBwdRows, kBwdCols };
@@ -616,112 +667,132 @@ bool on_16_bytes(const void *p, const int64_t st[3], size_t size) {
     return true;
 }
 
-template <typename T>
-sla_status join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int heads, int width, void *out0, void *out1,
-                     cudaStream_t s) {
-    if (p.n_multi == 0) return SLA_OK;
-    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * heads;
-    attn_join_sums_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(
-        static_cast<const typename AccOf<T>::type *>(a.part), n_rows, a.batch, p.n_slots, p.rows, heads, a.dim, width,
-        p.n_multi, p.multi_unit, p.multi_slot, static_cast<T *>(out0), static_cast<T *>(out1));
-    SLA_CHECK_LAUNCH();
-    return SLA_OK;
-}
-
-void use_plan(AttnArgs &a, const AttnPlan &p) {
-    a.n_units = p.n_units;
-    a.n_items = p.n_items;
-    a.n_slots = p.n_slots;
-    a.seg_len = p.seg_len;
-    a.item_unit = p.item_unit;
-    a.item_seg = p.item_seg;
-    a.item_slot = p.item_slot;
-}
-
 size_t acc_size(int32_t dt) { return dt == SLA_F64 ? 8 : 4; }
 
 template <typename T>
-sla_status attn_forward(const Csr *h, AttnArgs a, cudaStream_t s) {
-    const AttnPlan &p = h->attn->row[0];
+sla_status attn_forward(const AttnPlan &p, AttnArgs a, bool tiled, cudaStream_t s) {
+    using A = typename AccOf<T>::type;
     use_plan(a, p);
-    a.rowptr = h->rowptr;
-    a.colind = h->colind;
-    const int V = 16 / sizeof(T);
-    const bool vec = a.dim % V == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) && on_16_bytes(a.k, a.ks, sizeof(T)) &&
-                     on_16_bytes(a.v, a.vs, sizeof(T)) && (((uintptr_t)a.out | (uintptr_t)a.wide) & 15) == 0;
-    sla_status st = launch_rows_of<T>(kFwd, a, vec, s);
-    if (st != SLA_OK || p.n_multi == 0) return st;
-    const int64_t warps = (int64_t)a.batch * p.n_multi * a.heads;
-    attn_join_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(a, 1, p.n_multi, p.multi_unit,
-                                                                                    p.multi_slot);
+    sla_status st;
+    if constexpr (sizeof(T) == 2) {
+        if (tiled) {
+            st = attn_tile_forward<T>(a, s);
+            return st != SLA_OK ? st : attn_join<T>(a, p, s);
+        }
+    }
+    const int64_t dense[3] = {(int64_t)a.dim, (int64_t)a.dim, (int64_t)a.dim};
+    const bool vec = a.dim % (16 / (int)sizeof(T)) == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) &&
+                     on_16_bytes(a.k, a.ks, sizeof(T)) && on_16_bytes(a.v, a.vs, sizeof(T)) &&
+                     on_16_bytes(a.out, dense, sizeof(T)) && on_16_bytes(a.wide, dense, sizeof(A));
+    st = launch_rows_of<T>(kFwd, a, vec, s);
+    return st != SLA_OK ? st : attn_join<T>(a, p, s);
+}
+
+template <typename A, typename V>
+sla_status attn_dvals(const AttnArgs &a, bool tiled, cudaStream_t s) {
+    const int64_t entries = (int64_t)a.batch * a.nnz;
+    if (entries == 0) return SLA_OK;
+    if (tiled)
+        attn_dvals_heads_kernel<V><<<blocks_of(entries), 256, 0, s>>>(entries, a.nnz, a.heads, a.ds_out,
+                                                                     static_cast<V *>(a.dvals));
+    else
+        attn_dvals_kernel<A, V><<<blocks_of(entries), 256, 0, s>>>(entries, a.heads, static_cast<const A *>(a.pds),
+                                                                   static_cast<V *>(a.dvals));
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }
 
 template <typename T>
-sla_status attn_backward(const Csr *h, AttnArgs a, cudaStream_t s) {
+sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, AttnArgs a, bool tiled, cudaStream_t s) {
     using A = typename AccOf<T>::type;
-    const AttnPlan &p = h->attn->row[0];
-    const int V = 16 / sizeof(T);
     const int64_t dense[3] = {(int64_t)a.dim, (int64_t)a.dim, (int64_t)a.dim};
-    const bool vec = a.dim % V == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) && on_16_bytes(a.k, a.ks, sizeof(T)) &&
-                     on_16_bytes(a.v, a.vs, sizeof(T)) && on_16_bytes(a.dout, a.ds, sizeof(T)) &&
-                     on_16_bytes(a.o, dense, sizeof(A)) && on_16_bytes(a.dq, dense, sizeof(T)) &&
-                     on_16_bytes(a.dk, dense, sizeof(T)) && on_16_bytes(a.dv, dense, sizeof(T));
+    const bool vec = a.dim % (16 / (int)sizeof(T)) == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) &&
+                     on_16_bytes(a.k, a.ks, sizeof(T)) && on_16_bytes(a.v, a.vs, sizeof(T)) &&
+                     on_16_bytes(a.dout, a.ds, sizeof(T)) && on_16_bytes(a.o, dense, sizeof(A)) &&
+                     on_16_bytes(a.dq, dense, sizeof(T)) && on_16_bytes(a.dk, dense, sizeof(T)) &&
+                     on_16_bytes(a.dv, dense, sizeof(T));
     use_plan(a, p);
-    a.rowptr = h->rowptr;
-    a.colind = h->colind;
-    sla_status st = launch_rows_of<T>(kBwdRows, a, vec, s);
+    sla_status st;
+    if constexpr (sizeof(T) == 2) st = tiled ? attn_tile_bwd_rows<T>(a, s) : launch_rows_of<T>(kBwdRows, a, vec, s);
+    else st = launch_rows_of<T>(kBwdRows, a, vec, s);
     if (st != SLA_OK) return st;
-    if (a.dq && (st = join_sums<T>(a, p, a.n_rows, a.heads, a.dim, a.dq, nullptr, s)) != SLA_OK) return st;
-    const int64_t entries = (int64_t)a.batch * a.nnz;
-    if (a.dvals && entries > 0) {
-        if (a.vals_f64)
-            attn_dvals_kernel<A, double><<<blocks_of(entries), 256, 0, s>>>(
-                entries, a.heads, static_cast<const A *>(a.pds), static_cast<double *>(a.dvals));
-        else
-            attn_dvals_kernel<A, float><<<blocks_of(entries), 256, 0, s>>>(
-                entries, a.heads, static_cast<const A *>(a.pds), static_cast<float *>(a.dvals));
-        SLA_CHECK_LAUNCH();
+    if (a.dq && (st = attn_join_sums<T>(a, p, a.n_rows, a.heads, a.dim, a.dq, nullptr, s)) != SLA_OK) return st;
+    if (a.dvals) {
+        st = a.vals_f64 ? attn_dvals<A, double>(a, tiled, s) : attn_dvals<A, float>(a, tiled, s);
+        if (st != SLA_OK) return st;
     }
     if (!a.dk && !a.dv) return SLA_OK;
-    const AttnPlan &pt = h->attn->row[1];
     use_plan(a, pt);
     a.rowptr = h->rowptrT;
     a.colind = h->colindT;
     a.perm = h->permT;
-    st = launch_rows_of<T>(kBwdCols, a, vec, s);
+    if constexpr (sizeof(T) == 2) st = tiled ? attn_tile_bwd_cols<T>(a, s) : launch_rows_of<T>(kBwdCols, a, vec, s);
+    else st = launch_rows_of<T>(kBwdCols, a, vec, s);
     if (st != SLA_OK) return st;
-    return join_sums<T>(a, pt, a.n_cols, a.kv_heads, 2 * a.dim, a.dk, a.dv, s);
+    return attn_join_sums<T>(a, pt, a.n_cols, a.kv_heads, 2 * a.dim, a.dk, a.dv, s);
 }
 
-// Workspace: (p, ds) of every entry and head (backward), then the partial sums.
-size_t attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
-    const size_t acc = acc_size(o->dtype), B = (size_t)h->batch;
-    const AttnPlan &p = h->attn->row[0], &pt = h->attn->row[1];
-    if (!backward) return align_up(B * p.n_slots * o->heads * (size_t)(o->dim + 2) * acc);
-    const size_t rows = B * p.n_slots * o->heads * (size_t)o->dim * acc;
-    const size_t cols = B * pt.n_slots * o->kv_heads * 2 * (size_t)o->dim * acc;
-    return align_up(B * (size_t)h->nnz * o->heads * 2 * acc) + align_up(std::max(rows, cols));
+// Workspace pieces: what the backward keeps for every entry (row kernels) or
+// row (tile kernels), then the partial sums of split rows.
+struct AttnWs {
+    size_t pds = 0, stat = 0, ds = 0, part = 0;
+    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(part); }
+};
+
+const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
+    return (attn_tiled(o) ? h->attn->tile : h->attn->row)[transposed][attn_level(h, o)];
 }
 
-sla_status check_opts(const char *fn, const Csr *h, const sla_attn_opts *o) {
-    SLA_REQUIRE(h != nullptr, "%s: NULL handle", fn);
+AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
+    const size_t acc = acc_size(o->dtype), B = (size_t)h->batch, H = (size_t)o->heads, D = (size_t)o->dim;
+    const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
+    AttnWs w;
+    if (!backward) {
+        w.part = B * p.n_slots * p.rows * H * (D + 2) * acc;
+        return w;
+    }
+    if (attn_tiled(o)) {
+        w.stat = B * H * (size_t)h->n_rows * sizeof(float2);
+        w.ds = B * H * (size_t)h->nnz * sizeof(float);
+    } else {
+        w.pds = B * (size_t)h->nnz * H * 2 * acc;
+    }
+    w.part = std::max(B * p.n_slots * p.rows * H * D * acc, B * pt.n_slots * pt.rows * (size_t)o->kv_heads * 2 * D * acc);
+    return w;
+}
+
+sla_status check_opts(const char *fn, const sla_attn_opts *o) {
     SLA_REQUIRE(o != nullptr, "%s: NULL options", fn);
     SLA_REQUIRE(o->dtype >= SLA_F64 && o->dtype <= SLA_F16, "%s: bad dtype %d", fn, o->dtype);
     SLA_REQUIRE(o->heads >= 1 && o->kv_heads >= 1 && o->heads % o->kv_heads == 0 && o->heads <= 65536,
                 "%s: heads must be a positive multiple of kv_heads (%d, %d)", fn, o->heads, o->kv_heads);
     SLA_REQUIRE(o->dim >= 1 && o->dim <= 256, "%s: dim must be in [1, 256] (got %d)", fn, o->dim);
     SLA_REQUIRE(o->scale == o->scale && o->scale <= DBL_MAX && o->scale >= -DBL_MAX, "%s: scale is not finite", fn);
+    return SLA_OK;
+}
+
+sla_status check_device(const char *fn, const Csr *h) {
+    SLA_REQUIRE(h != nullptr, "%s: NULL handle", fn);
     int dev = -1;
     SLA_CHECK_CUDA(cudaGetDevice(&dev));
     SLA_REQUIRE(dev == h->device, "%s: the handle lives on device %d, the current device is %d", fn, h->device, dev);
     return SLA_OK;
 }
 
-sla_status prepare(Csr *h, bool backward, cudaStream_t s) {
-    const bool ready = h->attn && h->attn->row[0].built && (!backward || (h->has_transpose && h->attn->row[1].built));
-    if (ready) return SLA_OK;
+bool plans_ready(const Csr *h, const sla_attn_opts *o, bool backward) {
+    if (!h->attn || (backward && !h->has_transpose)) return false;
+    for (int l = 0; l < kAttnLevels; ++l)
+        for (int tiled = 0; tiled < 2; ++tiled) {
+            if (o && (l != attn_level(h, o) || (bool)tiled != attn_tiled(o))) continue;
+            const auto &p = tiled ? h->attn->tile : h->attn->row;
+            if (!p[0][l].built || (backward && !p[1][l].built)) return false;
+        }
+    return true;
+}
+
+// The plans these options need; every one without options.
+sla_status prepare(Csr *h, const sla_attn_opts *o, bool backward, cudaStream_t s) {
+    if (plans_ready(h, o, backward)) return SLA_OK;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
         cudaGetLastError();
@@ -736,11 +807,27 @@ sla_status prepare(Csr *h, bool backward, cudaStream_t s) {
             return SLA_ERR_OOM;
         }
     }
-    sla_status st = ensure_attn_plan(h, &h->attn->row[0], 1, false, s);
-    if (st != SLA_OK || !backward) return st;
-    st = ensure_transpose(h, s);
-    if (st == SLA_OK) st = ensure_attn_plan(h, &h->attn->row[1], 1, true, s);
-    return st;
+    sla_status st = SLA_OK;
+    if (backward && (st = ensure_transpose(h, s)) != SLA_OK) return st;
+    for (int l = 0; l < kAttnLevels; ++l)
+        for (int tiled = 0; tiled < 2; ++tiled) {
+            if (o && (l != attn_level(h, o) || (bool)tiled != attn_tiled(o))) continue;
+            for (int t = 0; t <= (backward ? 1 : 0); ++t)
+                if ((st = ensure_plan(h, tiled != 0, t != 0, l, s)) != SLA_OK) return st;
+        }
+    return SLA_OK;
+}
+
+// The tile kernels read 16 bytes at a time.
+sla_status check_tiled(const char *fn, const sla_attn_opts *o, std::initializer_list<const void *> dense,
+                       std::initializer_list<std::pair<const void *, const int64_t *>> strided) {
+    if (!attn_tiled(o)) return SLA_OK;
+    bool ok = true;
+    for (const void *p : dense) ok = ok && ((uintptr_t)p & 15) == 0;
+    for (const auto &x : strided) ok = ok && on_16_bytes(x.first, x.second, 2);
+    SLA_REQUIRE(ok, "%s: 16-bit heads of a multiple of 16 elements need addresses and strides of a multiple of 16 bytes",
+                fn);
+    return SLA_OK;
 }
 
 AttnArgs make_args(const Csr *h, const sla_attn_opts *o, const void *q, const void *k, const void *v,
@@ -750,6 +837,8 @@ AttnArgs make_args(const Csr *h, const sla_attn_opts *o, const void *q, const vo
     a.n_cols = h->n_cols;
     a.batch = h->batch;
     a.nnz = h->nnz;
+    a.rowptr = h->rowptr;
+    a.colind = h->colind;
     a.heads = o->heads;
     a.kv_heads = o->kv_heads;
     a.dim = o->dim;
@@ -773,23 +862,20 @@ AttnArgs make_args(const Csr *h, const sla_attn_opts *o, const void *q, const vo
 
 using namespace sla;
 
-extern "C" sla_status sla_attention_prepare(sla_csr_t hh, int32_t backward, void *stream) {
+extern "C" sla_status sla_attention_prepare(sla_csr_t hh, const sla_attn_opts *o, int32_t backward, void *stream) {
     SLA_RANGE("sla_attention_prepare");
     clear_error();
     Csr *h = reinterpret_cast<Csr *>(hh);
-    SLA_REQUIRE(h != nullptr, "sla_attention_prepare: NULL handle");
-    int dev = -1;
-    SLA_CHECK_CUDA(cudaGetDevice(&dev));
-    SLA_REQUIRE(dev == h->device, "sla_attention_prepare: the handle lives on device %d, the current device is %d",
-                h->device, dev);
-    return prepare(h, backward != 0, as_stream(stream));
+    sla_status st = check_device("sla_attention_prepare", h);
+    if (st == SLA_OK && o) st = check_opts("sla_attention_prepare", o);
+    return st != SLA_OK ? st : prepare(h, o, backward != 0, as_stream(stream));
 }
 
 extern "C" size_t sla_attention_workspace_bytes(sla_csr_t hh, const sla_attn_opts *o, int32_t backward) {
     const Csr *h = reinterpret_cast<const Csr *>(hh);
-    if (!h || !o || !h->attn || !h->attn->row[0].built || (backward && !h->attn->row[1].built)) return 0;
-    if (o->dtype < SLA_F64 || o->dtype > SLA_F16 || o->heads < 1 || o->kv_heads < 1 || o->dim < 1) return 0;
-    return attn_ws(h, o, backward != 0);
+    clear_error();
+    if (!h || check_opts("sla_attention_workspace_bytes", o) != SLA_OK || !plans_ready(h, o, backward != 0)) return 0;
+    return attn_ws(h, o, backward != 0).total();
 }
 
 extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, const void *v, const void *vals,
@@ -798,26 +884,32 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     SLA_RANGE("sla_attention");
     clear_error();
     Csr *h = reinterpret_cast<Csr *>(hh);
-    sla_status st = check_opts("sla_attention", h, o);
+    sla_status st = check_device("sla_attention", h);
+    if (st == SLA_OK) st = check_opts("sla_attention", o);
     if (st != SLA_OK) return st;
     if (h->n_rows == 0) return SLA_OK;
     SLA_REQUIRE(q && out && lse && (h->n_cols == 0 || (k && v)), "sla_attention: NULL pointer");
-    cudaStream_t s = as_stream(stream);
-    st = prepare(h, false, s);
+    if (o->dtype == SLA_F64 || o->dtype == SLA_F32) out_wide = nullptr;
+    st = check_tiled("sla_attention", o, {out, out_wide}, {{q, o->q_stride}, {k, o->k_stride}, {v, o->v_stride}});
     if (st != SLA_OK) return st;
-    const size_t need = attn_ws(h, o, false);
+    cudaStream_t s = as_stream(stream);
+    st = prepare(h, o, false, s);
+    if (st != SLA_OK) return st;
+    const size_t need = attn_ws(h, o, false).total();
     SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention: workspace too small (%zu < %zu)", ws_bytes, need);
     SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention: workspace must be 256-byte aligned");
     AttnArgs a = make_args(h, o, q, k, v, vals);
     a.out = out;
-    a.wide = o->dtype == SLA_BF16 || o->dtype == SLA_F16 ? out_wide : nullptr;
+    a.wide = out_wide;
     a.lse = lse;
     a.part = ws;
+    const AttnPlan &p = plan_of(h, o, false);
+    const bool tiled = attn_tiled(o);
     switch (o->dtype) {
-        case SLA_F64: return attn_forward<double>(h, a, s);
-        case SLA_F32: return attn_forward<float>(h, a, s);
-        case SLA_BF16: return attn_forward<__nv_bfloat16>(h, a, s);
-        default: return attn_forward<__half>(h, a, s);
+        case SLA_F64: return attn_forward<double>(p, a, tiled, s);
+        case SLA_F32: return attn_forward<float>(p, a, tiled, s);
+        case SLA_BF16: return attn_forward<__nv_bfloat16>(p, a, tiled, s);
+        default: return attn_forward<__half>(p, a, tiled, s);
     }
 }
 
@@ -828,18 +920,22 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     SLA_RANGE("sla_attention_grad");
     clear_error();
     Csr *h = reinterpret_cast<Csr *>(hh);
-    sla_status st = check_opts("sla_attention_grad", h, o);
+    sla_status st = check_device("sla_attention_grad", h);
+    if (st == SLA_OK) st = check_opts("sla_attention_grad", o);
     if (st != SLA_OK) return st;
     SLA_REQUIRE(!dvals || vals, "sla_attention_grad: dvals without vals");
     SLA_REQUIRE(h->n_rows == 0 || (q && out && lse && dout), "sla_attention_grad: NULL pointer");
     SLA_REQUIRE(h->n_cols == 0 || (k && v), "sla_attention_grad: NULL pointer");
+    st = check_tiled("sla_attention_grad", o, {out, dq, dk, dv},
+                     {{q, o->q_stride}, {k, o->k_stride}, {v, o->v_stride}, {dout, o->do_stride}});
+    if (st != SLA_OK) return st;
     cudaStream_t s = as_stream(stream);
     if (!dq && !dk && !dv && !dvals) return SLA_OK;
-    st = prepare(h, true, s);
+    st = prepare(h, o, true, s);
     if (st != SLA_OK) return st;
-    const size_t need = attn_ws(h, o, true);
-    SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention_grad: workspace too small (%zu < %zu)", ws_bytes,
-                need);
+    const AttnWs w = attn_ws(h, o, true);
+    SLA_REQUIRE(w.total() == 0 || (ws && ws_bytes >= w.total()), "sla_attention_grad: workspace too small (%zu < %zu)",
+                ws_bytes, w.total());
     SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention_grad: workspace must be 256-byte aligned");
     AttnArgs a = make_args(h, o, q, k, v, vals);
     a.o = out;
@@ -850,13 +946,17 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     a.dv = dv;
     a.dvals = dvals;
     Carver c(ws);
-    a.pds = c.take<char>((size_t)h->batch * h->nnz * o->heads * 2 * acc_size(o->dtype));
+    a.pds = c.take<char>(w.pds);
+    a.stat = reinterpret_cast<float2 *>(c.take<char>(w.stat));
+    a.ds_out = dvals ? reinterpret_cast<float *>(c.take<char>(w.ds)) : (c.take<char>(w.ds), nullptr);
+    a.part = c.take<char>(w.part);
     if (!dk && !dv && !dvals) a.pds = nullptr;
-    a.part = c.base ? c.base + c.off : nullptr;
+    const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
+    const bool tiled = attn_tiled(o);
     switch (o->dtype) {
-        case SLA_F64: return attn_backward<double>(h, a, s);
-        case SLA_F32: return attn_backward<float>(h, a, s);
-        case SLA_BF16: return attn_backward<__nv_bfloat16>(h, a, s);
-        default: return attn_backward<__half>(h, a, s);
+        case SLA_F64: return attn_backward<double>(h, p, pt, a, tiled, s);
+        case SLA_F32: return attn_backward<float>(h, p, pt, a, tiled, s);
+        case SLA_BF16: return attn_backward<__nv_bfloat16>(h, p, pt, a, tiled, s);
+        default: return attn_backward<__half>(h, p, pt, a, tiled, s);
     }
 }

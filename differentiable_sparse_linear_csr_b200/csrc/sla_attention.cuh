@@ -29,11 +29,34 @@ struct AttnPlan {
     int32_t *item_unit = nullptr, *item_seg = nullptr, *item_slot = nullptr;   // [n_items]
     int32_t *multi_unit = nullptr;                                             // [n_multi]
     int32_t *multi_slot = nullptr;                                             // [n_multi + 1]
+    // Tiles (rows == kTileRows): the columns any row of the item stores, in
+    // increasing order, 16 to a chunk (the last one padded with its last column),
+    // and for every row of a chunk the bits of the columns it stores.
+    int32_t *chunk_ptr = nullptr;                                              // [n_items + 1]
+    int32_t *cols = nullptr;                                                   // [n_chunks * 16]
+    uint16_t *bits = nullptr;                                                  // [n_chunks * 16]
+    int32_t *row_start = nullptr;      // [n_items * 16]: first entry of each row in the item
 };
 
+constexpr int kTileRows = 16;
+// How finely long rows are split depends on how many systems and heads share
+// the GPU: a plan for few, some and many of them.
+constexpr int kAttnLevels = 3;
+
 struct AttnPlans {
-    AttnPlan row[2];                 // one row a unit: A, A^T
+    AttnPlan row[2][kAttnLevels];      // one row a unit: A, A^T
+    AttnPlan tile[2][kAttnLevels];     // kTileRows rows a unit
 };
+
+inline int attn_level(const Csr *h, const sla_attn_opts *o) {
+    const int64_t share = (int64_t)h->batch * o->heads;
+    return share >= 64 ? 2 : (share >= 8 ? 1 : 0);
+}
+
+// 16-bit heads of whole 16-element steps go through the tensor cores.
+inline bool attn_tiled(const sla_attn_opts *o) {
+    return (o->dtype == SLA_BF16 || o->dtype == SLA_F16) && o->dim % 16 == 0 && o->dim <= 128;
+}
 
 // What every kernel gets (strides in elements, heads of `dim` consecutive elements).
 struct AttnArgs {
@@ -41,15 +64,19 @@ struct AttnArgs {
     int64_t nnz;
     double scale;
     const int32_t *rowptr, *colind, *perm;
-    int32_t n_units, n_items, n_slots, seg_len;
+    int32_t n_items, n_slots, seg_len;
     const int32_t *item_unit, *item_seg, *item_slot;
+    const int32_t *chunk_ptr, *cols, *row_start;
+    const uint16_t *bits;
     const void *q, *k, *v, *o, *dout;
     int64_t qs[3], ks[3], vs[3], ds[3];    // system, row, head
     const void *vals;
     int32_t vals_f64;
     void *out, *wide, *lse;                // forward (wide: out before its rounding, or null)
     void *dq, *dk, *dv, *dvals;            // backward
-    void *pds;                             // [B][nnz][heads] pairs (p, ds)
+    void *pds;                             // row kernels: [B][nnz][heads] pairs (p, ds)
+    float2 *stat;                          // tile kernels: [B][heads][n_rows] pairs (lse, D)
+    float *ds_out;                         // tile kernels: [B][heads][nnz] ds, or null
     void *part;                            // partial sums of split rows
 };
 
@@ -115,7 +142,47 @@ __host__ __device__ __forceinline__ int64_t part_index(int64_t slot, int32_t n_s
     return (((int64_t)b * n_slots + slot) * rows + r) * heads + h;
 }
 
-sla_status ensure_attn_plan(Csr *h, AttnPlan *p, int rows, bool transposed, cudaStream_t s);
+void use_plan(AttnArgs &a, const AttnPlan &p);
 void free_attn_plans(Csr *h);
+
+// Joins of split rows (sla_attention.cu), shared by the row and tile kernels.
+template <typename T>
+sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s);
+template <typename T>
+sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int heads, int width, void *out0, void *out1,
+                          cudaStream_t s);
+
+// Tile kernels (sla_attention_tile.cu): plan arrays of a tile plan, and the calls.
+sla_status build_tiles(AttnPlan *p, int n_rows, const int32_t *rowptr, const int32_t *colind, cudaStream_t s);
+template <typename T> sla_status attn_tile_forward(const AttnArgs &a, cudaStream_t s);
+template <typename T> sla_status attn_tile_bwd_rows(const AttnArgs &a, cudaStream_t s);
+template <typename T> sla_status attn_tile_bwd_cols(const AttnArgs &a, cudaStream_t s);
+
+inline unsigned blocks_of(int64_t n, int t = 256) { return (unsigned)((n + t - 1) / t); }
+
+// Device memory freed when the scope ends.
+struct DeviceScratch {
+    std::vector<void *> held;
+    ~DeviceScratch() {
+        for (void *p : held) cudaFree(p);
+    }
+    template <typename U>
+    U *get(size_t count) {
+        void *p = nullptr;
+        if (cudaMalloc(&p, (count > 0 ? count : 1) * sizeof(U)) != cudaSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        held.push_back(p);
+        return static_cast<U *>(p);
+    }
+};
+
+template <typename U>
+bool alloc_array(U **p, size_t count) {
+    if (cudaMalloc(p, (count > 0 ? count : 1) * sizeof(U)) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
+}
 
 }  // namespace sla

@@ -464,8 +464,11 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * first call builds (host synchronisation, device memory owned by the handle)
  * and which a stream capture cannot hold (SLA_ERR_UNSUPPORTED): call
  * sla_attention_prepare before capturing, and before asking for the workspace
- * size (0 until then).  Workspaces are 256-byte aligned; calls in flight at the
- * same time need distinct ones.
+ * size (0 until then).  It prepares what calls with `opts` need (its strides do
+ * not matter), or with NULL what any call needs.  Workspaces are 256-byte
+ * aligned; calls in flight at the same time need distinct ones.  With 16-bit
+ * types and dim a multiple of 16 up to 128, addresses and strides of the head
+ * tensors must be multiples of 16 bytes (SLA_ERR_INVALID otherwise).
  */
 typedef struct {
     int32_t dtype;            /* sla_dtype of q, k, v, out and their gradients */
@@ -478,7 +481,8 @@ typedef struct {
     int64_t v_stride[3];
     int64_t do_stride[3];     /* of dout (sla_attention_grad) */
 } sla_attn_opts;
-sla_status sla_attention_prepare(sla_csr_t h, int32_t backward, void *stream);
+sla_status sla_attention_prepare(sla_csr_t h, const sla_attn_opts *opts, int32_t backward,
+                                 void *stream);
 size_t sla_attention_workspace_bytes(sla_csr_t h, const sla_attn_opts *opts, int32_t backward);
 sla_status sla_attention(sla_csr_t h, const void *q, const void *k, const void *v, const void *vals,
                          void *out, void *out_wide, void *lse, const sla_attn_opts *opts, void *ws,

@@ -156,8 +156,14 @@ def test_a_bad_column_stays_in_its_rows(code, bad):
     hit = np.zeros(rp.shape[0] - 1, bool)
     hit[rows[ci == 100]] = True
     assert not np.isfinite(got[0][0, hit]).any()
-    assert np.array_equal(got[0][0, ~hit], clean[0][0, ~hit])
-    assert np.array_equal(got[1][0, ~hit], clean[1][0, ~hit])          # dq
+    # rows that share work with a bad one are summed entry by entry, in another order
+    # than otherwise: the bounds hold for any order, equal bits do not
+    res, err = attention(rp, ci, *(x[0].double().numpy() for x in (q, k, v)), None, 64 ** -0.5, do[0].double().numpy(),
+                         code)
+    for x, y in (("o", 0), ("dq", 1)):
+        assert within(got[y][0, ~hit], res[x][~hit], err[x][~hit]) <= 1.0
+    far = ~hit & (np.abs(np.arange(rp.shape[0] - 1) - 100) > 40)       # work items that hold no bad row
+    assert np.array_equal(got[0][0, far], clean[0][0, far]) and np.array_equal(got[1][0, far], clean[1][0, far])
 
 
 def test_lowest_finite_values_are_no_mask():

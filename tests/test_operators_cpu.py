@@ -17,7 +17,7 @@ def test_attention_argument_errors_need_no_gpu():
     assert lib.sla_attention(*null, ctypes.byref(opts), None, 0, None) == L.SLA_ERR_INVALID
     assert "NULL handle" in L.sla_last_error_string()
     assert lib.sla_attention_grad(*([None] * 12), ctypes.byref(opts), None, 0, None) == L.SLA_ERR_INVALID
-    assert lib.sla_attention_prepare(None, 1, None) == L.SLA_ERR_INVALID
+    assert lib.sla_attention_prepare(None, None, 1, None) == L.SLA_ERR_INVALID
     assert lib.sla_attention_workspace_bytes(None, ctypes.byref(opts), 0) == 0
 
 
