@@ -30,7 +30,7 @@ __global__ void unit_len_kernel(int n_rows, int rows, int n_units, const int32_t
 
 // Segments, slots (segments of split units) and split units of every unit.
 __global__ void unit_split_kernel(int n_units, int seg_len, const unsigned *__restrict__ len, unsigned *nseg,
-                                  unsigned *slots, unsigned *multi) {
+                                  unsigned *slots, unsigned *multi, unsigned *most) {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;
     if (u > n_units) return;
     unsigned n = 0;
@@ -38,6 +38,7 @@ __global__ void unit_split_kernel(int n_units, int seg_len, const unsigned *__re
     nseg[u] = n;
     slots[u] = n > 1 ? n : 0;
     multi[u] = n > 1 ? 1 : 0;
+    if (n > 1) atomicMax(most, n);
 }
 
 __global__ void unit_fill_kernel(int n_units, const unsigned *__restrict__ item0, const unsigned *__restrict__ slot0,
@@ -67,58 +68,55 @@ void free_plan(AttnPlan *p) {
     cudaFree(p->item_slot);
     cudaFree(p->multi_unit);
     cudaFree(p->multi_slot);
-    cudaFree(p->chunk_ptr);
-    cudaFree(p->cols);
-    cudaFree(p->bits);
-    cudaFree(p->row_start);
     *p = AttnPlan();
 }
 
-sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, int level, cudaStream_t s) {
-    const int n = transposed ? h->n_cols : h->n_rows;
-    const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr;
-    p->rows = rows;
-    p->n_units = (n + rows - 1) / rows;
+// Lengths of tiles in chunks.
+__global__ void tile_len_kernel(int n_units, const int32_t *__restrict__ chunk0, unsigned *len) {
+    const int u = blockIdx.x * blockDim.x + threadIdx.x;
+    if (u <= n_units) len[u] = u < n_units ? (unsigned)(chunk0[u + 1] - chunk0[u]) : 0u;
+}
+
+// Items of units with the lengths len (device, [n_units + 1]).  seg_len > 0: a
+// given segment length; else one that makes about `fill` items when the units
+// are few, and at least `least`.
+sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, cudaStream_t s) {
     const int U = p->n_units;
-    if (U == 0) {
-        p->built = true;
-        return SLA_OK;
-    }
     DeviceScratch tmp;
-    unsigned *len = tmp.get<unsigned>(U + 1), *sum = tmp.get<unsigned>(U + 1), *nseg = tmp.get<unsigned>(U + 1),
-             *slots = tmp.get<unsigned>(U + 1), *multi = tmp.get<unsigned>(U + 1);
-    void *ws = tmp.get<char>(scan_ws_bytes(U + 1));
-    if (!len || !sum || !nseg || !slots || !multi || !ws) {
+    unsigned *nseg = tmp.get<unsigned>((size_t)U + 1), *slots = tmp.get<unsigned>((size_t)U + 1),
+             *multi = tmp.get<unsigned>((size_t)U + 1);
+    void *ws = tmp.get<char>(scan_ws_bytes((int64_t)U + 1));
+    unsigned *most = tmp.get<unsigned>(1);
+    if (!nseg || !slots || !multi || !ws || !most) {
         set_error("attention plan: out of device memory");
         return SLA_ERR_OOM;
     }
-    unit_len_kernel<<<blocks_of(U + 1), 256, 0, s>>>(n, rows, U, rowptr, len);
-    SLA_CHECK_LAUNCH();
-    sla_status st = exclusive_scan(len, sum, U + 1, ws, s);
-    if (st != SLA_OK) return st;
-    unsigned total = 0;
-    SLA_CHECK_CUDA(cudaMemcpyAsync(&total, sum + U, sizeof total, cudaMemcpyDeviceToHost, s));
-    SLA_CHECK_CUDA(cudaStreamSynchronize(s));
-    // Enough segments to fill the GPU (16 an SM) when there are few units, none
-    // shorter than 64 entries: a shorter one spends more on its partial result
-    // than on its entries.  A level counts on 8 times as many systems and heads
-    // as the one before, so it splits 8 times less.
-    const int64_t fill = std::max<int64_t>(1, (int64_t)h->num_sms * 16 >> (3 * level));
-    const int64_t want = ((int64_t)total + fill - 1) / fill;
-    p->seg_len = (int32_t)std::max<int64_t>(64, (want + 15) / 16 * 16);
-    unit_split_kernel<<<blocks_of(U + 1), 256, 0, s>>>(U, p->seg_len, len, nseg, slots, multi);
+    sla_status st;
+    if (seg_len <= 0) {
+        unsigned total = 0;
+        st = exclusive_scan(len, nseg, (int64_t)U + 1, ws, s);
+        if (st != SLA_OK) return st;
+        SLA_CHECK_CUDA(cudaMemcpyAsync(&total, nseg + U, sizeof total, cudaMemcpyDeviceToHost, s));
+        SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+        seg_len = (int)std::max<int64_t>(least, ((int64_t)total + fill - 1) / fill);
+    }
+    p->seg_len = seg_len;
+    SLA_CHECK_CUDA(cudaMemsetAsync(most, 0, sizeof(unsigned), s));
+    unit_split_kernel<<<blocks_of((int64_t)U + 1), 256, 0, s>>>(U, seg_len, len, nseg, slots, multi, most);
     SLA_CHECK_LAUNCH();
     unsigned *vec[3] = {nseg, slots, multi};
-    unsigned tot[3] = {0, 0, 0};
+    unsigned tot[4] = {0, 0, 0, 1};
     for (int i = 0; i < 3; ++i) {
-        st = exclusive_scan(vec[i], vec[i], U + 1, ws, s);
+        st = exclusive_scan(vec[i], vec[i], (int64_t)U + 1, ws, s);
         if (st != SLA_OK) return st;
         SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[i], vec[i] + U, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
     }
+    SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[3], most, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
     p->n_items = (int32_t)tot[0];
     p->n_slots = (int32_t)tot[1];
     p->n_multi = (int32_t)tot[2];
+    p->most_segs = (int32_t)tot[3];
     if (p->n_multi > 0) {
         if (!alloc_array(&p->item_unit, tot[0]) || !alloc_array(&p->item_seg, tot[0]) ||
             !alloc_array(&p->item_slot, tot[0]) || !alloc_array(&p->multi_unit, tot[2]) ||
@@ -126,17 +124,68 @@ sla_status build_plan(Csr *h, AttnPlan *p, int rows, bool transposed, int level,
             set_error("attention plan: out of device memory");
             return SLA_ERR_OOM;
         }
-        unit_fill_kernel<<<blocks_of(U + 1), 256, 0, s>>>(U, nseg, slots, multi, p->item_unit, p->item_seg,
-                                                          p->item_slot, p->multi_unit, p->multi_slot);
+        unit_fill_kernel<<<blocks_of((int64_t)U + 1), 256, 0, s>>>(U, nseg, slots, multi, p->item_unit, p->item_seg,
+                                                                   p->item_slot, p->multi_unit, p->multi_slot);
+        SLA_CHECK_LAUNCH();
+        SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+    }
+    return SLA_OK;
+}
+
+// Enough items to fill the GPU when there are few units (16 an SM), but none
+// shorter than 64 entries or columns: a shorter one spends more on its partial
+// result than on its entries.  A level counts on 8 times as many systems and
+// heads as the one before, so it splits 8 times less.
+int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 16 >> (3 * level)); }
+
+// All levels of one direction's row plans (tiled == false) or its tiles and
+// their plans.  The lengths are the same for every level.
+sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
+    AttnPlan *p = &(tiled ? h->attn->tile : h->attn->row)[transposed][level];
+    AttnTiles *tiles = &h->attn->tiles[transposed];
+    const int n = transposed ? h->n_cols : h->n_rows;
+    const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr, *colind = transposed ? h->colindT : h->colind;
+    p->rows = tiled ? kTileRows : 1;
+    p->n_units = (n + p->rows - 1) / p->rows;
+    const int U = p->n_units;
+    if (U == 0) {
+        p->built = true;
+        return SLA_OK;
+    }
+    DeviceScratch tmp;
+    unsigned *len = tmp.get<unsigned>((size_t)U + 1);
+    if (!len) {
+        set_error("attention plan: out of device memory");
+        return SLA_ERR_OOM;
+    }
+    const unsigned grid = blocks_of((int64_t)U + 1);
+    if (!tiled || !tiles->built) {
+        unit_len_kernel<<<grid, 256, 0, s>>>(n, p->rows, U, rowptr, len);
         SLA_CHECK_LAUNCH();
     }
-    if (rows == kTileRows) {
-        st = build_tiles(p, n, rowptr, transposed ? h->colindT : h->colind, s);
-        if (st != SLA_OK) return st;
+    sla_status st;
+    if (tiled) {
+        if (!tiles->built) {
+            // columns are gathered by parts of 256 entries of a tile's longest row
+            AttnPlan parts;
+            parts.n_units = U;
+            st = build_items(&parts, len, 256, 0, 0, s);
+            if (st == SLA_OK) st = build_tiles(tiles, parts, n, rowptr, colind, s);
+            free_plan(&parts);
+            if (st != SLA_OK) return st;
+        }
+        tile_len_kernel<<<grid, 256, 0, s>>>(U, tiles->chunk0, len);
+        SLA_CHECK_LAUNCH();
     }
-    SLA_CHECK_CUDA(cudaStreamSynchronize(s));
-    p->built = true;
-    return SLA_OK;
+    st = build_items(p, len, 0, fill_of(h, level), tiled ? 64 / 16 : 64, s);
+    if (st == SLA_OK) p->built = true;
+    return st;
+}
+
+void free_tiles(AttnTiles *t) {
+    cudaFree(t->chunk0);
+    cudaFree(t->chunks);
+    *t = AttnTiles();
 }
 
 sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
@@ -144,13 +193,14 @@ sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStrea
     if (p->built) return SLA_OK;
     sla_status st = SLA_ERR_OOM;
     try {
-        st = build_plan(h, p, tiled ? kTileRows : 1, transposed, level, s);
+        st = build_plans(h, tiled, transposed, level, s);
     } catch (const std::bad_alloc &) {
         set_error("sla_attention_prepare: out of host memory");
     }
     if (st != SLA_OK) {
         cudaStreamSynchronize(s);
         free_plan(p);
+        if (!h->attn->tiles[transposed].built) free_tiles(&h->attn->tiles[transposed]);
     }
     return st;
 }
@@ -164,10 +214,11 @@ void use_plan(AttnArgs &a, const AttnPlan &p) {
     a.item_unit = p.item_unit;
     a.item_seg = p.item_seg;
     a.item_slot = p.item_slot;
-    a.chunk_ptr = p.chunk_ptr;
-    a.cols = p.cols;
-    a.bits = p.bits;
-    a.row_start = p.row_start;
+}
+
+static void use_tiles(AttnArgs &a, const AttnTiles &t) {
+    a.chunk0 = t.chunk0;
+    a.chunks = t.chunks;
 }
 
 void free_attn_plans(Csr *h) {
@@ -177,6 +228,7 @@ void free_attn_plans(Csr *h) {
             free_plan(&h->attn->row[t][l]);
             free_plan(&h->attn->tile[t][l]);
         }
+    for (AttnTiles &t : h->attn->tiles) free_tiles(&t);
     delete h->attn;
     h->attn = nullptr;
 }
@@ -371,43 +423,93 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const AttnA
     }
 }
 
-// Joins the segments of split rows: one warp a (system, split unit, row, head).
-template <typename T>
-__global__ void __launch_bounds__(kAttnThreads)
+// Joins the segments of split rows: a block of W warps a (system, split unit,
+// row, head).  A lane holds the elements lane + 32 i of the head; the warps take
+// the segments in turn, 4 at a time with their loads in flight together, and
+// are added up in order.
+template <typename A, int W>
+__device__ __forceinline__ A join_block(A v, A *red, bool take_max) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const A u = __shfl_xor_sync(0xffffffffu, v, o);
+        v = take_max ? fmax(v, u) : v + u;
+    }
+    if constexpr (W > 1) {
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v = take_max ? fmax(v, red[w]) : v + red[w];
+    }
+    return v;
+}
+
+struct JoinAt { int b, h, r, s0, n; int64_t row; };
+__device__ __forceinline__ bool join_at(JoinAt &j, int64_t w, int n_rows, int rows, int heads, int n_multi,
+                                        const int32_t *multi_unit, const int32_t *multi_slot) {
+    j.h = (int)(w % heads);
+    j.r = (int)(w / heads % rows);
+    const int mu = (int)(w / heads / rows % n_multi);
+    j.b = (int)(w / heads / rows / n_multi);
+    j.row = (int64_t)__ldg(multi_unit + mu) * rows + j.r;
+    j.s0 = __ldg(multi_slot + mu);
+    j.n = __ldg(multi_slot + mu + 1) - j.s0;
+    return j.row < n_rows;
+}
+
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * W)
 attn_join_kernel(const AttnArgs a, int rows, int n_multi, const int32_t *__restrict__ multi_unit,
                  const int32_t *__restrict__ multi_slot) {
     using A = typename AccOf<T>::type;
-    const int64_t w = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (w >= (int64_t)a.batch * n_multi * rows * a.heads) return;
-    const int h = (int)(w % a.heads), r = (int)(w / a.heads % rows);
-    const int mu = (int)(w / a.heads / rows % n_multi);
-    const int b = (int)(w / a.heads / rows / n_multi);
-    const int64_t row = (int64_t)__ldg(multi_unit + mu) * rows + r;
-    if (row >= a.n_rows) return;
-    const int s0 = __ldg(multi_slot + mu), n = __ldg(multi_slot + mu + 1) - s0;
+    __shared__ A red[W];
+    __shared__ A sums[W > 1 ? W : 1][W > 1 ? 256 : 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    JoinAt j;
+    if (!join_at(j, blockIdx.x, a.n_rows, rows, a.heads, n_multi, multi_unit, multi_slot)) return;
     const int64_t step = (int64_t)rows * a.heads * (a.dim + 2);
-    const A *p = static_cast<const A *>(a.part) + part_index(s0, a.n_slots, b, rows, r, a.heads, h) * (a.dim + 2);
+    const A *p = static_cast<const A *>(a.part) + part_index(j.s0, a.n_slots, j.b, rows, j.r, a.heads, j.h) * (a.dim + 2);
     const A none = neg_inf<A>();
-    A m = none;
-    for (int s = lane; s < n; s += 32) m = fmax(m, p[s * step + a.dim]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    A m = none, l = (A)0;
+    for (int s = threadIdx.x; s < j.n; s += 32 * W) m = fmax(m, p[s * step + a.dim]);
+    m = join_block<A, W>(m, red, true);
     const A ref = m == none ? (A)0 : m;
-    A l = (A)0;
-    for (int s = lane; s < n; s += 32) l += p[s * step + a.dim + 1] * exp_acc(p[s * step + a.dim] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int s = threadIdx.x; s < j.n; s += 32 * W) l += p[s * step + a.dim + 1] * exp_acc(p[s * step + a.dim] - ref);
+    l = join_block<A, W>(l, red, false);
     const A inv = l > (A)0 || l != l ? (A)1 / l : (A)0;
-    const int64_t at = ((int64_t)b * a.n_rows + row) * a.heads + h;
-    for (int d = lane; d < a.dim; d += 32) {
-        A x = (A)0;
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) x += p[s * step + d] * exp_acc(p[s * step + a.dim] - ref);
-        static_cast<T *>(a.out)[at * a.dim + d] = from_acc<T>(x * inv);
-        if (a.wide) static_cast<A *>(a.wide)[at * a.dim + d] = x * inv;
+    A x[8] = {};
+    for (int s = warp; s < j.n; s += 4 * W) {
+        A w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w[u] = s + u * W < j.n ? exp_acc(p[(s + u * W) * step + a.dim] - ref) : (A)0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i * 32 + lane < a.dim)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (s + u * W < j.n) x[i] = fma(w[u], p[(s + u * W) * step + i * 32 + lane], x[i]);
     }
-    if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[warp][i * 32 + lane] = x[i];
+        __syncthreads();
+    }
+    const int64_t at = ((int64_t)j.b * a.n_rows + j.row) * a.heads + j.h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int d = i * 32 + lane;
+        if (d >= a.dim || i % W != warp) continue;
+        A y = x[i];
+        if constexpr (W > 1) {
+            y = sums[0][d];
+#pragma unroll
+            for (int w = 1; w < W; ++w) y += sums[w][d];
+        }
+        static_cast<T *>(a.out)[at * a.dim + d] = from_acc<T>(y * inv);
+        if (a.wide) static_cast<A *>(a.wide)[at * a.dim + d] = y * inv;
+    }
+    if (threadIdx.x == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
 }
 
 // Gradients by A's rows: p and ds of every entry and head, and dq.
@@ -550,30 +652,36 @@ __global__ void __launch_bounds__(kAttnThreads) attn_bwd_cols_kernel(const AttnA
 
 // out0 (and out1) of split rows: the segments' sums added in order, `width`
 // elements a partial, the first `dim` for out0, the next for out1.
-template <typename T>
-__global__ void __launch_bounds__(kAttnThreads)
-attn_join_sums_kernel(const typename AccOf<T>::type *__restrict__ part, int n_rows, int batch, int n_slots, int rows,
+template <typename T, int W>
+__global__ void __launch_bounds__(32 * W)
+attn_join_sums_kernel(const typename AccOf<T>::type *__restrict__ part, int n_rows, int n_slots, int rows,
                       int heads, int dim, int width, int n_multi, const int32_t *__restrict__ multi_unit,
                       const int32_t *__restrict__ multi_slot, T *out0, T *out1) {
     using A = typename AccOf<T>::type;
-    const int64_t w = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31;
-    if (w >= (int64_t)batch * n_multi * rows * heads) return;
-    const int h = (int)(w % heads), r = (int)(w / heads % rows);
-    const int mu = (int)(w / heads / rows % n_multi);
-    const int b = (int)(w / heads / rows / n_multi);
-    const int64_t row = (int64_t)__ldg(multi_unit + mu) * rows + r;
-    if (row >= n_rows) return;
-    const int s0 = __ldg(multi_slot + mu), n = __ldg(multi_slot + mu + 1) - s0;
+    __shared__ A sums[W > 1 ? W : 1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    JoinAt j;
+    if (!join_at(j, blockIdx.x, n_rows, rows, heads, n_multi, multi_unit, multi_slot)) return;
     const int64_t step = (int64_t)rows * heads * width;
-    const A *p = part + part_index(s0, n_slots, b, rows, r, heads, h) * width;
-    const int64_t at = (((int64_t)b * n_rows + row) * heads + h) * dim;
-    for (int d = lane; d < width; d += 32) {
+    const A *p = part + part_index(j.s0, n_slots, j.b, rows, j.r, heads, j.h) * width;
+    const int64_t at = (((int64_t)j.b * n_rows + j.row) * heads + j.h) * dim;
+    for (int d0 = 0; d0 < width; d0 += 32) {
+        const int d = d0 + lane;
         A x = (A)0;
-#pragma unroll 4
-        for (int s = 0; s < n; ++s) x += p[s * step + d];
+        if (d < width) {
+#pragma unroll 8
+            for (int s = warp; s < j.n; s += W) x += p[s * step + d];
+        }
+        if constexpr (W > 1) {
+            __syncthreads();
+            sums[warp][lane] = x;
+            __syncthreads();
+            x = sums[0][lane];
+#pragma unroll
+            for (int w = 1; w < W; ++w) x += sums[w][lane];
+        }
         T *out = d < dim ? out0 : out1;
-        if (out) out[at + (d < dim ? d : d - dim)] = from_acc<T>(x);
+        if (out && d < width && warp == 0) out[at + (d < dim ? d : d - dim)] = from_acc<T>(x);
     }
 }
 
@@ -602,12 +710,18 @@ attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__rest
 
 }  // namespace
 
+// One warp a joined row while segments are few (one batch of loads each), else 8.
+constexpr int kJoinFew = 8;
+
 template <typename T>
 sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s) {
-    if (p.n_multi == 0) return SLA_OK;
-    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * a.heads;
-    attn_join_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit,
-                                                                                    p.multi_slot);
+    const int64_t blocks = (int64_t)a.batch * p.n_multi * p.rows * a.heads;
+    SLA_REQUIRE(blocks < INT_MAX, "sla_attention: too many split rows, systems and heads");
+    if (blocks == 0) return SLA_OK;
+    if (p.most_segs <= kJoinFew)
+        attn_join_kernel<T, 1><<<(unsigned)blocks, 32, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit, p.multi_slot);
+    else
+        attn_join_kernel<T, 8><<<(unsigned)blocks, 256, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit, p.multi_slot);
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }
@@ -615,11 +729,17 @@ sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s) {
 template <typename T>
 sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int heads, int width, void *out0, void *out1,
                           cudaStream_t s) {
-    if (p.n_multi == 0) return SLA_OK;
-    const int64_t warps = (int64_t)a.batch * p.n_multi * p.rows * heads;
-    attn_join_sums_kernel<T><<<blocks_of(warps * 32, kAttnThreads), kAttnThreads, 0, s>>>(
-        static_cast<const typename AccOf<T>::type *>(a.part), n_rows, a.batch, p.n_slots, p.rows, heads, a.dim, width,
-        p.n_multi, p.multi_unit, p.multi_slot, static_cast<T *>(out0), static_cast<T *>(out1));
+    const int64_t blocks = (int64_t)a.batch * p.n_multi * p.rows * heads;
+    SLA_REQUIRE(blocks < INT_MAX, "sla_attention: too many split rows, systems and heads");
+    if (blocks == 0) return SLA_OK;
+    const auto *part = static_cast<const typename AccOf<T>::type *>(a.part);
+    T *o0 = static_cast<T *>(out0), *o1 = static_cast<T *>(out1);
+    if (p.most_segs <= kJoinFew)
+        attn_join_sums_kernel<T, 1><<<(unsigned)blocks, 32, 0, s>>>(part, n_rows, p.n_slots, p.rows, heads, a.dim, width,
+                                                                    p.n_multi, p.multi_unit, p.multi_slot, o0, o1);
+    else
+        attn_join_sums_kernel<T, 8><<<(unsigned)blocks, 256, 0, s>>>(part, n_rows, p.n_slots, p.rows, heads, a.dim, width,
+                                                                     p.n_multi, p.multi_unit, p.multi_slot, o0, o1);
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }
@@ -670,9 +790,10 @@ bool on_16_bytes(const void *p, const int64_t st[3], size_t size) {
 size_t acc_size(int32_t dt) { return dt == SLA_F64 ? 8 : 4; }
 
 template <typename T>
-sla_status attn_forward(const AttnPlan &p, AttnArgs a, bool tiled, cudaStream_t s) {
+sla_status attn_forward(const Csr *h, const AttnPlan &p, AttnArgs a, bool tiled, cudaStream_t s) {
     using A = typename AccOf<T>::type;
     use_plan(a, p);
+    use_tiles(a, h->attn->tiles[0]);
     sla_status st;
     if constexpr (sizeof(T) == 2) {
         if (tiled) {
@@ -712,6 +833,7 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
                      on_16_bytes(a.dq, dense, sizeof(T)) && on_16_bytes(a.dk, dense, sizeof(T)) &&
                      on_16_bytes(a.dv, dense, sizeof(T));
     use_plan(a, p);
+    use_tiles(a, h->attn->tiles[0]);
     sla_status st;
     if constexpr (sizeof(T) == 2) st = tiled ? attn_tile_bwd_rows<T>(a, s) : launch_rows_of<T>(kBwdRows, a, vec, s);
     else st = launch_rows_of<T>(kBwdRows, a, vec, s);
@@ -723,6 +845,7 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
     }
     if (!a.dk && !a.dv) return SLA_OK;
     use_plan(a, pt);
+    use_tiles(a, h->attn->tiles[1]);
     a.rowptr = h->rowptrT;
     a.colind = h->colindT;
     a.perm = h->permT;
@@ -824,7 +947,10 @@ sla_status check_tiled(const char *fn, const sla_attn_opts *o, std::initializer_
     if (!attn_tiled(o)) return SLA_OK;
     bool ok = true;
     for (const void *p : dense) ok = ok && ((uintptr_t)p & 15) == 0;
-    for (const auto &x : strided) ok = ok && on_16_bytes(x.first, x.second, 2);
+    for (const auto &x : strided) {
+        ok = ok && on_16_bytes(x.first, x.second, 2);
+        SLA_REQUIRE(x.second[1] >= 0 && x.second[1] < (int64_t)1 << 31, "%s: row strides must be below 2^31 elements", fn);
+    }
     SLA_REQUIRE(ok, "%s: 16-bit heads of a multiple of 16 elements need addresses and strides of a multiple of 16 bytes",
                 fn);
     return SLA_OK;
@@ -906,10 +1032,10 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     const AttnPlan &p = plan_of(h, o, false);
     const bool tiled = attn_tiled(o);
     switch (o->dtype) {
-        case SLA_F64: return attn_forward<double>(p, a, tiled, s);
-        case SLA_F32: return attn_forward<float>(p, a, tiled, s);
-        case SLA_BF16: return attn_forward<__nv_bfloat16>(p, a, tiled, s);
-        default: return attn_forward<__half>(p, a, tiled, s);
+        case SLA_F64: return attn_forward<double>(h, p, a, tiled, s);
+        case SLA_F32: return attn_forward<float>(h, p, a, tiled, s);
+        case SLA_BF16: return attn_forward<__nv_bfloat16>(h, p, a, tiled, s);
+        default: return attn_forward<__half>(h, p, a, tiled, s);
     }
 }
 

@@ -20,22 +20,28 @@
 namespace sla {
 
 // Work items of one direction of a pattern: a unit is `rows` consecutive rows;
-// a unit whose longest row has more than seg_len entries is split into several
-// items (segments), whose partial results a second kernel joins.  Null item
-// arrays: item == unit, one segment each.
+// a unit longer than seg_len (entries of its row; chunks of its tile) is split
+// into several items (segments), whose partial results a second kernel joins.
+// Null item arrays: item == unit, one segment each.
 struct AttnPlan {
     bool built = false;
-    int32_t rows = 1, n_units = 0, n_items = 0, n_slots = 0, n_multi = 0, seg_len = 0;
+    int32_t rows = 1, n_units = 0, n_items = 0, n_slots = 0, n_multi = 0, seg_len = 0, most_segs = 1;
     int32_t *item_unit = nullptr, *item_seg = nullptr, *item_slot = nullptr;   // [n_items]
     int32_t *multi_unit = nullptr;                                             // [n_multi]
     int32_t *multi_slot = nullptr;                                             // [n_multi + 1]
-    // Tiles (rows == kTileRows): the columns any row of the item stores, in
-    // increasing order, 16 to a chunk (the last one padded with its last column),
-    // and for every row of a chunk the bits of the columns it stores.
-    int32_t *chunk_ptr = nullptr;                                              // [n_items + 1]
-    int32_t *cols = nullptr;                                                   // [n_chunks * 16]
-    uint16_t *bits = nullptr;                                                  // [n_chunks * 16]
-    int32_t *row_start = nullptr;      // [n_items * 16]: first entry of each row in the item
+};
+
+// The tiles (kTileRows rows each) of one direction: the columns that any row of
+// the tile stores, in increasing order, 16 to a chunk.
+struct AttnTiles {
+    bool built = false;
+    int32_t *chunk0 = nullptr;         // [n_units + 1]: first chunk of each tile
+    struct TileChunk *chunks = nullptr;
+};
+struct TileChunk {
+    int32_t col[16];                   // a tile's last chunk is padded with valid columns
+    uint16_t bits[16];                 // row r: the columns it stores
+    int32_t start[16];                 // row r: its first entry in this chunk
 };
 
 constexpr int kTileRows = 16;
@@ -46,6 +52,7 @@ constexpr int kAttnLevels = 3;
 struct AttnPlans {
     AttnPlan row[2][kAttnLevels];      // one row a unit: A, A^T
     AttnPlan tile[2][kAttnLevels];     // kTileRows rows a unit
+    AttnTiles tiles[2];
 };
 
 inline int attn_level(const Csr *h, const sla_attn_opts *o) {
@@ -66,8 +73,8 @@ struct AttnArgs {
     const int32_t *rowptr, *colind, *perm;
     int32_t n_items, n_slots, seg_len;
     const int32_t *item_unit, *item_seg, *item_slot;
-    const int32_t *chunk_ptr, *cols, *row_start;
-    const uint16_t *bits;
+    const int32_t *chunk0;                 // tiles
+    const TileChunk *chunks;
     const void *q, *k, *v, *o, *dout;
     int64_t qs[3], ks[3], vs[3], ds[3];    // system, row, head
     const void *vals;
@@ -153,7 +160,8 @@ sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int 
                           cudaStream_t s);
 
 // Tile kernels (sla_attention_tile.cu): plan arrays of a tile plan, and the calls.
-sla_status build_tiles(AttnPlan *p, int n_rows, const int32_t *rowptr, const int32_t *colind, cudaStream_t s);
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
+                       cudaStream_t s);
 template <typename T> sla_status attn_tile_forward(const AttnArgs &a, cudaStream_t s);
 template <typename T> sla_status attn_tile_bwd_rows(const AttnArgs &a, cudaStream_t s);
 template <typename T> sla_status attn_tile_bwd_cols(const AttnArgs &a, cudaStream_t s);

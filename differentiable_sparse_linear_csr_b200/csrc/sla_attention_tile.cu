@@ -39,34 +39,37 @@ constexpr int kTileThreads = 32 * kTileWarps;
 constexpr unsigned kAll = 0xffffffffu;
 
 // ----------------------------------------------------------------- plan ----
-// One warp an item; lane r < 16 walks row r's entries in the item's range of
-// columns, and the smallest column any row is at is the next one.
+// One warp a part of a tile: the columns from one entry of the tile's longest
+// row to the entry seg_len further on.  Lane r < 16 walks row r's entries
+// there, and the smallest column any row is at is the next one.  FILL == false
+// counts the columns; FILL writes them, at[part] columns after the first part's.
 template <bool FILL>
 __global__ void __launch_bounds__(128)
-tile_columns_kernel(int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_items,
-                    int seg_len, const int32_t *__restrict__ item_unit, const int32_t *__restrict__ item_seg,
-                    unsigned *chunks, const int32_t *__restrict__ chunk_ptr, int32_t *cols, uint16_t *bits,
-                    int32_t *row_start) {
-    const int it = (blockIdx.x * 128 + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-    if (it > n_items) return;
-    if (it == n_items) {
-        if (!FILL && lane == 0) chunks[it] = 0;
+tile_columns_kernel(int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_parts,
+                    int seg_len, const int32_t *__restrict__ part_unit, const int32_t *__restrict__ part_seg,
+                    unsigned *count, const unsigned *__restrict__ at, const int32_t *__restrict__ chunk0,
+                    TileChunk *chunks) {
+    const int part = (int)((blockIdx.x * (int64_t)128 + threadIdx.x) >> 5), lane = threadIdx.x & 31;
+    if (part > n_parts) return;
+    if (part == n_parts) {
+        if (!FILL && lane == 0) count[part] = 0;
         return;
     }
-    const int unit = item_unit ? item_unit[it] : it, seg = item_seg ? item_seg[it] : 0;
+    const int unit = part_unit ? part_unit[part] : part, seg = part_seg ? part_seg[part] : 0;
     const int64_t row = (int64_t)unit * kTileRows + lane;
     int t0 = 0, t1 = 0;
     if (lane < kTileRows && row < n_rows) {
         t0 = rowptr[row];
         t1 = rowptr[row + 1];
     }
-    if (item_unit) {
-        // the segment's columns: from the longest row's entry seg * seg_len on
+    bool last = true;
+    if (part_unit) {
         const int len = t1 - t0, most = __reduce_max_sync(kAll, len);
         const int who = __ffs(__ballot_sync(kAll, len == most)) - 1;
         const int b0 = __shfl_sync(kAll, t0, who);
         const int64_t e0 = (int64_t)seg * seg_len, e1 = e0 + seg_len;
         const int lo = seg == 0 ? 0 : colind[b0 + e0], hi = e1 < most ? colind[b0 + e1] : INT_MAX;
+        last = hi == INT_MAX;
         auto first_at = [&](int c) {            // first entry of the row with a column >= c
             int a = t0, b = t1;
             while (a < b) {
@@ -80,36 +83,49 @@ tile_columns_kernel(int n_rows, const int32_t *__restrict__ rowptr, const int32_
         t0 = a;
         t1 = b;
     }
-    if (FILL && lane < kTileRows) row_start[(int64_t)it * kTileRows + lane] = t0;
-    int cur = t0 < t1 ? colind[t0] : INT_MAX, next = t0 + 1 < t1 ? colind[t0 + 1] : INT_MAX, t = t0 + 2;
-    int n = 0, mine = 0;
-    unsigned row_bits = 0;
-    int64_t at = FILL ? (int64_t)chunk_ptr[it] * kTileRows + lane : 0;
+    int cur = t0 < t1 ? colind[t0] : INT_MAX, next = t0 + 1 < t1 ? colind[t0 + 1] : INT_MAX, t = t0;
+    const unsigned n0 = FILL ? at[part] - at[part - seg] : 0;
+    unsigned n = n0, row_bits = 0;
+    int mine = 0, first = (int)(n0 & 15);       // places [first, n & 15) of the current chunk are this part's
+    TileChunk *ck = FILL ? chunks + chunk0[unit] + (n0 >> 4) : nullptr;
+    auto flush = [&](int end) {
+        if (lane >= first && lane < end) ck->col[lane] = mine;
+        // two rows a word; neighbouring parts may share a chunk
+        if (lane < kTileRows && row_bits)
+            atomicOr(reinterpret_cast<unsigned *>(ck->bits) + (lane >> 1), row_bits << (16 * (lane & 1)));
+        row_bits = 0;
+        first = 0;
+        ++ck;
+    };
     for (;;) {
         const int c = __reduce_min_sync(kAll, cur);
         if (c == INT_MAX) break;
+        const int place = (int)(n & 15);
+        if (FILL && place == 0 && lane < kTileRows) ck->start[lane] = t;
         if (cur == c) {
-            row_bits |= 1u << (n & 15);
+            row_bits |= 1u << place;
             cur = next;
-            next = t < t1 ? colind[t] : INT_MAX;
             ++t;
+            next = t + 1 < t1 ? colind[t + 1] : INT_MAX;
         }
-        if (lane >= (n & 15)) mine = c;          // later places hold the last column until they get theirs
+        if (lane >= place) mine = c;            // later places hold the last column until they get theirs
         ++n;
-        if ((n & 15) == 0) {
-            if (FILL && lane < kTileRows) {
-                cols[at] = mine;
-                bits[at] = (uint16_t)row_bits;
-                at += kTileRows;
-            }
-            row_bits = 0;
-        }
+        if (FILL && place == 15) flush(16);
     }
-    if (FILL && (n & 15) && lane < kTileRows) {
-        cols[at] = mine;
-        bits[at] = (uint16_t)row_bits;
-    }
-    if (!FILL && lane == 0) chunks[it] = (unsigned)((n + 15) / 16);
+    if (FILL && (n & 15) && n > n0) flush(last ? 16 : (int)(n & 15));
+    if (!FILL && lane == 0) count[part] = n;
+}
+
+// Chunks of each tile, from its parts' columns.
+__global__ void tile_chunks_kernel(int n_units, int n_parts, const unsigned *__restrict__ at,
+                                   const int32_t *__restrict__ part_unit, const int32_t *__restrict__ part_seg,
+                                   unsigned *chunks) {
+    const int part = blockIdx.x * blockDim.x + threadIdx.x;
+    if (part == 0) chunks[n_units] = 0;
+    if (part >= n_parts) return;
+    const int unit = part_unit ? part_unit[part] : part, seg = part_seg ? part_seg[part] : 0;
+    if (part + 1 < n_parts && part_seg && part_seg[part + 1] > seg) return;    // not the tile's last part
+    chunks[unit] = (at[part + 1] - at[part - seg] + 15) / 16;
 }
 
 // ------------------------------------------------------------ operands ----
@@ -198,6 +214,24 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 }
 
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
+
+// The main loops hold scores in units of log 2, so that a weight is one
+// exponential of a difference (the hardware's: 2 ulp, results below 2^-126 are
+// zero, which a softmax does not notice).
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// A stored value in those units; a finite one stays finite.
+__device__ __forceinline__ float value_log2(float x) {
+    constexpr float kMost = 2.3e38f;
+    if (x > kMost && x <= FLT_MAX) x = kMost;
+    if (x < -kMost && x >= -FLT_MAX) x = -kMost;
+    return x * kLog2e;
+}
+
 
 // The tile's own 16 rows as the left operand of score products.
 template <int D>
@@ -308,52 +342,74 @@ struct Sums {
     }
 };
 
-// A warp's work: item `it` of the plan, one head of one system.
+// A warp's work: chunks [ch0, ch1) of a tile, one head of one system.
 struct TileWork {
-    int64_t it, row0;
+    int64_t row0;
     int b, h, kh, slot;
-    int ch0, ch1;
+    const TileChunk *ch0, *ch1;
 };
 
-__device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, int64_t x, int64_t y, int share) {
-    if (x >= (int64_t)a.n_items * share) return false;
-    w.it = x / share;
-    w.kh = (int)(y % a.kv_heads);
-    w.b = (int)(y / a.kv_heads);
-    w.h = w.kh * (a.heads / a.kv_heads) + (int)(x % share);
-    w.row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + w.it) : (int)w.it) * kTileRows;
-    w.slot = a.item_unit ? __ldg(a.item_slot + w.it) : -1;
-    w.ch0 = __ldg(a.chunk_ptr + w.it);
-    w.ch1 = __ldg(a.chunk_ptr + w.it + 1);
+__device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, unsigned x, unsigned y, unsigned share) {
+    const unsigned it = x / share;
+    if (it >= (unsigned)a.n_items) return false;
+    w.b = (int)(y / (unsigned)a.kv_heads);
+    w.kh = (int)(y - (unsigned)w.b * a.kv_heads);
+    w.h = w.kh * (a.heads / a.kv_heads) + (int)(x - it * share);
+    int unit = (int)it, seg = 0;
+    w.slot = -1;
+    if (a.item_unit) {
+        unit = __ldg(a.item_unit + it);
+        seg = __ldg(a.item_seg + it);
+        w.slot = __ldg(a.item_slot + it);
+    }
+    w.row0 = (int64_t)unit * kTileRows;
+    const int c0 = __ldg(a.chunk0 + unit), c1 = __ldg(a.chunk0 + unit + 1);
+    const int64_t from = (int64_t)c0 + (int64_t)seg * a.seg_len, to = from + a.seg_len;
+    w.ch0 = a.chunks + from;
+    w.ch1 = a.chunks + (to < c1 ? to : (int64_t)c1);
     return true;
 }
 
 // What a thread needs of a chunk: the columns it reads for the scores (g and
-// 8 + g) and for the sums (8 blk + 2c, + 1), and rows g's and g + 8's bits.
+// 8 + g) and for the sums (8 blk + 2c, + 1), rows g's and g + 8's bits, and
+// with ENTRIES the first entry of those rows.
+template <bool ENTRIES>
 struct Chunk {
-    int kc[2], vc[4];
-    unsigned bits[2];
-    __device__ __forceinline__ void load(const AttnArgs &a, int ch, int g, int c, int n_cols) {
-        const int32_t *p = a.cols + (int64_t)ch * 16;
-        const uint16_t *q = a.bits + (int64_t)ch * 16;
-        kc[0] = __ldg(p + g);
-        kc[1] = __ldg(p + 8 + g);
-        const int2 x = __ldg(reinterpret_cast<const int2 *>(p) + c), y = __ldg(reinterpret_cast<const int2 *>(p) + 4 + c);
-        vc[0] = x.x;
-        vc[1] = x.y;
-        vc[2] = y.x;
-        vc[3] = y.y;
-        bits[0] = __ldg(q + g);
-        bits[1] = __ldg(q + 8 + g);
+    unsigned kc[2], vc[4], bits[2];
+    int at[2];
+    __device__ __forceinline__ void load(const TileChunk *p, int g, int c, int n_cols) {
+        kc[0] = (unsigned)__ldg(p->col + g);
+        kc[1] = (unsigned)__ldg(p->col + 8 + g);
+        const int2 x = __ldg(reinterpret_cast<const int2 *>(p->col) + c);
+        const int2 y = __ldg(reinterpret_cast<const int2 *>(p->col) + 4 + c);
+        vc[0] = (unsigned)x.x;
+        vc[1] = (unsigned)x.y;
+        vc[2] = (unsigned)y.x;
+        vc[3] = (unsigned)y.y;
+        bits[0] = __ldg(p->bits + g);
+        bits[1] = __ldg(p->bits + 8 + g);
+        if constexpr (ENTRIES) {
+            at[0] = __ldg(p->start + g);
+            at[1] = __ldg(p->start + 8 + g);
+        }
 #if SLA_DEBUG_BOUNDS
-        kc[0] = SLA_IDX(kc[0], n_cols, kBndColumn);
-        kc[1] = SLA_IDX(kc[1], n_cols, kBndColumn);
-        for (int i = 0; i < 4; ++i) vc[i] = SLA_IDX(vc[i], n_cols, kBndColumn);
+        for (int i = 0; i < 2; ++i) kc[i] = (unsigned)SLA_IDX((int)kc[i], n_cols, kBndColumn);
+        for (int i = 0; i < 4; ++i) vc[i] = (unsigned)SLA_IDX((int)vc[i], n_cols, kBndColumn);
 #else
         (void)n_cols;
 #endif
     }
+    // Entry of row g + 8 i at position pos (if the row stores it).
+    __device__ __forceinline__ int entry(int i, int pos) const {
+        return at[i] + __popc(bits[i] & ((1u << pos) - 1u));
+    }
 };
+
+// Row `col` of a tensor with rows `bytes` apart (below 2^32: one multiply-add).
+template <typename T>
+__device__ __forceinline__ const void *row_at(const T *base, unsigned col, unsigned bytes) {
+    return reinterpret_cast<const char *>(base) + (uint64_t)col * bytes;
+}
 
 // Zeros for the gathered rows of the columns that no row of the tile uses; used:
 // bit j for this thread's column vc[j], from its own rows.
@@ -370,12 +426,11 @@ __device__ __forceinline__ void drop_unused(uint32_t (&x)[4][W], unsigned used) 
 }
 
 // Entry range of row r of the tile in the item (every lane r < 16 its own row).
-__device__ __forceinline__ void row_range(const AttnArgs &a, const TileWork &w, int lane, int &t0, int &t1) {
+__device__ __forceinline__ void row_range(const TileWork &w, int lane, int &t0, int &t1) {
     t0 = t1 = 0;
-    if (lane < kTileRows) {
-        t0 = __ldg(a.row_start + w.it * kTileRows + lane);
-        t1 = t0;
-        for (int ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(a.bits + (int64_t)ch * 16 + lane));
+    if (lane < kTileRows && w.ch0 < w.ch1) {
+        t0 = t1 = __ldg(w.ch0->start + lane);
+        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(ch->bits + lane));
     }
 }
 
@@ -406,7 +461,7 @@ template <typename T>
 __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(a, w, lane, s0, s1);
+    row_range(w, lane, s0, s1);
     const T *qb = static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2];
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
@@ -453,13 +508,15 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid_constant__ AttnArgs a) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    const float scale = (float)a.scale, none = neg_inf<float>();
-    for (int64_t y = blockIdx.y; y < (int64_t)a.batch * a.kv_heads; y += gridDim.y) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const unsigned share = (unsigned)(a.heads / a.kv_heads), n_y = (unsigned)a.batch * a.kv_heads;
+    const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
+    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * (int64_t)kTileWarps + (threadIdx.x >> 5), y, share)) return;
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, share)) return;
         Own<D> q;
         q.load(static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
         const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2] + c * (D / 4);
@@ -467,47 +524,50 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
         Sums<T, D> acc;
         acc.zero();
         float m[2] = {none, none}, l[2] = {0.0f, 0.0f};
-        int at[2] = {0, 0};                             // next entry of rows g and g + 8
-        if (a.vals)
-            for (int i = 0; i < 2; ++i) at[i] = __ldg(a.row_start + w.it * kTileRows + g + 8 * i);
-        Chunk next;
-        if (w.ch0 < w.ch1) next.load(a, w.ch0, g, c, a.n_cols);
-        for (int ch = w.ch0; ch < w.ch1; ++ch) {
-            const Chunk cur = next;
+        Chunk<VALS> next;
+        if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_cols);
+        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
+            const Chunk<VALS> cur = next;
             uint32_t k[2][D / 8], v[4][D / 16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) load_words<D / 8>(k[i], kb + cur.kc[i] * a.ks[1]);
+            for (int i = 0; i < 2; ++i) load_words<D / 8>(k[i], row_at(kb, cur.kc[i], kst));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) load_words<D / 16>(v[i], vb + cur.vc[i] * a.vs[1]);
-            if (ch + 1 < w.ch1) next.load(a, ch + 1, g, c, a.n_cols);
+            for (int i = 0; i < 4; ++i) load_words<D / 16>(v[i], row_at(vb, cur.vc[i], vst));
+            if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_cols);
             float s[2][4];
             score_products<T, D>(s, q, k);
             float top[2] = {m[0], m[1]};
             unsigned used = 0;
+            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {           // row g + 8 (e / 2), column 8 blk + 2c + e % 2
-                    const int i = e >> 1, pos = 8 * blk + 2 * c + (e & 1);
-                    const bool on = cur.bits[i] >> pos & 1;
-                    float x = 0.0f;
-                    if (a.vals && on)
-                        x = load_value<float>(a.vals, a.vals_f64,
-                                              w.b * a.nnz + at[i] + __popc(cur.bits[i] & ((1u << pos) - 1u)));
-                    used |= (unsigned)(on && x != none) << (2 * blk + (e & 1));
-                    s[blk][e] = on && x != none ? fmaf(s[blk][e], scale, x) : none;
+                    const int i = e >> 1;
+                    bool on = mine[i] & (1u << (8 * blk + (e & 1)));
+                    if constexpr (VALS) {
+                        float x = 0.0f;
+                        if (on)
+                            x = load_value<float>(a.vals, a.vals_f64,
+                                                  w.b * a.nnz + cur.entry(i, 8 * blk + 2 * c + (e & 1)));
+                        on = on && x != none;
+                        used |= (unsigned)on << (2 * blk + (e & 1));
+                        s[blk][e] = fmaf(s[blk][e], scale, value_log2(x));
+                    } else {
+                        s[blk][e] *= scale;
+                    }
+                    s[blk][e] = on ? s[blk][e] : none;
                     top[i] = fmaxf(top[i], s[blk][e]);
                 }
-            if (a.vals) drop_unused(v, used);
+            if constexpr (VALS) drop_unused(v, used);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                at[i] += __popc(cur.bits[i]);
                 top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
                 top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
             }
             const float ref[2] = {top[0] == none ? 0.0f : top[0], top[1] == none ? 0.0f : top[1]};
             if (__any_sync(kAll, top[0] != m[0] || top[1] != m[1])) {
-                const float f0 = exp_of(m[0] - ref[0]), f1 = exp_of(m[1] - ref[1]);
+                const float f0 = exp2_of(m[0] - ref[0]), f1 = exp2_of(m[1] - ref[1]);
                 acc.scale(f0, f1);
                 l[0] *= f0;
                 l[1] *= f1;
@@ -518,7 +578,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
             for (int blk = 0; blk < 2; ++blk) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[blk][e] = exp_of(s[blk][e] - ref[e >> 1]);
+                    s[blk][e] = exp2_of(s[blk][e] - ref[e >> 1]);
                     l[e >> 1] += s[blk][e];
                 }
                 acc.add(s[blk], v[2 * blk], v[2 * blk + 1]);
@@ -532,6 +592,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
         for (int i = 0; i < 2; ++i) {
             l[i] += __shfl_xor_sync(kAll, l[i], 1);
             l[i] += __shfl_xor_sync(kAll, l[i], 2);
+            m[i] *= kLn2;
         }
         if (w.slot < 0) acc.scale(l[0] > 0.0f ? 1.0f / l[0] : 0.0f, l[1] > 0.0f ? 1.0f / l[1] : 0.0f);
 #pragma unroll
@@ -566,7 +627,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(a, w, lane, s0, s1);
+    row_range(w, lane, s0, s1);
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
     const float scale = (float)a.scale, none = neg_inf<float>();
@@ -603,13 +664,15 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
 }
 
 // By A's rows: (lse, D) of every row, dq, and ds of every entry if asked for.
-template <typename T, int D>
+template <typename T, int D, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    const float scale = (float)a.scale, none = neg_inf<float>();
-    for (int64_t y = blockIdx.y; y < (int64_t)a.batch * a.kv_heads; y += gridDim.y) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const unsigned share = (unsigned)(a.heads / a.kv_heads), n_y = (unsigned)a.batch * a.kv_heads;
+    const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
+    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * (int64_t)kTileWarps + (threadIdx.x >> 5), y, share)) return;
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, share)) return;
         Own<D> q, go;
         q.load(static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
         go.load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + w.h * a.ds[2], a.ds[1], w.row0, a.n_rows, g, c);
@@ -635,60 +698,67 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
             delta[i] += __shfl_xor_sync(kAll, delta[i], 1);
             delta[i] += __shfl_xor_sync(kAll, delta[i], 2);
             if (row < a.n_rows && c == 0)
-                a.stat[((int64_t)w.b * a.heads + w.h) * a.n_rows + row] = make_float2(lse[i], delta[i]);
+                a.stat[((int64_t)w.b * a.heads + w.h) * a.n_rows + row] = make_float2(lse[i] * kLog2e, delta[i]);
         }
-        const T *ks = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
-        const T *vs = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2] + c * (D / 4);
+        const bool dead[2] = {lse[0] == none, lse[1] == none};
+        lse[0] *= kLog2e;
+        lse[1] *= kLog2e;
+        const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
+        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2] + c * (D / 4);
+        float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
         Sums<T, D> acc;
         acc.zero();
-        int at[2];
-        for (int i = 0; i < 2; ++i) at[i] = __ldg(a.row_start + w.it * kTileRows + g + 8 * i);
-        Chunk next;
-        if (w.ch0 < w.ch1) next.load(a, w.ch0, g, c, a.n_cols);
-        for (int ch = w.ch0; ch < w.ch1; ++ch) {
-            const Chunk cur = next;
+        Chunk<VALS> next;
+        if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_cols);
+        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
+            const Chunk<VALS> cur = next;
             float s[2][4], dp[2][4];
             uint32_t x[4][D / 16];
             {
                 uint32_t k[2][D / 8], v[2][D / 8];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    load_words<D / 8>(k[i], ks + c * (D / 4) + cur.kc[i] * a.ks[1]);
-                    load_words<D / 8>(v[i], vs + cur.kc[i] * a.vs[1]);
+                    load_words<D / 8>(k[i], row_at(kb + c * (D / 4), cur.kc[i], kst));
+                    load_words<D / 8>(v[i], row_at(vb, cur.kc[i], vst));
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) load_words<D / 16>(x[i], ks + g * (D / 8) + cur.vc[i] * a.ks[1]);
-                if (ch + 1 < w.ch1) next.load(a, ch + 1, g, c, a.n_cols);
+                for (int i = 0; i < 4; ++i) load_words<D / 16>(x[i], row_at(kb + g * (D / 8), cur.vc[i], kst));
+                if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_cols);
                 score_products<T, D>(s, q, k);
                 score_products<T, D>(dp, go, v);
             }
             unsigned used = 0;
+            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
+            for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = e >> 1, pos = 8 * blk + 2 * c + (e & 1);
-                    const bool there = cur.bits[i] >> pos & 1;
-                    const int64_t t = at[i] + __popc(cur.bits[i] & ((1u << pos) - 1u));
-                    const float val = a.vals && there ? load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + t) : 0.0f;
-                    const bool on = there && val != none && lse[i] != none;
-                    used |= (unsigned)on << (2 * blk + (e & 1));
-                    s[blk][e] = on ? exp_of(fmaf(s[blk][e], scale, val) - lse[i]) * (dp[blk][e] - delta[i]) : 0.0f;
-                    if (a.ds_out && there) a.ds_out[((int64_t)w.b * a.heads + w.h) * a.nnz + t] = s[blk][e];
+                    const int i = e >> 1;
+                    const bool there = mine[i] & (1u << (8 * blk + (e & 1)));
+                    bool on = there && !dead[i];
+                    if constexpr (VALS) {
+                        float val = 0.0f;
+                        const int t = cur.entry(i, 8 * blk + 2 * c + (e & 1));
+                        if (there) val = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + t);
+                        on = on && val != none;
+                        used |= (unsigned)on << (2 * blk + (e & 1));
+                        s[blk][e] = fmaf(s[blk][e], scale, value_log2(val)) - lse[i];
+                        s[blk][e] = on ? exp2_of(s[blk][e]) * (dp[blk][e] - delta[i]) : 0.0f;
+                        if (ds_out && there) ds_out[t] = s[blk][e];
+                    } else {
+                        s[blk][e] = on ? exp2_of(fmaf(s[blk][e], scale, -lse[i])) * (dp[blk][e] - delta[i]) : 0.0f;
+                    }
                 }
-            }
-            if (a.vals) drop_unused(x, used);
+            if constexpr (VALS) drop_unused(x, used);
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) acc.add(s[blk], x[2 * blk], x[2 * blk + 1]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) at[i] += __popc(cur.bits[i]);
         }
         if (!a.dq) continue;
         if (acc.bad()) {
             slow_bwd_rows<T>(a, w);
             continue;
         }
-        acc.scale(scale, scale);
+        acc.scale((float)a.scale, (float)a.scale);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = g + 8 * i;
@@ -707,7 +777,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w, bool want_dk, bool want_dv) {
     const int lane = threadIdx.x & 31, share = a.heads / a.kv_heads;
     int s0, s1;
-    row_range(a, w, lane, s0, s1);
+    row_range(w, lane, s0, s1);
     const float scale = (float)a.scale, none = neg_inf<float>();
     for (int r = 0; r < kTileRows && w.row0 + r < a.n_cols; ++r) {
         const int t0 = __shfl_sync(kAll, s0, r), t1 = __shfl_sync(kAll, s1, r);
@@ -725,7 +795,7 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
                 float q[kSlowVec], go[kSlowVec];
                 slow_load(q, static_cast<const T *>(a.q) + w.b * a.qs[0] + i * a.qs[1] + h * a.qs[2], a.dim, lane);
                 slow_load(go, static_cast<const T *>(a.dout) + w.b * a.ds[0] + i * a.ds[1] + h * a.ds[2], a.dim, lane);
-                const float p = exp_of(fmaf(slow_dot(q, k), scale, x) - st.x);
+                const float p = exp2f(fmaf(fmaf(slow_dot(q, k), scale, x), kLog2e, -st.x));
                 const float ds = p * (slow_dot(go, v) - st.y);
 #pragma unroll
                 for (int j = 0; j < kSlowVec; ++j) {
@@ -754,13 +824,15 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 // By A^T's rows: dk (DK) and dv (DV) of 16 columns of A, the shared heads one
 // after the other.  Wide heads take two launches: both sums and both own
 // operands would not fit the registers.
-template <typename T, int D, bool DK, bool DV>
+template <typename T, int D, bool DK, bool DV, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    const float scale = (float)a.scale, none = neg_inf<float>();
-    for (int64_t y = blockIdx.y; y < (int64_t)a.batch * a.kv_heads; y += gridDim.y) {
+    const unsigned n_y = (unsigned)a.batch * a.kv_heads;
+    const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
+    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * (int64_t)kTileWarps + (threadIdx.x >> 5), y, 1)) return;
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, 1)) return;
         Own<D> k, v;
         k.load(static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2], a.ks[1], w.row0, a.n_cols, g, c);
         if constexpr (DK)
@@ -772,63 +844,61 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
             const T *qb = static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2];
             const T *gb = static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2];
             const float2 *stat = a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows;
-            int at[2];
-            for (int i = 0; i < 2; ++i) at[i] = __ldg(a.row_start + w.it * kTileRows + g + 8 * i);
-            Chunk next;
-            if (w.ch0 < w.ch1) next.load(a, w.ch0, g, c, a.n_rows);
-            for (int ch = w.ch0; ch < w.ch1; ++ch) {
-                const Chunk cur = next;
+            Chunk<VALS> next;
+            if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_rows);
+            for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
+                const Chunk<VALS> cur = next;
                 float s[2][4], dp[2][4];
                 float2 st[4];
                 {
                     uint32_t x[2][D / 8], z[2][D / 8];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        load_words<D / 8>(x[i], qb + c * (D / 4) + cur.kc[i] * a.qs[1]);
-                        if constexpr (DK) load_words<D / 8>(z[i], gb + c * (D / 4) + cur.kc[i] * a.ds[1]);
+                        load_words<D / 8>(x[i], row_at(qb + c * (D / 4), cur.kc[i], qst));
+                        if constexpr (DK) load_words<D / 8>(z[i], row_at(gb + c * (D / 4), cur.kc[i], dst));
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) st[i] = stat[cur.vc[i]];
-                    if (ch + 1 < w.ch1) next.load(a, ch + 1, g, c, a.n_rows);
+                    if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_rows);
                     score_products<T, D>(s, k, x);
                     if constexpr (DK) score_products<T, D>(dp, v, z);
                 }
                 unsigned used = 0;
+                const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
+                for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = e >> 1, j = 2 * blk + (e & 1), pos = 8 * blk + 2 * c + (e & 1);
-                        const bool there = cur.bits[i] >> pos & 1;
+                        const int i = e >> 1, j = 2 * blk + (e & 1);
+                        bool on = mine[i] & (1u << (8 * blk + (e & 1)));
                         float val = 0.0f;
-                        if (a.vals && there) {
-                            const int t = at[i] + __popc(cur.bits[i] & ((1u << pos) - 1u));
-                            val = load_value<float>(a.vals, a.vals_f64,
-                                                    w.b * a.nnz + SLA_IDX((int64_t)__ldg(a.perm + t), a.nnz, kBndEntry));
+                        if constexpr (VALS) {
+                            if (on) {
+                                const int64_t at = SLA_IDX((int64_t)__ldg(a.perm + cur.entry(i, 8 * blk + 2 * c + (e & 1))),
+                                                           a.nnz, kBndEntry);
+                                val = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + at);
+                            }
                         }
-                        const bool on = there && val != none && st[j].x != none;
-                        used |= (unsigned)on << j;
-                        s[blk][e] = on ? exp_of(fmaf(s[blk][e], scale, val) - st[j].x) : 0.0f;
+                        on = on && val != none && st[j].x != none;
+                        if constexpr (VALS) used |= (unsigned)on << j;
+                        s[blk][e] = on ? exp2_of(fmaf(s[blk][e], scale, value_log2(val)) - st[j].x) : 0.0f;
                         if constexpr (DK) dp[blk][e] = on ? s[blk][e] * (dp[blk][e] - st[j].y) : 0.0f;
                     }
-                }
                 uint32_t x[4][D / 16];
                 if constexpr (DV) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], gb + g * (D / 8) + cur.vc[j] * a.ds[1]);
-                    if (a.vals) drop_unused(x, used);
+                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], row_at(gb + g * (D / 8), cur.vc[j], dst));
+                    if constexpr (VALS) drop_unused(x, used);
                     dv.add(s[0], x[0], x[1]);
                     dv.add(s[1], x[2], x[3]);
                 }
                 if constexpr (DK) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], qb + g * (D / 8) + cur.vc[j] * a.qs[1]);
-                    if (a.vals) drop_unused(x, used);
+                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], row_at(qb + g * (D / 8), cur.vc[j], qst));
+                    if constexpr (VALS) drop_unused(x, used);
                     dk.add(dp[0], x[0], x[1]);
                     dk.add(dp[1], x[2], x[3]);
                 }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) at[i] += __popc(cur.bits[i]);
             }
         }
         bool bad = false;
@@ -838,7 +908,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
             slow_bwd_cols<T>(a, w, DK, DV);
             continue;
         }
-        if constexpr (DK) dk.scale(scale, scale);
+        if constexpr (DK) dk.scale((float)a.scale, (float)a.scale);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int r = g + 8 * i;
@@ -862,25 +932,30 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
 // -------------------------------------------------------------- launches ----
 enum { kTileFwd, kTileBwdRows, kTileBwdCols };
 
-template <typename T, int D>
+template <typename T, int D, bool VALS>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
     const int64_t warps = (int64_t)a.n_items * (what == kTileBwdCols ? 1 : a.heads / a.kv_heads);
     const int64_t x = (warps + kTileWarps - 1) / kTileWarps, y = (int64_t)a.batch * a.kv_heads;
-    SLA_REQUIRE(x < INT_MAX, "sla_attention: too many rows and heads");
+    SLA_REQUIRE(x < INT_MAX / kTileWarps && y < INT_MAX, "sla_attention: too many rows, systems and heads");
     if (x == 0) return SLA_OK;
     const dim3 grid((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
     if (what == kTileFwd) {
-        tile_forward_kernel<T, D><<<grid, kTileThreads, 0, s>>>(a);
+        tile_forward_kernel<T, D, VALS><<<grid, kTileThreads, 0, s>>>(a);
     } else if (what == kTileBwdRows) {
-        tile_bwd_rows_kernel<T, D><<<grid, kTileThreads, 0, s>>>(a);
+        tile_bwd_rows_kernel<T, D, VALS><<<grid, kTileThreads, 0, s>>>(a);
     } else if constexpr (D <= 64) {
-        tile_bwd_cols_kernel<T, D, true, true><<<grid, kTileThreads, 0, s>>>(a);
+        tile_bwd_cols_kernel<T, D, true, true, VALS><<<grid, kTileThreads, 0, s>>>(a);
     } else {
-        if (a.dv) tile_bwd_cols_kernel<T, D, false, true><<<grid, kTileThreads, 0, s>>>(a);
-        if (a.dk) tile_bwd_cols_kernel<T, D, true, false><<<grid, kTileThreads, 0, s>>>(a);
+        if (a.dv) tile_bwd_cols_kernel<T, D, false, true, VALS><<<grid, kTileThreads, 0, s>>>(a);
+        if (a.dk) tile_bwd_cols_kernel<T, D, true, false, VALS><<<grid, kTileThreads, 0, s>>>(a);
     }
     SLA_CHECK_LAUNCH();
     return SLA_OK;
+}
+
+template <typename T, int D>
+sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
+    return a.vals ? launch_tile<T, D, true>(what, a, s) : launch_tile<T, D, false>(what, a, s);
 }
 
 template <typename T>
@@ -899,33 +974,39 @@ sla_status launch_tile_of(int what, const AttnArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-sla_status build_tiles(AttnPlan *p, int n_rows, const int32_t *rowptr, const int32_t *colind, cudaStream_t s) {
-    const int n = p->n_items;
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
+                       cudaStream_t s) {
+    const int n = parts.n_items, U = parts.n_units;
     DeviceScratch tmp;
-    unsigned *chunks = tmp.get<unsigned>((size_t)n + 1);
+    unsigned *count = tmp.get<unsigned>((size_t)n + 1), *chunks = tmp.get<unsigned>((size_t)U + 1);
     void *ws = tmp.get<char>(scan_ws_bytes((int64_t)n + 1));
-    if (!chunks || !ws || !alloc_array(&p->chunk_ptr, (size_t)n + 1) ||
-        !alloc_array(&p->row_start, (size_t)n * kTileRows)) {
+    if (!count || !chunks || !ws || !alloc_array(&t->chunk0, (size_t)U + 1)) {
         set_error("attention plan: out of device memory");
         return SLA_ERR_OOM;
     }
     const unsigned grid = blocks_of(((int64_t)n + 1) * 32, 128);
-    tile_columns_kernel<false><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, p->seg_len, p->item_unit, p->item_seg,
-                                                    chunks, nullptr, nullptr, nullptr, nullptr);
+    tile_columns_kernel<false><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+                                                    parts.item_seg, count, nullptr, nullptr, nullptr);
     SLA_CHECK_LAUNCH();
-    sla_status st = exclusive_scan(chunks, reinterpret_cast<unsigned *>(p->chunk_ptr), (int64_t)n + 1, ws, s);
+    sla_status st = exclusive_scan(count, count, (int64_t)n + 1, ws, s);
+    if (st != SLA_OK) return st;
+    tile_chunks_kernel<<<blocks_of(n), 256, 0, s>>>(U, n, count, parts.item_unit, parts.item_seg, chunks);
+    SLA_CHECK_LAUNCH();
+    st = exclusive_scan(chunks, reinterpret_cast<unsigned *>(t->chunk0), (int64_t)U + 1, ws, s);
     if (st != SLA_OK) return st;
     int32_t total = 0;
-    SLA_CHECK_CUDA(cudaMemcpyAsync(&total, p->chunk_ptr + n, sizeof total, cudaMemcpyDeviceToHost, s));
+    SLA_CHECK_CUDA(cudaMemcpyAsync(&total, t->chunk0 + U, sizeof total, cudaMemcpyDeviceToHost, s));
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
-    if (!alloc_array(&p->cols, (size_t)total * 16) || !alloc_array(&p->bits, (size_t)total * 16)) {
+    if (!alloc_array(&t->chunks, (size_t)total)) {
         set_error("attention plan: out of device memory");
         return SLA_ERR_OOM;
     }
-    tile_columns_kernel<true><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, p->seg_len, p->item_unit, p->item_seg,
-                                                   nullptr, p->chunk_ptr, p->cols, p->bits, p->row_start);
+    SLA_CHECK_CUDA(cudaMemsetAsync(t->chunks, 0, (size_t)total * sizeof(TileChunk), s));
+    tile_columns_kernel<true><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+                                                   parts.item_seg, nullptr, count, t->chunk0, t->chunks);
     SLA_CHECK_LAUNCH();
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+    t->built = true;
     return SLA_OK;
 }
 
