@@ -132,11 +132,11 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
     return SLA_OK;
 }
 
-// Enough items to fill the GPU when there are few units (16 an SM), but none
+// Enough items to fill the GPU when there are few units (8 an SM), but none
 // shorter than 64 entries or columns: a shorter one spends more on its partial
 // result than on its entries.  A level counts on 8 times as many systems and
 // heads as the one before, so it splits 8 times less.
-int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 16 >> (3 * level)); }
+int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 8 >> (3 * level)); }
 
 // All levels of one direction's row plans (tiled == false) or its tiles and
 // their plans.  The lengths are the same for every level.
@@ -711,7 +711,7 @@ attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__rest
 }  // namespace
 
 // One warp a joined row while segments are few (one batch of loads each), else 8.
-constexpr int kJoinFew = 8;
+constexpr int kJoinFew = 16;
 
 template <typename T>
 sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s) {
@@ -858,8 +858,8 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
 // Workspace pieces: what the backward keeps for every entry (row kernels) or
 // row (tile kernels), then the partial sums of split rows.
 struct AttnWs {
-    size_t pds = 0, stat = 0, ds = 0, part = 0;
-    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(part); }
+    size_t pds = 0, stat = 0, ds = 0, vals_t = 0, part = 0;
+    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(vals_t) + align_up(part); }
 };
 
 const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
@@ -877,6 +877,7 @@ AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
     if (attn_tiled(o)) {
         w.stat = B * H * (size_t)h->n_rows * sizeof(float2);
         w.ds = B * H * (size_t)h->nnz * sizeof(float);
+        w.vals_t = B * (size_t)h->nnz * sizeof(float);
     } else {
         w.pds = B * (size_t)h->nnz * H * 2 * acc;
     }
@@ -1075,6 +1076,7 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     a.pds = c.take<char>(w.pds);
     a.stat = reinterpret_cast<float2 *>(c.take<char>(w.stat));
     a.ds_out = dvals ? reinterpret_cast<float *>(c.take<char>(w.ds)) : (c.take<char>(w.ds), nullptr);
+    a.vals_t = reinterpret_cast<float *>(c.take<char>(w.vals_t));
     a.part = c.take<char>(w.part);
     if (!dk && !dv && !dvals) a.pds = nullptr;
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);

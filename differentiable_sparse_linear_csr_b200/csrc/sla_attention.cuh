@@ -84,6 +84,7 @@ struct AttnArgs {
     void *pds;                             // row kernels: [B][nnz][heads] pairs (p, ds)
     float2 *stat;                          // tile kernels: [B][heads][n_rows] pairs (lse, D)
     float *ds_out;                         // tile kernels: [B][heads][nnz] ds, or null
+    float *vals_t;                         // tile kernels: [B][nnz] values in A^T's order
     void *part;                            // partial sums of split rows
 };
 

@@ -8,14 +8,17 @@
 // Most of that product is thrown away (a 5-point grid uses 5 of 34 columns a
 // row), which costs nothing: the gathers bound the kernel.
 //
-// No shared memory: operands go from global memory to the registers the matrix
-// instructions take.  A dot product does not depend on the order of its terms,
-// so thread (g, c) of a quad layout (g = lane / 4, c = lane % 4) reads dim / 4
-// consecutive elements of column g (16-byte loads) and feeds them as its four
-// places of every k step, the tile's own rows in the same order.  For the
-// products that sum over columns, thread (g, c) reads dim / 8 consecutive
-// elements of the columns 2c and 2c + 1 and takes element nb of them as output
-// block nb, so its outputs are consecutive too.
+// Each warp copies the chunk's rows into its own ring of shared-memory stages
+// (cp.async, a few chunks ahead: the loads' latency is what the kernels wait for)
+// and reads them from there twice, as columns of the scores and as rows of the
+// sums.  The 16-byte pieces of a row are permuted by its number so that both
+// reads are free of bank conflicts.  A dot product does not depend on the order of
+// its terms, so thread (g, c) of a quad layout (g = lane / 4, c = lane % 4) takes
+// piece 4 i + c of a column as its places of the k steps 2 i and 2 i + 1, and in
+// the sums piece 8 i + g, element e, as output block 8 i + e: whole 16-byte reads.
+// Narrow heads go several to a warp, so that a gathered row is at least 128
+// consecutive bytes and the chunk's bookkeeping is shared; so do heads that
+// share their key head, which is then fetched once.
 //
 // Scores: 16-bit products, exact, summed in 32 bits.  Weights are not rounded to
 // 16 bits: they multiply as tf32 (the 16-bit operand is exact in it), rounded to
@@ -129,44 +132,52 @@ __global__ void tile_chunks_kernel(int n_units, int n_parts, const unsigned *__r
 }
 
 // ------------------------------------------------------------ operands ----
-// W consecutive 32-bit words (W * 4 bytes apart for neighbouring threads).
-template <int W>
-__device__ __forceinline__ void load_words(uint32_t (&r)[W], const void *p) {
-    if constexpr (W % 4 == 0) {
+__device__ __forceinline__ uint4 lds16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
+__device__ __forceinline__ uint2 lds8(const char *p) { return *reinterpret_cast<const uint2 *>(p); }
+
+// One head's row: D elements in pieces of 8 (16 bytes).  What a thread takes of it:
+//   scores: pieces 4 i + c (i < D / 32), then 8 bytes of the last two pieces if
+//           D is not a multiple of 32;  word 2 s, 2 s + 1 belong to k step s;
+//   sums:   pieces 8 i + g (i < D / 64), then 8 bytes of the next four pieces,
+//           then 4 bytes of the next two; word w holds output blocks 2 w, 2 w + 1.
+// A staged row r starts at r * pitch; its piece p is found at p ^ swizzle(r).
+__device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 2)) & 1) << 2 | (r & 2); }
+__device__ __forceinline__ int piece_at(int p, int r) { return (p ^ swizzle(r)) * 16; }
+
+template <int D>
+__device__ __forceinline__ void read_score(uint32_t (&w)[D / 8], const char *row, int r, int p0, int c) {
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i) {
-            const uint4 x = __ldg(static_cast<const uint4 *>(p) + i);
-            r[4 * i] = x.x;
-            r[4 * i + 1] = x.y;
-            r[4 * i + 2] = x.z;
-            r[4 * i + 3] = x.w;
-        }
-    } else if constexpr (W % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) {
-            const uint2 x = __ldg(static_cast<const uint2 *>(p) + i);
-            r[2 * i] = x.x;
-            r[2 * i + 1] = x.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) r[i] = __ldg(static_cast<const uint32_t *>(p) + i);
+    for (int i = 0; i < D / 32; ++i) {
+        const uint4 x = lds16(row + piece_at(p0 + 4 * i + c, r));
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
+    }
+    if constexpr (D % 32 != 0) {
+        const uint2 x = lds8(row + piece_at(p0 + D / 8 - 2 + (c >> 1), r) + (c & 1) * 8);
+        w[D / 8 - 2] = x.x;
+        w[D / 8 - 1] = x.y;
     }
 }
 
-template <int W>
-__device__ __forceinline__ void store_words(void *p, const uint32_t (&r)[W]) {
-    if constexpr (W % 4 == 0) {
+template <int D>
+__device__ __forceinline__ void read_sum(uint32_t (&w)[D / 16], const char *row, int r, int p0, int g) {
 #pragma unroll
-        for (int i = 0; i < W / 4; ++i)
-            static_cast<uint4 *>(p)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-    } else if constexpr (W % 2 == 0) {
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i) static_cast<uint2 *>(p)[i] = make_uint2(r[2 * i], r[2 * i + 1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < W; ++i) static_cast<uint32_t *>(p)[i] = r[i];
+    for (int i = 0; i < D / 64; ++i) {
+        const uint4 x = lds16(row + piece_at(p0 + 8 * i + g, r));
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
     }
+    if constexpr (D % 64 >= 32) {
+        const uint2 x = lds8(row + piece_at(p0 + D / 64 * 8 + (g >> 1), r) + (g & 1) * 8);
+        w[D / 64 * 4] = x.x;
+        w[D / 64 * 4 + 1] = x.y;
+    }
+    if constexpr (D % 32 != 0)
+        w[D / 16 - 1] = *reinterpret_cast<const uint32_t *>(row + piece_at(p0 + D / 8 - 2 + (g >> 2), r) + (g & 3) * 4);
 }
 
 template <typename T>
@@ -239,39 +250,78 @@ struct Own {
     uint32_t a[D / 16][4];
     template <typename T>
     __device__ __forceinline__ void load(const T *base, int64_t stride, int64_t row0, int n_rows, int g, int c) {
-        uint32_t r[2][D / 8];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (row0 + g + 8 * i < n_rows) load_words<D / 8>(r[i], base + (row0 + g + 8 * i) * stride + c * (D / 4));
-            else {
+            const bool on = row0 + g + 8 * i < n_rows;
+            const char *p = reinterpret_cast<const char *>(base + (row0 + g + 8 * i) * stride);
 #pragma unroll
-                for (int w = 0; w < D / 8; ++w) r[i][w] = 0;
+            for (int j = 0; j < D / 32; ++j) {
+                const uint4 x = on ? __ldg(reinterpret_cast<const uint4 *>(p) + 4 * j + c) : make_uint4(0, 0, 0, 0);
+                a[2 * j][i] = x.x;
+                a[2 * j][2 + i] = x.y;
+                a[2 * j + 1][i] = x.z;
+                a[2 * j + 1][2 + i] = x.w;
+            }
+            if constexpr (D % 32 != 0) {
+                const uint2 x = on ? __ldg(reinterpret_cast<const uint2 *>(p + D / 32 * 64) + c) : make_uint2(0, 0);
+                a[D / 16 - 1][i] = x.x;
+                a[D / 16 - 1][2 + i] = x.y;
             }
         }
+    }
+    // Row g + 8 i's dot product with the same elements of 32-bit rows, this
+    // thread's share.
+    template <typename T>
+    __device__ __forceinline__ float dot(const float *p, int i, int c) const {
+        float s = 0.0f;
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-            a[s][0] = r[0][2 * s];
-            a[s][1] = r[1][2 * s];
-            a[s][2] = r[0][2 * s + 1];
-            a[s][3] = r[1][2 * s + 1];
+        for (int j = 0; j < D / 16; ++j) {
+            // k step j: elements 32 (j / 2) + 8 c + 4 (j % 2) + 0..3, or 4 c + 0..3 of the last 16
+            const int d = j / 2 < D / 32 ? 32 * (j / 2) + 8 * c + 4 * (j % 2) : D / 32 * 32 + 4 * c;
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(p + d));
+            uint32_t e0, e1, e2, e3;
+            widen<T>(a[j][i], e0, e1);
+            widen<T>(a[j][2 + i], e2, e3);
+            s = fmaf(__uint_as_float(e0), x.x, s);
+            s = fmaf(__uint_as_float(e1), x.y, s);
+            s = fmaf(__uint_as_float(e2), x.z, s);
+            s = fmaf(__uint_as_float(e3), x.w, s);
         }
+        return s;
     }
 };
 
-// s[2][4]: the products of the 16 own rows with the 16 columns of a chunk, the
-// columns 8 blk + (2c, 2c + 1) of rows g and g + 8 in this thread.
-template <typename T, int D>
-__device__ __forceinline__ void score_products(float (&s)[2][4], const Own<D> &own, const uint32_t (&k)[2][D / 8]) {
+// s[2][4]: the products of the 16 own rows with the 16 staged columns of a chunk,
+// the columns 8 blk + (2c, 2c + 1) of rows g and g + 8 in this thread.
+template <typename T, int D, int PITCH>
+__device__ __forceinline__ void score_products(float (&s)[2][4], const Own<D> &own, const char *stage, int p0, int g,
+                                               int c) {
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
+        uint32_t k[D / 8];
+        read_score<D>(k, stage + (8 * blk + g) * PITCH, 8 * blk + g, p0, c);
         s[blk][0] = s[blk][1] = s[blk][2] = s[blk][3] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) mma16<T>(s[blk], own.a[i], k[blk][2 * i], k[blk][2 * i + 1]);
+        for (int i = 0; i < D / 16; ++i) mma16<T>(s[blk], own.a[i], k[2 * i], k[2 * i + 1]);
     }
 }
 
+// Zeros for the gathered rows of the columns that no row of the tile uses; used:
+// bit j for this thread's column vc[j], from its own rows.
+template <int W>
+__device__ __forceinline__ void drop_unused(uint32_t (&x)[4][W], unsigned used) {
+    used |= __shfl_xor_sync(kAll, used, 4);
+    used |= __shfl_xor_sync(kAll, used, 8);
+    used |= __shfl_xor_sync(kAll, used, 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (!(used >> j & 1))
+#pragma unroll
+            for (int i = 0; i < W; ++i) x[j][i] = 0;
+}
+
 // Sums over a chunk's columns: o[nb] += w . x, with x the rows of the columns
-// 8 blk + (2c, 2c + 1), elements g * (D / 8) + nb.
+// 8 blk + (2c, 2c + 1).
 template <typename T, int D>
 struct Sums {
     float o[D / 8][4];
@@ -321,40 +371,82 @@ struct Sums {
             for (int i = 0; i < 4; ++i) b = b || o[nb][i] != o[nb][i];
         return __any_sync(kAll, b);
     }
-    // Row g (i = 0) or g + 8 (i = 1): elements 2c (D / 8) and the next D / 4.
-    __device__ __forceinline__ void store(T *p, int i, int c) const {
-        uint32_t w[D / 8];
+    // All of a chunk: the weights w[2][4] with the staged rows.  used: see
+    // drop_unused.
+    template <int PITCH, bool DROP>
+    __device__ __forceinline__ void add_chunk(const float (&w)[2][4], const char *stage, int p0, int g, int c,
+                                              unsigned used) {
+        uint32_t x[4][D / 16];
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            w[j] = narrow2<T>(o[2 * j][2 * i], o[2 * j + 1][2 * i]);
-            w[D / 16 + j] = narrow2<T>(o[2 * j][2 * i + 1], o[2 * j + 1][2 * i + 1]);
+        for (int j = 0; j < 4; ++j) {
+            const int r = 8 * (j >> 1) + 2 * c + (j & 1);
+            read_sum<D>(x[j], stage + r * PITCH, r, p0, g);
         }
-        store_words<D / 8>(p + c * (D / 4), w);
+        if constexpr (DROP) drop_unused(x, used);
+        add(w[0], x[0], x[1]);
+        add(w[1], x[2], x[3]);
     }
-    __device__ __forceinline__ void store(float *p, int i, int c) const {
-        uint32_t w[D / 4];
+    // Row g (i = 0) or g + 8 (i = 1) to its D elements at p.  Of every group of
+    // blocks this thread holds consecutive elements, first those of column 2c.
+    template <typename O>
+    __device__ __forceinline__ void store(O *p, int i, int c) const {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) put<O, 8>(p + 64 * j + 16 * c, 8 * j, i);
+        if constexpr (D % 64 >= 32) put<O, 4>(p + D / 64 * 64 + 8 * c, D / 64 * 8, i);
+        if constexpr (D % 32 != 0) put<O, 2>(p + D / 32 * 32 + 4 * c, D / 8 - 2, i);
+    }
+    template <typename O, int N>
+    __device__ __forceinline__ void put(O *p, int nb, int i) const {
+        float x[2 * N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            x[e] = o[nb + e][2 * i];
+            x[N + e] = o[nb + e][2 * i + 1];
+        }
+        if constexpr (sizeof(O) == 4) {
+#pragma unroll
+            for (int e = 0; e < N / 2; ++e)
+                reinterpret_cast<float4 *>(p)[e] = make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        } else if constexpr (N >= 4) {
+#pragma unroll
+            for (int e = 0; e < N / 4; ++e)
+                reinterpret_cast<uint4 *>(p)[e] =
+                    make_uint4(narrow2<T>(x[8 * e], x[8 * e + 1]), narrow2<T>(x[8 * e + 2], x[8 * e + 3]),
+                               narrow2<T>(x[8 * e + 4], x[8 * e + 5]), narrow2<T>(x[8 * e + 6], x[8 * e + 7]));
+        } else {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(narrow2<T>(x[0], x[1]), narrow2<T>(x[2], x[3]));
+        }
+    }
+    // The same for numbers that need not lie on 16 bytes.
+    __device__ __forceinline__ void store_odd(float *p, int i, int c) const {
 #pragma unroll
         for (int nb = 0; nb < D / 8; ++nb) {
-            w[nb] = __float_as_uint(o[nb][2 * i]);
-            w[D / 8 + nb] = __float_as_uint(o[nb][2 * i + 1]);
+            const int n = nb < D / 64 * 8 ? 8 : (nb < D / 32 * 4 ? 4 : 2);              // blocks of the group
+            const int d0 = nb < D / 64 * 8 ? nb / 8 * 64 : (nb < D / 32 * 4 ? D / 64 * 64 : D / 32 * 32);
+            const int d = d0 + 2 * n * c + (nb * 8 - d0) / 8;
+            p[d] = o[nb][2 * i];
+            p[d + n] = o[nb][2 * i + 1];
         }
-        store_words<D / 4>(p + c * (D / 4), w);
     }
 };
 
-// A warp's work: chunks [ch0, ch1) of a tile, one head of one system.
+// A warp's work: chunks [ch0, ch1) of a tile, heads h (and following) of one
+// system, whose key heads start at kh.
 struct TileWork {
     int64_t row0;
     int b, h, kh, slot;
     const TileChunk *ch0, *ch1;
 };
 
-__device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, unsigned x, unsigned y, unsigned share) {
-    const unsigned it = x / share;
+// Head groups of n_h heads; y counts systems and the groups of key heads (n_kh
+// of them each), x items and, within a key head, the groups of its query heads.
+__device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, unsigned x, unsigned y, unsigned n_h,
+                                          unsigned n_kh, unsigned groups) {
+    const unsigned it = x / groups, ky = (unsigned)a.kv_heads / n_kh;
     if (it >= (unsigned)a.n_items) return false;
-    w.b = (int)(y / (unsigned)a.kv_heads);
-    w.kh = (int)(y - (unsigned)w.b * a.kv_heads);
-    w.h = w.kh * (a.heads / a.kv_heads) + (int)(x - it * share);
+    w.b = (int)(y / ky);
+    w.kh = (int)((y - (unsigned)w.b * ky) * n_kh);
+    w.h = w.kh * (a.heads / a.kv_heads) + (int)((x - it * groups) * n_h);
     int unit = (int)it, seg = 0;
     w.slot = -1;
     if (a.item_unit) {
@@ -370,34 +462,19 @@ __device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, unsign
     return true;
 }
 
-// What a thread needs of a chunk: the columns it reads for the scores (g and
-// 8 + g) and for the sums (8 blk + 2c, + 1), rows g's and g + 8's bits, and
-// with ENTRIES the first entry of those rows.
+// What a thread keeps of a chunk: rows g's and g + 8's bits and, with ENTRIES,
+// their first entries.
 template <bool ENTRIES>
 struct Chunk {
-    unsigned kc[2], vc[4], bits[2];
+    unsigned bits[2];
     int at[2];
-    __device__ __forceinline__ void load(const TileChunk *p, int g, int c, int n_cols) {
-        kc[0] = (unsigned)__ldg(p->col + g);
-        kc[1] = (unsigned)__ldg(p->col + 8 + g);
-        const int2 x = __ldg(reinterpret_cast<const int2 *>(p->col) + c);
-        const int2 y = __ldg(reinterpret_cast<const int2 *>(p->col) + 4 + c);
-        vc[0] = (unsigned)x.x;
-        vc[1] = (unsigned)x.y;
-        vc[2] = (unsigned)y.x;
-        vc[3] = (unsigned)y.y;
+    __device__ __forceinline__ void load(const TileChunk *p, int g) {
         bits[0] = __ldg(p->bits + g);
         bits[1] = __ldg(p->bits + 8 + g);
         if constexpr (ENTRIES) {
             at[0] = __ldg(p->start + g);
             at[1] = __ldg(p->start + 8 + g);
         }
-#if SLA_DEBUG_BOUNDS
-        for (int i = 0; i < 2; ++i) kc[i] = (unsigned)SLA_IDX((int)kc[i], n_cols, kBndColumn);
-        for (int i = 0; i < 4; ++i) vc[i] = (unsigned)SLA_IDX((int)vc[i], n_cols, kBndColumn);
-#else
-        (void)n_cols;
-#endif
     }
     // Entry of row g + 8 i at position pos (if the row stores it).
     __device__ __forceinline__ int entry(int i, int pos) const {
@@ -405,24 +482,51 @@ struct Chunk {
     }
 };
 
-// Row `col` of a tensor with rows `bytes` apart (below 2^32: one multiply-add).
-template <typename T>
-__device__ __forceinline__ const void *row_at(const T *base, unsigned col, unsigned bytes) {
-    return reinterpret_cast<const char *>(base) + (uint64_t)col * bytes;
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
+                 :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                 :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
-// Zeros for the gathered rows of the columns that no row of the tile uses; used:
-// bit j for this thread's column vc[j], from its own rows.
-template <int W>
-__device__ __forceinline__ void drop_unused(uint32_t (&x)[4][W], unsigned used) {
-    used |= __shfl_xor_sync(kAll, used, 4);
-    used |= __shfl_xor_sync(kAll, used, 8);
-    used |= __shfl_xor_sync(kAll, used, 16);
+// A warp's ring of stages: two gathered tensors of HEADS heads, 16 rows each,
+// and with STAT a pair of numbers a column and head.
+template <int D, int HEADS, bool STAT>
+struct Ring {
+    static constexpr int kPieces = D / 8 * HEADS;                       // of a row
+    static constexpr int kPitch = (kPieces + 7) / 8 * 128;
+    static constexpr int kTensor = 16 * kPitch;
+    static constexpr int kStage = 2 * kTensor + (STAT ? 16 * 8 * HEADS : 0);
+    static constexpr int kStages = kStage <= 4608 ? 3 : 2;
+    static constexpr int kBytes = kStage * kStages;
+
+    // Copies of one tensor's rows of the columns in `col` (lane r: column r).
+    template <typename T>
+    static __device__ __forceinline__ void gather(char *stage, const T *base, unsigned stride, int64_t head_stride,
+                                                  unsigned col, int lane) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (!(used >> j & 1))
-#pragma unroll
-            for (int i = 0; i < W; ++i) x[j][i] = 0;
+        for (int i = 0; i < kPieces / 2; ++i) {
+            const int x = i * 32 + lane, r = x / kPieces, p = x - r * kPieces;
+            const unsigned cl = __shfl_sync(kAll, col, r);
+            const char *src = reinterpret_cast<const char *>(base) + (uint64_t)cl * stride;
+            if constexpr (HEADS == 1) src += p * 16;
+            else src += p / (D / 8) * head_stride * 2 + p % (D / 8) * 16;
+            cp_async16(stage + r * kPitch + piece_at(p, r), src);
+        }
+    }
+};
+
+__device__ __forceinline__ unsigned chunk_column(const TileChunk *ch, int lane, int n_cols) {
+#if SLA_DEBUG_BOUNDS
+    return (unsigned)SLA_IDX(__ldg(ch->col + (lane & 15)), n_cols, kBndColumn);
+#else
+    (void)n_cols;
+    return (unsigned)__ldg(ch->col + (lane & 15));
+#endif
 }
 
 // Entry range of row r of the tile in the item (every lane r < 16 its own row).
@@ -508,113 +612,155 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
     }
 }
 
-template <typename T, int D, bool VALS>
+// H heads a warp, on KH key heads (H: one each; 1: one for all).
+template <typename T, int D, int H, int KH, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid_constant__ AttnArgs a) {
+    using R = Ring<D, KH, false>;
+    extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const unsigned share = (unsigned)(a.heads / a.kv_heads), n_y = (unsigned)a.batch * a.kv_heads;
+    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, share)) return;
-        Own<D> q;
-        q.load(static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
-        const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2] + c * (D / 4);
-        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2] + g * (D / 8);
-        Sums<T, D> acc;
-        acc.zero();
-        float m[2] = {none, none}, l[2] = {0.0f, 0.0f};
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
+        const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
+        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
+        const int n = (int)(w.ch1 - w.ch0);
+        auto issue = [&](int i, unsigned col) {
+            char *st = ring + i % R::kStages * R::kStage;
+            R::gather(st, kb, kst, a.ks[2], col, lane);
+            R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
+        };
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < R::kStages - 1; ++i) {
+            if (i < n) issue(i, chunk_column(w.ch0 + i, lane, a.n_cols));
+            cp_commit();
+        }
+        unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
+        Own<D> q[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h + j) * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
+        Sums<T, D> acc[H];
+        float m[H][2], l[H][2];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            acc[j].zero();
+            m[j][0] = m[j][1] = none;
+            l[j][0] = l[j][1] = 0.0f;
+        }
         Chunk<VALS> next;
-        if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_cols);
-        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
+        if (n > 0) next.load(w.ch0, g);
+        for (int ch = 0; ch < n; ++ch) {
             const Chunk<VALS> cur = next;
-            uint32_t k[2][D / 8], v[4][D / 16];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) load_words<D / 8>(k[i], row_at(kb, cur.kc[i], kst));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) load_words<D / 16>(v[i], row_at(vb, cur.vc[i], vst));
-            if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_cols);
-            float s[2][4];
-            score_products<T, D>(s, q, k);
-            float top[2] = {m[0], m[1]};
-            unsigned used = 0;
+            cp_wait<R::kStages - 2>();
+            __syncwarp();
+            if (ch + R::kStages - 1 < n) issue(ch + R::kStages - 1, col);
+            cp_commit();
+            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
+            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+            const char *stage = ring + ch % R::kStages * R::kStage;
+            // score term and presence of the pairs (row g + 8 (e / 2), column 8 blk + 2c + e % 2)
             const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
+            bool on[2][4];
+            float x[2][4];
+            unsigned used = 0;
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {           // row g + 8 (e / 2), column 8 blk + 2c + e % 2
-                    const int i = e >> 1;
-                    bool on = mine[i] & (1u << (8 * blk + (e & 1)));
-                    if constexpr (VALS) {
-                        float x = 0.0f;
-                        if (on)
-                            x = load_value<float>(a.vals, a.vals_f64,
-                                                  w.b * a.nnz + cur.entry(i, 8 * blk + 2 * c + (e & 1)));
-                        on = on && x != none;
-                        used |= (unsigned)on << (2 * blk + (e & 1));
-                        s[blk][e] = fmaf(s[blk][e], scale, value_log2(x));
-                    } else {
-                        s[blk][e] *= scale;
-                    }
-                    s[blk][e] = on ? s[blk][e] : none;
-                    top[i] = fmaxf(top[i], s[blk][e]);
-                }
-            if constexpr (VALS) drop_unused(v, used);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-                top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
-            }
-            const float ref[2] = {top[0] == none ? 0.0f : top[0], top[1] == none ? 0.0f : top[1]};
-            if (__any_sync(kAll, top[0] != m[0] || top[1] != m[1])) {
-                const float f0 = exp2_of(m[0] - ref[0]), f1 = exp2_of(m[1] - ref[1]);
-                acc.scale(f0, f1);
-                l[0] *= f0;
-                l[1] *= f1;
-                m[0] = top[0];
-                m[1] = top[1];
-            }
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk) {
-#pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s[blk][e] = exp2_of(s[blk][e] - ref[e >> 1]);
-                    l[e >> 1] += s[blk][e];
+                    on[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
+                    if constexpr (VALS) {
+                        x[blk][e] = 0.0f;
+                        if (on[blk][e])
+                            x[blk][e] = load_value<float>(a.vals, a.vals_f64,
+                                                          w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
+                        on[blk][e] = on[blk][e] && x[blk][e] != none;
+                        used |= (unsigned)on[blk][e] << (2 * blk + (e & 1));
+                        x[blk][e] = value_log2(x[blk][e]);
+                    }
                 }
-                acc.add(s[blk], v[2 * blk], v[2 * blk + 1]);
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                const int p0 = KH == 1 ? 0 : j * (D / 8);
+                float s[2][4];
+                score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
+                float top[2] = {m[j][0], m[j][1]};
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (VALS) s[blk][e] = fmaf(s[blk][e], scale, x[blk][e]);
+                        else s[blk][e] *= scale;
+                        s[blk][e] = on[blk][e] ? s[blk][e] : none;
+                        top[e >> 1] = fmaxf(top[e >> 1], s[blk][e]);
+                    }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
+                    top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+                }
+                const float ref[2] = {top[0] == none ? 0.0f : top[0], top[1] == none ? 0.0f : top[1]};
+                if (__any_sync(kAll, top[0] != m[j][0] || top[1] != m[j][1])) {
+                    const float f0 = exp2_of(m[j][0] - ref[0]), f1 = exp2_of(m[j][1] - ref[1]);
+                    acc[j].scale(f0, f1);
+                    l[j][0] *= f0;
+                    l[j][1] *= f1;
+                    m[j][0] = top[0];
+                    m[j][1] = top[1];
+                }
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[blk][e] = exp2_of(s[blk][e] - ref[e >> 1]);
+                        l[j][e >> 1] += s[blk][e];
+                    }
+                acc[j].template add_chunk<R::kPitch, VALS>(s, stage + R::kTensor, p0, g, c, used);
             }
         }
-        if (acc.bad()) {
-            slow_forward<T>(a, w);
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < H; ++j) bad = acc[j].bad() || bad;
+        if (bad) {
+            for (int j = 0; j < H; ++j) {
+                TileWork one = w;
+                one.h = w.h + j;
+                one.kh = KH == 1 ? w.kh : w.kh + j;
+                slow_forward<T>(a, one);
+            }
             continue;
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            l[i] += __shfl_xor_sync(kAll, l[i], 1);
-            l[i] += __shfl_xor_sync(kAll, l[i], 2);
-            m[i] *= kLn2;
-        }
-        if (w.slot < 0) acc.scale(l[0] > 0.0f ? 1.0f / l[0] : 0.0f, l[1] > 0.0f ? 1.0f / l[1] : 0.0f);
+        for (int j = 0; j < H; ++j) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            if (w.row0 + r >= a.n_rows) continue;
-            if (w.slot < 0) {
-                const int64_t o = ((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h;
-                acc.store(static_cast<T *>(a.out) + o * D, i, c);
-                if (a.wide) acc.store(static_cast<float *>(a.wide) + o * D, i, c);
-                if (c == 0) static_cast<float *>(a.lse)[o] = l[i] == 0.0f ? none : m[i] + logf(l[i]);
-            } else {
-                float *p = static_cast<float *>(a.part) +
-                           part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h) * (D + 2);
+            for (int i = 0; i < 2; ++i) {
+                l[j][i] += __shfl_xor_sync(kAll, l[j][i], 1);
+                l[j][i] += __shfl_xor_sync(kAll, l[j][i], 2);
+                m[j][i] *= kLn2;
+            }
+            if (w.slot < 0)
+                acc[j].scale(l[j][0] > 0.0f ? 1.0f / l[j][0] : 0.0f, l[j][1] > 0.0f ? 1.0f / l[j][1] : 0.0f);
 #pragma unroll
-                for (int nb = 0; nb < D / 8; ++nb) {    // D + 2 numbers a partial: not on 16 bytes
-                    p[c * (D / 4) + nb] = acc.o[nb][2 * i];
-                    p[c * (D / 4) + D / 8 + nb] = acc.o[nb][2 * i + 1];
-                }
-                if (c == 0) {
-                    p[D] = m[i];
-                    p[D + 1] = l[i];
+            for (int i = 0; i < 2; ++i) {
+                const int r = g + 8 * i;
+                if (w.row0 + r >= a.n_rows) continue;
+                if (w.slot < 0) {
+                    const int64_t o = ((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h + j;
+                    acc[j].store(static_cast<T *>(a.out) + o * D, i, c);
+                    if (a.wide) acc[j].store(static_cast<float *>(a.wide) + o * D, i, c);
+                    if (c == 0) static_cast<float *>(a.lse)[o] = l[j][i] == 0.0f ? none : m[j][i] + logf(l[j][i]);
+                } else {
+                    float *p = static_cast<float *>(a.part) +
+                               part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h + j) * (D + 2);
+                    acc[j].store_odd(p, i, c);          // D + 2 numbers a partial
+                    if (c == 0) {
+                        p[D] = m[j][i];
+                        p[D + 1] = l[j][i];
+                    }
                 }
             }
         }
@@ -664,110 +810,138 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
 }
 
 // By A's rows: (lse, D) of every row, dq, and ds of every entry if asked for.
-template <typename T, int D, bool VALS>
+template <typename T, int D, int H, int KH, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a) {
+    using R = Ring<D, KH, false>;
+    extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const unsigned share = (unsigned)(a.heads / a.kv_heads), n_y = (unsigned)a.batch * a.kv_heads;
+    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, share)) return;
-        Own<D> q, go;
-        q.load(static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
-        go.load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + w.h * a.ds[2], a.ds[1], w.row0, a.n_rows, g, c);
-        float lse[2] = {none, none}, delta[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t row = w.row0 + g + 8 * i;
-            if (row < a.n_rows) {
-                const int64_t at = ((int64_t)w.b * a.n_rows + row) * a.heads + w.h;
-                lse[i] = __ldg(static_cast<const float *>(a.lse) + at);
-                uint32_t o[D / 4];
-                load_words<D / 4>(o, static_cast<const float *>(a.o) + at * D + c * (D / 4));
-#pragma unroll
-                for (int s = 0; s < D / 16; ++s)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        uint32_t lo, hi;
-                        widen<T>(go.a[s][2 * e + i], lo, hi);
-                        delta[i] = fmaf(__uint_as_float(lo), __uint_as_float(o[4 * s + 2 * e]), delta[i]);
-                        delta[i] = fmaf(__uint_as_float(hi), __uint_as_float(o[4 * s + 2 * e + 1]), delta[i]);
-                    }
-            }
-            delta[i] += __shfl_xor_sync(kAll, delta[i], 1);
-            delta[i] += __shfl_xor_sync(kAll, delta[i], 2);
-            if (row < a.n_rows && c == 0)
-                a.stat[((int64_t)w.b * a.heads + w.h) * a.n_rows + row] = make_float2(lse[i] * kLog2e, delta[i]);
-        }
-        const bool dead[2] = {lse[0] == none, lse[1] == none};
-        lse[0] *= kLog2e;
-        lse[1] *= kLog2e;
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
         const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
-        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2] + c * (D / 4);
-        float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
-        Sums<T, D> acc;
-        acc.zero();
-        Chunk<VALS> next;
-        if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_cols);
-        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
-            const Chunk<VALS> cur = next;
-            float s[2][4], dp[2][4];
-            uint32_t x[4][D / 16];
-            {
-                uint32_t k[2][D / 8], v[2][D / 8];
+        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
+        const int n = (int)(w.ch1 - w.ch0);
+        auto issue = [&](int i, unsigned col) {
+            char *st = ring + i % R::kStages * R::kStage;
+            R::gather(st, kb, kst, a.ks[2], col, lane);
+            R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
+        };
+        __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    load_words<D / 8>(k[i], row_at(kb + c * (D / 4), cur.kc[i], kst));
-                    load_words<D / 8>(v[i], row_at(vb, cur.kc[i], vst));
+        for (int i = 0; i < R::kStages - 1; ++i) {
+            if (i < n) issue(i, chunk_column(w.ch0 + i, lane, a.n_cols));
+            cp_commit();
+        }
+        unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
+        Own<D> q[H], go[H];
+        float lse[H][2], delta[H][2];
+        bool dead[H][2];
+        Sums<T, D> acc[H];
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+            const int h = w.h + j;
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
+            go[j].load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], a.ds[1], w.row0, a.n_rows, g, c);
+            acc[j].zero();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t row = w.row0 + g + 8 * i, at = ((int64_t)w.b * a.n_rows + row) * a.heads + h;
+                lse[j][i] = none;
+                delta[j][i] = 0.0f;
+                if (row < a.n_rows) {
+                    lse[j][i] = __ldg(static_cast<const float *>(a.lse) + at);
+                    delta[j][i] = go[j].template dot<T>(static_cast<const float *>(a.o) + at * D, i, c);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) load_words<D / 16>(x[i], row_at(kb + g * (D / 8), cur.vc[i], kst));
-                if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_cols);
-                score_products<T, D>(s, q, k);
-                score_products<T, D>(dp, go, v);
+                delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 1);
+                delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 2);
+                dead[j][i] = lse[j][i] == none;
+                lse[j][i] *= kLog2e;
+                if (row < a.n_rows && c == 0)
+                    a.stat[((int64_t)w.b * a.heads + h) * a.n_rows + row] = make_float2(lse[j][i], delta[j][i]);
             }
-            unsigned used = 0;
+        }
+        float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
+        Chunk<VALS> next;
+        if (n > 0) next.load(w.ch0, g);
+        for (int ch = 0; ch < n; ++ch) {
+            const Chunk<VALS> cur = next;
+            cp_wait<R::kStages - 2>();
+            __syncwarp();
+            if (ch + R::kStages - 1 < n) issue(ch + R::kStages - 1, col);
+            cp_commit();
+            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
+            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+            const char *stage = ring + ch % R::kStages * R::kStage;
             const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
+            bool there[2][4];
+            float x[2][4];
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int i = e >> 1;
-                    const bool there = mine[i] & (1u << (8 * blk + (e & 1)));
-                    bool on = there && !dead[i];
-                    if constexpr (VALS) {
-                        float val = 0.0f;
-                        const int t = cur.entry(i, 8 * blk + 2 * c + (e & 1));
-                        if (there) val = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + t);
-                        on = on && val != none;
-                        used |= (unsigned)on << (2 * blk + (e & 1));
-                        s[blk][e] = fmaf(s[blk][e], scale, value_log2(val)) - lse[i];
-                        s[blk][e] = on ? exp2_of(s[blk][e]) * (dp[blk][e] - delta[i]) : 0.0f;
-                        if (ds_out && there) ds_out[t] = s[blk][e];
-                    } else {
-                        s[blk][e] = on ? exp2_of(fmaf(s[blk][e], scale, -lse[i])) * (dp[blk][e] - delta[i]) : 0.0f;
-                    }
+                    there[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
+                    x[blk][e] = 0.0f;
+                    if (VALS && there[blk][e])
+                        x[blk][e] = load_value<float>(a.vals, a.vals_f64,
+                                                      w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
                 }
-            if constexpr (VALS) drop_unused(x, used);
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk) acc.add(s[blk], x[2 * blk], x[2 * blk + 1]);
+            for (int j = 0; j < H; ++j) {
+                const int p0 = KH == 1 ? 0 : j * (D / 8);
+                float s[2][4], dp[2][4];
+                score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
+                score_products<T, D, R::kPitch>(dp, go[j], stage + R::kTensor, p0, g, c);
+                unsigned used = 0;
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = e >> 1;
+                        const bool on = there[blk][e] && !dead[j][i] && (!VALS || x[blk][e] != none);
+                        if constexpr (VALS) {
+                            used |= (unsigned)on << (2 * blk + (e & 1));
+                            s[blk][e] = fmaf(s[blk][e], scale, value_log2(x[blk][e])) - lse[j][i];
+                        } else {
+                            s[blk][e] = fmaf(s[blk][e], scale, -lse[j][i]);
+                        }
+                        s[blk][e] = on ? exp2_of(s[blk][e]) * (dp[blk][e] - delta[j][i]) : 0.0f;
+                        if (VALS && ds_out && there[blk][e])
+                            ds_out[j * a.nnz + cur.entry(i, 8 * blk + 2 * c + (e & 1))] = s[blk][e];
+                    }
+                acc[j].template add_chunk<R::kPitch, VALS>(s, stage, p0, g, c, used);
+            }
         }
         if (!a.dq) continue;
-        if (acc.bad()) {
-            slow_bwd_rows<T>(a, w);
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < H; ++j) bad = acc[j].bad() || bad;
+        if (bad) {
+            for (int j = 0; j < H; ++j) {
+                TileWork one = w;
+                one.h = w.h + j;
+                one.kh = KH == 1 ? w.kh : w.kh + j;
+                slow_bwd_rows<T>(a, one);
+            }
             continue;
         }
-        acc.scale((float)a.scale, (float)a.scale);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            if (w.row0 + r >= a.n_rows) continue;
-            if (w.slot < 0)
-                acc.store(static_cast<T *>(a.dq) + (((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h) * D, i, c);
-            else
-                acc.store(static_cast<float *>(a.part) +
-                              part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h) * D, i, c);
+        for (int j = 0; j < H; ++j) {
+            acc[j].scale((float)a.scale, (float)a.scale);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = g + 8 * i;
+                if (w.row0 + r >= a.n_rows) continue;
+                if (w.slot < 0)
+                    acc[j].store(static_cast<T *>(a.dq) +
+                                     (((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h + j) * D, i, c);
+                else
+                    acc[j].store(static_cast<float *>(a.part) +
+                                     part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h + j) * D, i, c);
+            }
         }
     }
 }
@@ -821,141 +995,211 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
     }
 }
 
-// By A^T's rows: dk (DK) and dv (DV) of 16 columns of A, the shared heads one
-// after the other.  Wide heads take two launches: both sums and both own
-// operands would not fit the registers.
-template <typename T, int D, bool DK, bool DV, bool VALS>
+// By A^T's rows: dk (DK) and dv (DV) of 16 columns of A for KH key heads, the
+// query heads that share one following each other.  Wide heads take two launches:
+// both sums and both own operands would not fit the registers.  The values come in
+// A^T's order and units of log 2 (tile_values_kernel).
+template <typename T, int D, int KH, bool DK, bool DV, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a) {
+    using R = Ring<D, KH, true>;
+    extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    const unsigned n_y = (unsigned)a.batch * a.kv_heads;
+    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
     const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, 1)) return;
-        Own<D> k, v;
-        k.load(static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2], a.ks[1], w.row0, a.n_cols, g, c);
-        if constexpr (DK)
-            v.load(static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2], a.vs[1], w.row0, a.n_cols, g, c);
-        Sums<T, D> dk, dv;
-        if constexpr (DK) dk.zero();
-        if constexpr (DV) dv.zero();
-        for (int h = w.kh * share; h < (w.kh + 1) * share; ++h) {
-            const T *qb = static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2];
-            const T *gb = static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2];
-            const float2 *stat = a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows;
-            Chunk<VALS> next;
-            if (w.ch0 < w.ch1) next.load(w.ch0, g, c, a.n_rows);
-            for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) {
-                const Chunk<VALS> cur = next;
-                float s[2][4], dp[2][4];
-                float2 st[4];
-                {
-                    uint32_t x[2][D / 8], z[2][D / 8];
+        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, KH, KH, 1)) return;
+        Own<D> k[KH], v[DK ? KH : 1];
+        Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        load_words<D / 8>(x[i], row_at(qb + c * (D / 4), cur.kc[i], qst));
-                        if constexpr (DK) load_words<D / 8>(z[i], row_at(gb + c * (D / 4), cur.kc[i], dst));
+        for (int j = 0; j < KH; ++j) {
+            k[j].load(static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.kh + j) * a.ks[2], a.ks[1], w.row0, a.n_cols, g, c);
+            if constexpr (DK) {
+                v[j].load(static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.kh + j) * a.vs[2], a.vs[1], w.row0, a.n_cols, g, c);
+                dk[j].zero();
+            }
+            if constexpr (DV) dv[j].zero();
+        }
+        const int n = (int)(w.ch1 - w.ch0), total = n * share;
+        // step x: chunk x % n of the query heads kh * share + x / n (KH > 1: share is 1)
+        auto issue = [&](int x, unsigned col) {
+            char *st = ring + x % R::kStages * R::kStage;
+            const int h = w.kh * share + (KH == 1 ? x / n : 0);
+            R::gather(st, static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, a.qs[2], col, lane);
+            R::gather(st + R::kTensor, static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, a.ds[2], col, lane);
+            const float2 *stat = a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows + col;
+#pragma unroll
+            for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
+                const int jj = KH == 1 ? 0 : j + (lane >> 4);
+                if (KH > 1 || lane < 16)
+                    cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8, stat + (int64_t)jj * a.n_rows);
+            }
+        };
+        auto chunk = [&](int x) { return w.ch0 + (KH == 1 ? x % n : x); };
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < R::kStages - 1; ++i) {
+            if (i < total) issue(i, chunk_column(chunk(i), lane, a.n_rows));
+            cp_commit();
+        }
+        unsigned col = R::kStages - 1 < total ? chunk_column(chunk(R::kStages - 1), lane, a.n_rows) : 0;
+        Chunk<VALS> next;
+        if (total > 0) next.load(w.ch0, g);
+        for (int x = 0; x < total; ++x) {
+            const Chunk<VALS> cur = next;
+            cp_wait<R::kStages - 2>();
+            __syncwarp();
+            if (x + R::kStages - 1 < total) issue(x + R::kStages - 1, col);
+            cp_commit();
+            if (x + R::kStages < total) col = chunk_column(chunk(x + R::kStages), lane, a.n_rows);
+            if (x + 1 < total) next.load(chunk(x + 1), g);
+            const char *stage = ring + x % R::kStages * R::kStage;
+            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
+            bool on[2][4];
+            float val[2][4];
+            unsigned used = 0;
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    on[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
+                    if constexpr (VALS) {
+                        val[blk][e] = none;
+                        if (on[blk][e])
+                            val[blk][e] = __ldg(a.vals_t + w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
+                        on[blk][e] = on[blk][e] && val[blk][e] != none;
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) st[i] = stat[cur.vc[i]];
-                    if (ch + 1 < w.ch1) next.load(ch + 1, g, c, a.n_rows);
-                    score_products<T, D>(s, k, x);
-                    if constexpr (DK) score_products<T, D>(dp, v, z);
                 }
-                unsigned used = 0;
-                const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
+            for (int j = 0; j < KH; ++j) {
+                const int p0 = j * (D / 8);
+                float s[2][4], dp[2][4];
+                score_products<T, D, R::kPitch>(s, k[j], stage, p0, g, c);
+                if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], stage + R::kTensor, p0, g, c);
+                const float4 *sp = reinterpret_cast<const float4 *>(stage + 2 * R::kTensor + j * 128);
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk) {
+                    const float4 st = sp[4 * blk + c];              // (lse, D) of the columns 2c and 2c + 1
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = e >> 1, j = 2 * blk + (e & 1);
-                        bool on = mine[i] & (1u << (8 * blk + (e & 1)));
-                        float val = 0.0f;
+                        const float lse = e & 1 ? st.z : st.x, delta = e & 1 ? st.w : st.y;
+                        const bool live = on[blk][e] && lse != none;
                         if constexpr (VALS) {
-                            if (on) {
-                                const int64_t at = SLA_IDX((int64_t)__ldg(a.perm + cur.entry(i, 8 * blk + 2 * c + (e & 1))),
-                                                           a.nnz, kBndEntry);
-                                val = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + at);
-                            }
+                            used |= (unsigned)live << (2 * blk + (e & 1));
+                            s[blk][e] = fmaf(s[blk][e], scale, val[blk][e]) - lse;
+                        } else {
+                            s[blk][e] = fmaf(s[blk][e], scale, -lse);
                         }
-                        on = on && val != none && st[j].x != none;
-                        if constexpr (VALS) used |= (unsigned)on << j;
-                        s[blk][e] = on ? exp2_of(fmaf(s[blk][e], scale, value_log2(val)) - st[j].x) : 0.0f;
-                        if constexpr (DK) dp[blk][e] = on ? s[blk][e] * (dp[blk][e] - st[j].y) : 0.0f;
+                        s[blk][e] = live ? exp2_of(s[blk][e]) : 0.0f;
+                        if constexpr (DK) dp[blk][e] = live ? s[blk][e] * (dp[blk][e] - delta) : 0.0f;
                     }
-                uint32_t x[4][D / 16];
-                if constexpr (DV) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], row_at(gb + g * (D / 8), cur.vc[j], dst));
-                    if constexpr (VALS) drop_unused(x, used);
-                    dv.add(s[0], x[0], x[1]);
-                    dv.add(s[1], x[2], x[3]);
                 }
-                if constexpr (DK) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) load_words<D / 16>(x[j], row_at(qb + g * (D / 8), cur.vc[j], qst));
-                    if constexpr (VALS) drop_unused(x, used);
-                    dk.add(dp[0], x[0], x[1]);
-                    dk.add(dp[1], x[2], x[3]);
-                }
+                if constexpr (DV) dv[j].template add_chunk<R::kPitch, VALS>(s, stage + R::kTensor, p0, g, c, used);
+                if constexpr (DK) dk[j].template add_chunk<R::kPitch, VALS>(dp, stage, p0, g, c, used);
             }
         }
         bool bad = false;
-        if constexpr (DK) bad = dk.bad();
-        if constexpr (DV) bad = dv.bad() || bad;
+#pragma unroll
+        for (int j = 0; j < KH; ++j) {
+            if constexpr (DK) bad = dk[j].bad() || bad;
+            if constexpr (DV) bad = dv[j].bad() || bad;
+        }
         if (bad) {
-            slow_bwd_cols<T>(a, w, DK, DV);
+            for (int j = 0; j < KH; ++j) {
+                TileWork one = w;
+                one.kh = w.kh + j;
+                slow_bwd_cols<T>(a, one, DK, DV);
+            }
             continue;
         }
-        if constexpr (DK) dk.scale((float)a.scale, (float)a.scale);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = g + 8 * i;
-            if (w.row0 + r >= a.n_cols) continue;
-            if (w.slot < 0) {
-                const int64_t o = (((int64_t)w.b * a.n_cols + w.row0 + r) * a.kv_heads + w.kh) * D;
-                if constexpr (DK)
-                    if (a.dk) dk.store(static_cast<T *>(a.dk) + o, i, c);
-                if constexpr (DV)
-                    if (a.dv) dv.store(static_cast<T *>(a.dv) + o, i, c);
-            } else {
-                float *p = static_cast<float *>(a.part) +
-                           part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.kv_heads, w.kh) * 2 * D;
-                if constexpr (DK) dk.store(p, i, c);
-                if constexpr (DV) dv.store(p + D, i, c);
+        for (int j = 0; j < KH; ++j) {
+            if constexpr (DK) dk[j].scale((float)a.scale, (float)a.scale);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = g + 8 * i;
+                if (w.row0 + r >= a.n_cols) continue;
+                if (w.slot < 0) {
+                    const int64_t o = (((int64_t)w.b * a.n_cols + w.row0 + r) * a.kv_heads + w.kh + j) * D;
+                    if constexpr (DK)
+                        if (a.dk) dk[j].store(static_cast<T *>(a.dk) + o, i, c);
+                    if constexpr (DV)
+                        if (a.dv) dv[j].store(static_cast<T *>(a.dv) + o, i, c);
+                } else {
+                    float *p = static_cast<float *>(a.part) +
+                               part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.kv_heads, w.kh + j) * 2 * D;
+                    if constexpr (DK) dk[j].store(p, i, c);
+                    if constexpr (DV) dv[j].store(p + D, i, c);
+                }
             }
         }
     }
+}
+
+// The values in A^T's order and units of log 2.
+__global__ void __launch_bounds__(256)
+tile_values_kernel(int64_t nnz, int batch, const int32_t *__restrict__ perm, const void *vals, int f64,
+                   float *__restrict__ out) {
+    const int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (t >= nnz) return;
+    const int64_t e = SLA_IDX((int64_t)__ldg(perm + t), nnz, kBndEntry);
+    for (int b = 0; b < batch; ++b) out[b * nnz + t] = value_log2(load_value<float>(vals, f64, b * nnz + e));
 }
 
 // -------------------------------------------------------------- launches ----
 enum { kTileFwd, kTileBwdRows, kTileBwdCols };
 
-template <typename T, int D, bool VALS>
+// H heads a warp on KH key heads; for the columns KH of them.
+template <typename T, int D, int H, int KH, bool VALS>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
-    const int64_t warps = (int64_t)a.n_items * (what == kTileBwdCols ? 1 : a.heads / a.kv_heads);
-    const int64_t x = (warps + kTileWarps - 1) / kTileWarps, y = (int64_t)a.batch * a.kv_heads;
+    const bool cols = what == kTileBwdCols;
+    const int64_t warps = (int64_t)a.n_items * (cols ? 1 : a.heads / a.kv_heads * KH / H);
+    const int64_t x = (warps + kTileWarps - 1) / kTileWarps, y = (int64_t)a.batch * (a.kv_heads / KH);
     SLA_REQUIRE(x < INT_MAX / kTileWarps && y < INT_MAX, "sla_attention: too many rows, systems and heads");
     if (x == 0) return SLA_OK;
     const dim3 grid((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
-    if (what == kTileFwd) {
-        tile_forward_kernel<T, D, VALS><<<grid, kTileThreads, 0, s>>>(a);
-    } else if (what == kTileBwdRows) {
-        tile_bwd_rows_kernel<T, D, VALS><<<grid, kTileThreads, 0, s>>>(a);
-    } else if constexpr (D <= 64) {
-        tile_bwd_cols_kernel<T, D, true, true, VALS><<<grid, kTileThreads, 0, s>>>(a);
-    } else {
-        if (a.dv) tile_bwd_cols_kernel<T, D, false, true, VALS><<<grid, kTileThreads, 0, s>>>(a);
-        if (a.dk) tile_bwd_cols_kernel<T, D, true, false, VALS><<<grid, kTileThreads, 0, s>>>(a);
+    auto go = [&](auto *kernel, int ring) -> sla_status {
+        const int bytes = ring * kTileWarps;
+        if (bytes > 48 * 1024)
+            SLA_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+        kernel<<<grid, kTileThreads, bytes, s>>>(a);
+        SLA_CHECK_LAUNCH();
+        return SLA_OK;
+    };
+    if (what == kTileFwd) return go(tile_forward_kernel<T, D, H, KH, VALS>, Ring<D, KH, false>::kBytes);
+    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, H, KH, VALS>, Ring<D, KH, false>::kBytes);
+    if constexpr (H == KH) {
+        constexpr int bytes = Ring<D, KH, true>::kBytes;
+        if constexpr (D * KH <= 64) {
+            return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS>, bytes);
+        } else {
+            sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS>, bytes) : SLA_OK;
+            if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS>, bytes);
+            return st;
+        }
     }
-    SLA_CHECK_LAUNCH();
-    return SLA_OK;
+    return SLA_ERR_UNSUPPORTED;
+}
+
+// Heads a warp: as many as fill 128 bytes of a gathered row, if their number
+// allows; two that share a key head while their sums fit the registers.
+template <typename T, int D, bool VALS>
+sla_status launch_tile_heads(int what, const AttnArgs &a, cudaStream_t s) {
+    const int share = a.heads / a.kv_heads;
+    if constexpr (D <= 32) {
+        constexpr int K = 64 / D;
+        if (share == 1 && a.kv_heads % K == 0) return launch_tile<T, D, K, K, VALS>(what, a, s);
+    }
+    if constexpr (D <= 64)
+        if (what != kTileBwdCols && share % 2 == 0) return launch_tile<T, D, 2, 1, VALS>(what, a, s);
+    return launch_tile<T, D, 1, 1, VALS>(what, a, s);
 }
 
 template <typename T, int D>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
-    return a.vals ? launch_tile<T, D, true>(what, a, s) : launch_tile<T, D, false>(what, a, s);
+    return a.vals ? launch_tile_heads<T, D, true>(what, a, s) : launch_tile_heads<T, D, false>(what, a, s);
 }
 
 template <typename T>
@@ -1017,6 +1261,10 @@ template <typename T> sla_status attn_tile_bwd_rows(const AttnArgs &a, cudaStrea
     return launch_tile_of<T>(kTileBwdRows, a, s);
 }
 template <typename T> sla_status attn_tile_bwd_cols(const AttnArgs &a, cudaStream_t s) {
+    if (a.vals && a.nnz > 0) {
+        tile_values_kernel<<<blocks_of(a.nnz), 256, 0, s>>>(a.nnz, a.batch, a.perm, a.vals, a.vals_f64, a.vals_t);
+        SLA_CHECK_LAUNCH();
+    }
     return launch_tile_of<T>(kTileBwdCols, a, s);
 }
 template sla_status attn_tile_forward<__nv_bfloat16>(const AttnArgs &, cudaStream_t);
