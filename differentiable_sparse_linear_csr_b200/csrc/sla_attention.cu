@@ -858,8 +858,8 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
 // Workspace pieces: what the backward keeps for every entry (row kernels) or
 // row (tile kernels), then the partial sums of split rows.
 struct AttnWs {
-    size_t pds = 0, stat = 0, ds = 0, vals_t = 0, part = 0;
-    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(vals_t) + align_up(part); }
+    size_t pds = 0, stat = 0, ds = 0, vals_w = 0, part = 0;
+    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(vals_w) + align_up(part); }
 };
 
 const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
@@ -871,13 +871,14 @@ AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
     AttnWs w;
     if (!backward) {
+        if (attn_tiled(o) && h->dtype == SLA_F64) w.vals_w = B * (size_t)h->nnz * sizeof(float);
         w.part = B * p.n_slots * p.rows * H * (D + 2) * acc;
         return w;
     }
     if (attn_tiled(o)) {
         w.stat = B * H * (size_t)h->n_rows * sizeof(float2);
         w.ds = B * H * (size_t)h->nnz * sizeof(float);
-        w.vals_t = B * (size_t)h->nnz * sizeof(float);
+        w.vals_w = B * (size_t)h->nnz * sizeof(float);
     } else {
         w.pds = B * (size_t)h->nnz * H * 2 * acc;
     }
@@ -1022,14 +1023,17 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     cudaStream_t s = as_stream(stream);
     st = prepare(h, o, false, s);
     if (st != SLA_OK) return st;
-    const size_t need = attn_ws(h, o, false).total();
+    const AttnWs ww = attn_ws(h, o, false);
+    const size_t need = ww.total();
     SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention: workspace too small (%zu < %zu)", ws_bytes, need);
     SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention: workspace must be 256-byte aligned");
     AttnArgs a = make_args(h, o, q, k, v, vals);
     a.out = out;
     a.wide = out_wide;
     a.lse = lse;
-    a.part = ws;
+    Carver c(ws);
+    a.vals_w = reinterpret_cast<float *>(c.take<char>(ww.vals_w));
+    a.part = c.take<char>(ww.part);
     const AttnPlan &p = plan_of(h, o, false);
     const bool tiled = attn_tiled(o);
     switch (o->dtype) {
@@ -1076,7 +1080,7 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     a.pds = c.take<char>(w.pds);
     a.stat = reinterpret_cast<float2 *>(c.take<char>(w.stat));
     a.ds_out = dvals ? reinterpret_cast<float *>(c.take<char>(w.ds)) : (c.take<char>(w.ds), nullptr);
-    a.vals_t = reinterpret_cast<float *>(c.take<char>(w.vals_t));
+    a.vals_w = reinterpret_cast<float *>(c.take<char>(w.vals_w));
     a.part = c.take<char>(w.part);
     if (!dk && !dv && !dvals) a.pds = nullptr;
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);

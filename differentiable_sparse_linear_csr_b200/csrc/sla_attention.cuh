@@ -82,9 +82,10 @@ struct AttnArgs {
     void *out, *wide, *lse;                // forward (wide: out before its rounding, or null)
     void *dq, *dk, *dv, *dvals;            // backward
     void *pds;                             // row kernels: [B][nnz][heads] pairs (p, ds)
-    float2 *stat;                          // tile kernels: [B][heads][n_rows] pairs (lse, D)
+    float2 *stat;                          // tile kernels: [B][heads][n_rows] pairs (lse, D), lse / log 2 without values
     float *ds_out;                         // tile kernels: [B][heads][nnz] ds, or null
-    float *vals_t;                         // tile kernels: [B][nnz] values in A^T's order
+    float *vals_w;                         // tile kernels: room for [B][nnz] 32-bit values
+    const float *vals_f, *vals_t;          // and the values as they read them, in A's and A^T's order
     void *part;                            // partial sums of split rows
 };
 
@@ -163,9 +164,9 @@ sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int 
 // Tile kernels (sla_attention_tile.cu): plan arrays of a tile plan, and the calls.
 sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s);
-template <typename T> sla_status attn_tile_forward(const AttnArgs &a, cudaStream_t s);
-template <typename T> sla_status attn_tile_bwd_rows(const AttnArgs &a, cudaStream_t s);
-template <typename T> sla_status attn_tile_bwd_cols(const AttnArgs &a, cudaStream_t s);
+template <typename T> sla_status attn_tile_forward(AttnArgs a, cudaStream_t s);
+template <typename T> sla_status attn_tile_bwd_rows(AttnArgs a, cudaStream_t s);
+template <typename T> sla_status attn_tile_bwd_cols(AttnArgs a, cudaStream_t s);
 
 inline unsigned blocks_of(int64_t n, int t = 256) { return (unsigned)((n + t - 1) / t); }
 

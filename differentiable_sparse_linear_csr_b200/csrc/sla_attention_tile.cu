@@ -226,22 +226,31 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 
 __device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
 
-// The main loops hold scores in units of log 2, so that a weight is one
-// exponential of a difference (the hardware's: 2 ulp, results below 2^-126 are
-// zero, which a softmax does not notice).
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// The hardware's exponential: 2 ulp, results below 2^-126 are zero, which a
+// softmax does not notice.
 __device__ __forceinline__ float exp2_of(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// A stored value in those units; a finite one stays finite.
-__device__ __forceinline__ float value_log2(float x) {
-    constexpr float kMost = 2.3e38f;
-    if (x > kMost && x <= FLT_MAX) x = kMost;
-    if (x < -kMost && x >= -FLT_MAX) x = -kMost;
-    return x * kLog2e;
+// Scores less a reference (maximum or lse) in units of log 2.  Without values the
+// factor log2 e is part of `scale` and the references have the same unit: one
+// multiply-add.  Values come in natural units, and the difference is taken before
+// the factor, so that the lowest finite value does not overflow.
+template <bool VALS>
+__device__ __forceinline__ float relative(float dot, float scale, float val, float ref) {
+    if constexpr (VALS) return (fmaf(dot, scale, val) - ref) * kLog2e;
+    else return fmaf(dot, scale, -ref);
 }
+template <bool VALS>
+__device__ __forceinline__ float score_scale(double scale) {
+    return VALS ? (float)scale : (float)(scale * 1.4426950408889634);
+}
+
+// Bits of the pairs (row g + 8 (e / 2), column 8 blk + 2c + e % 2) in a row's
+// bits shifted by 2c.
+__device__ __forceinline__ unsigned pair_bit(int blk, int e) { return 1u << (8 * blk + (e & 1)); }
 
 
 // The tile's own 16 rows as the left operand of score products.
@@ -371,18 +380,18 @@ struct Sums {
             for (int i = 0; i < 4; ++i) b = b || o[nb][i] != o[nb][i];
         return __any_sync(kAll, b);
     }
-    // All of a chunk: the weights w[2][4] with the staged rows.  used: see
+    // All of a chunk: the weights w[2][4] with the staged rows.  drop, used: see
     // drop_unused.
-    template <int PITCH, bool DROP>
+    template <int PITCH>
     __device__ __forceinline__ void add_chunk(const float (&w)[2][4], const char *stage, int p0, int g, int c,
-                                              unsigned used) {
+                                              bool drop, unsigned used) {
         uint32_t x[4][D / 16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int r = 8 * (j >> 1) + 2 * c + (j & 1);
             read_sum<D>(x[j], stage + r * PITCH, r, p0, g);
         }
-        if constexpr (DROP) drop_unused(x, used);
+        if (drop) drop_unused(x, used);
         add(w[0], x[0], x[1]);
         add(w[1], x[2], x[3]);
     }
@@ -476,9 +485,23 @@ struct Chunk {
             at[1] = __ldg(p->start + 8 + g);
         }
     }
-    // Entry of row g + 8 i at position pos (if the row stores it).
-    __device__ __forceinline__ int entry(int i, int pos) const {
-        return at[i] + __popc(bits[i] & ((1u << pos) - 1u));
+    // Entries of rows g and g + 8 at columns 8 blk + 2c (the next column's entry
+    // follows if the row stores both).
+    __device__ __forceinline__ int entry(int i, int blk, int c) const {
+        return at[i] + __popc(bits[i] & ((1u << (8 * blk + 2 * c)) - 1u));
+    }
+    // The stored values of this thread's 8 pairs, 0 where nothing is stored.
+    __device__ __forceinline__ void values(float (&x)[2][4], const float *vals, int c) const {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const unsigned mine = bits[i] >> (2 * c);
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk) {
+                const float *p = vals + entry(i, blk, c);
+                x[blk][2 * i] = mine & pair_bit(blk, 0) ? __ldg(p) : 0.0f;
+                x[blk][2 * i + 1] = mine & pair_bit(blk, 1) ? __ldg(p + (mine >> (8 * blk) & 1)) : 0.0f;
+            }
+        }
     }
 };
 
@@ -621,22 +644,21 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
-    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
         if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
         const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
         const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
         const int n = (int)(w.ch1 - w.ch0);
-        auto issue = [&](int i, unsigned col) {
-            char *st = ring + i % R::kStages * R::kStage;
+        auto issue = [&](char *st, unsigned col) {
             R::gather(st, kb, kst, a.ks[2], col, lane);
             R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
         };
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < n) issue(i, chunk_column(w.ch0 + i, lane, a.n_cols));
+            if (i < n) issue(ring + i * R::kStage, chunk_column(w.ch0 + i, lane, a.n_cols));
             cp_commit();
         }
         unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
@@ -652,74 +674,114 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
             m[j][0] = m[j][1] = none;
             l[j][0] = l[j][1] = 0.0f;
         }
-        Chunk<VALS> next;
+        Chunk<VALS> next, cur;
+        float x_next[2][4] = {};
+        const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
         if (n > 0) next.load(w.ch0, g);
+        if constexpr (VALS) {
+            cur = next;
+            if (n > 0) cur.values(x_next, vals, c);
+            if (n > 1) next.load(w.ch0 + 1, g);
+        }
+        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
         for (int ch = 0; ch < n; ++ch) {
-            const Chunk<VALS> cur = next;
+            // bookkeeping of this chunk, and loads of the next one's
+            float x[2][4];
+            unsigned bits[2];
+            if constexpr (VALS) {
+                bits[0] = cur.bits[0];
+                bits[1] = cur.bits[1];
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
+                cur = next;
+                if (ch + 1 < n) cur.values(x_next, vals, c);
+                if (ch + 2 < n) next.load(w.ch0 + ch + 2, g);
+            } else {
+                bits[0] = next.bits[0];
+                bits[1] = next.bits[1];
+                if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+            }
             cp_wait<R::kStages - 2>();
             __syncwarp();
-            if (ch + R::kStages - 1 < n) issue(ch + R::kStages - 1, col);
+            if (ch + R::kStages - 1 < n) issue(ring + st_write, col);
             cp_commit();
             if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
-            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
-            const char *stage = ring + ch % R::kStages * R::kStage;
-            // score term and presence of the pairs (row g + 8 (e / 2), column 8 blk + 2c + e % 2)
-            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
-            bool on[2][4];
-            float x[2][4];
-            unsigned used = 0;
+            const char *stage = ring + st_read;
+            st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
+            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
+            unsigned mine[2] = {bits[0] >> (2 * c), bits[1] >> (2 * c)}, used = 0;
+            bool drop = false;
+            if constexpr (VALS) {
+                bool out = false;                       // a stored pair that a value of -inf leaves out
 #pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
+                for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    on[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
-                    if constexpr (VALS) {
-                        x[blk][e] = 0.0f;
-                        if (on[blk][e])
-                            x[blk][e] = load_value<float>(a.vals, a.vals_f64,
-                                                          w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
-                        on[blk][e] = on[blk][e] && x[blk][e] != none;
-                        used |= (unsigned)on[blk][e] << (2 * blk + (e & 1));
-                        x[blk][e] = value_log2(x[blk][e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (x[blk][e] == none) {
+                            mine[e >> 1] &= ~pair_bit(blk, e);
+                            out = true;
+                        }
+                drop = __any_sync(kAll, out);
+                if (drop) {
+                    if (!__any_sync(kAll, (mine[0] | mine[1]) & 0x303u)) continue;      // nothing left
+                    used = (mine[0] | mine[1]) & 0x303u;
+                    used = (used | used >> 6) & 15u;
                 }
+            }
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 const int p0 = KH == 1 ? 0 : j * (D / 8);
-                float s[2][4];
+                float s[2][4], t[2][4], far = none;
                 score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
-                float top[2] = {m[j][0], m[j][1]};
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if constexpr (VALS) s[blk][e] = fmaf(s[blk][e], scale, x[blk][e]);
-                        else s[blk][e] *= scale;
-                        s[blk][e] = on[blk][e] ? s[blk][e] : none;
-                        top[e >> 1] = fmaxf(top[e >> 1], s[blk][e]);
+                        t[blk][e] = relative<VALS>(s[blk][e], scale, x[blk][e], m[j][e >> 1]);
+                        t[blk][e] = mine[e >> 1] & pair_bit(blk, e) ? t[blk][e] : none;
+                        far = fmaxf(far, t[blk][e]);
                     }
+                // The reference moves only when a score is 2^8 above it (or the first of
+                // its row): any reference near the maximum does, and most chunks skip this.
+                if (__any_sync(kAll, far > 8.0f)) {
+                    float top[2] = {m[j][0], m[j][1]};
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-                    top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
-                }
-                const float ref[2] = {top[0] == none ? 0.0f : top[0], top[1] == none ? 0.0f : top[1]};
-                if (__any_sync(kAll, top[0] != m[j][0] || top[1] != m[j][1])) {
-                    const float f0 = exp2_of(m[j][0] - ref[0]), f1 = exp2_of(m[j][1] - ref[1]);
+                    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float u = relative<false>(s[blk][e], scale, 0.0f, VALS ? -x[blk][e] : 0.0f);
+                            top[e >> 1] = fmaxf(top[e >> 1], mine[e >> 1] & pair_bit(blk, e) ? u : none);
+                        }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
+                        top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+                    }
+                    const float f0 = m[j][0] == none ? 0.0f : exp2_of((m[j][0] - top[0]) * (VALS ? kLog2e : 1.0f));
+                    const float f1 = m[j][1] == none ? 0.0f : exp2_of((m[j][1] - top[1]) * (VALS ? kLog2e : 1.0f));
                     acc[j].scale(f0, f1);
                     l[j][0] *= f0;
                     l[j][1] *= f1;
                     m[j][0] = top[0];
                     m[j][1] = top[1];
+#pragma unroll
+                    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            t[blk][e] = relative<VALS>(s[blk][e], scale, x[blk][e], m[j][e >> 1]);
+                            t[blk][e] = mine[e >> 1] & pair_bit(blk, e) ? t[blk][e] : none;
+                        }
                 }
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[blk][e] = exp2_of(s[blk][e] - ref[e >> 1]);
+                        s[blk][e] = exp2_of(t[blk][e]);
                         l[j][e >> 1] += s[blk][e];
                     }
-                acc[j].template add_chunk<R::kPitch, VALS>(s, stage + R::kTensor, p0, g, c, used);
+                acc[j].template add_chunk<R::kPitch>(s, stage + R::kTensor, p0, g, c, VALS && drop, used);
             }
         }
         bool bad = false;
@@ -740,7 +802,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
             for (int i = 0; i < 2; ++i) {
                 l[j][i] += __shfl_xor_sync(kAll, l[j][i], 1);
                 l[j][i] += __shfl_xor_sync(kAll, l[j][i], 2);
-                m[j][i] *= kLn2;
+                if constexpr (!VALS) m[j][i] *= kLn2;
             }
             if (w.slot < 0)
                 acc[j].scale(l[j][0] > 0.0f ? 1.0f / l[j][0] : 0.0f, l[j][1] > 0.0f ? 1.0f / l[j][1] : 0.0f);
@@ -818,22 +880,21 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
-    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
         if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
         const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
         const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
         const int n = (int)(w.ch1 - w.ch0);
-        auto issue = [&](int i, unsigned col) {
-            char *st = ring + i % R::kStages * R::kStage;
+        auto issue = [&](char *st, unsigned col) {
             R::gather(st, kb, kst, a.ks[2], col, lane);
             R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
         };
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < n) issue(i, chunk_column(w.ch0 + i, lane, a.n_cols));
+            if (i < n) issue(ring + i * R::kStage, chunk_column(w.ch0 + i, lane, a.n_cols));
             cp_commit();
         }
         unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
@@ -859,60 +920,80 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
                 delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 1);
                 delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 2);
                 dead[j][i] = lse[j][i] == none;
-                lse[j][i] *= kLog2e;
+                if constexpr (!VALS) lse[j][i] *= kLog2e;       // the unit of relative()
                 if (row < a.n_rows && c == 0)
                     a.stat[((int64_t)w.b * a.heads + h) * a.n_rows + row] = make_float2(lse[j][i], delta[j][i]);
             }
         }
         float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
-        Chunk<VALS> next;
+        Chunk<VALS> next, cur;
+        float x_next[2][4] = {};
+        const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
         if (n > 0) next.load(w.ch0, g);
+        if constexpr (VALS)
+            if (n > 0) next.values(x_next, vals, c);
+        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
         for (int ch = 0; ch < n; ++ch) {
-            const Chunk<VALS> cur = next;
-            cp_wait<R::kStages - 2>();
-            __syncwarp();
-            if (ch + R::kStages - 1 < n) issue(ch + R::kStages - 1, col);
-            cp_commit();
-            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
-            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
-            const char *stage = ring + ch % R::kStages * R::kStage;
-            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
-            bool there[2][4];
+            cur = next;
             float x[2][4];
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    there[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
-                    x[blk][e] = 0.0f;
-                    if (VALS && there[blk][e])
-                        x[blk][e] = load_value<float>(a.vals, a.vals_f64,
-                                                      w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
+                for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
+            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+            cp_wait<R::kStages - 2>();
+            __syncwarp();
+            if (ch + R::kStages - 1 < n) issue(ring + st_write, col);
+            cp_commit();
+            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
+            const char *stage = ring + st_read;
+            st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
+            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
+            const unsigned there[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
+            unsigned mine[2] = {there[0], there[1]}, used = 0;
+            bool drop = false;
+            if constexpr (VALS) {
+                bool out = false;
+#pragma unroll
+                for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x[blk][e] == none) {
+                            mine[e >> 1] &= ~pair_bit(blk, e);
+                            out = true;
+                        }
+                drop = __any_sync(kAll, out);
+                if (drop) {
+                    used = (mine[0] | mine[1]) & 0x303u;
+                    used = (used | used >> 6) & 15u;
                 }
+            }
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 const int p0 = KH == 1 ? 0 : j * (D / 8);
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
                 score_products<T, D, R::kPitch>(dp, go[j], stage + R::kTensor, p0, g, c);
-                unsigned used = 0;
+                if (VALS && j == 0 && ch + 1 < n) next.values(x_next, vals, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e >> 1;
-                        const bool on = there[blk][e] && !dead[j][i] && (!VALS || x[blk][e] != none);
-                        if constexpr (VALS) {
-                            used |= (unsigned)on << (2 * blk + (e & 1));
-                            s[blk][e] = fmaf(s[blk][e], scale, value_log2(x[blk][e])) - lse[j][i];
-                        } else {
-                            s[blk][e] = fmaf(s[blk][e], scale, -lse[j][i]);
-                        }
-                        s[blk][e] = on ? exp2_of(s[blk][e]) * (dp[blk][e] - delta[j][i]) : 0.0f;
-                        if (VALS && ds_out && there[blk][e])
-                            ds_out[j * a.nnz + cur.entry(i, 8 * blk + 2 * c + (e & 1))] = s[blk][e];
+                        s[blk][e] = exp2_of(relative<VALS>(s[blk][e], scale, x[blk][e], lse[j][i])) * (dp[blk][e] - delta[j][i]);
+                        s[blk][e] = mine[i] & pair_bit(blk, e) && !dead[j][i] ? s[blk][e] : 0.0f;
                     }
-                acc[j].template add_chunk<R::kPitch, VALS>(s, stage, p0, g, c, used);
+                if (VALS && ds_out) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int blk = 0; blk < 2; ++blk) {
+                            float *p = ds_out + j * a.nnz + cur.entry(i, blk, c);
+                            if (there[i] & pair_bit(blk, 0)) p[0] = s[blk][2 * i];
+                            if (there[i] & pair_bit(blk, 1)) p[there[i] >> (8 * blk) & 1] = s[blk][2 * i + 1];
+                        }
+                }
+                acc[j].template add_chunk<R::kPitch>(s, stage, p0, g, c, VALS && drop, used);
             }
         }
         if (!a.dq) continue;
@@ -969,7 +1050,8 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
                 float q[kSlowVec], go[kSlowVec];
                 slow_load(q, static_cast<const T *>(a.q) + w.b * a.qs[0] + i * a.qs[1] + h * a.qs[2], a.dim, lane);
                 slow_load(go, static_cast<const T *>(a.dout) + w.b * a.ds[0] + i * a.ds[1] + h * a.ds[2], a.dim, lane);
-                const float p = exp2f(fmaf(fmaf(slow_dot(q, k), scale, x), kLog2e, -st.x));
+                const float p = exp2f(a.vals ? (fmaf(slow_dot(q, k), scale, x) - st.x) * kLog2e
+                                            : fmaf(slow_dot(q, k), scale * kLog2e, -st.x));
                 const float ds = p * (slow_dot(go, v) - st.y);
 #pragma unroll
                 for (int j = 0; j < kSlowVec; ++j) {
@@ -998,7 +1080,7 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 // By A^T's rows: dk (DK) and dv (DV) of 16 columns of A for KH key heads, the
 // query heads that share one following each other.  Wide heads take two launches:
 // both sums and both own operands would not fit the registers.  The values come in
-// A^T's order and units of log 2 (tile_values_kernel).
+// A^T's order (tile_values_kernel).
 template <typename T, int D, int KH, bool DK, bool DV, bool VALS>
 __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a) {
     using R = Ring<D, KH, true>;
@@ -1007,7 +1089,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
     const unsigned n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
-    const float scale = (float)(a.scale * 1.4426950408889634), none = neg_inf<float>();
+    const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
         TileWork w;
         if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, KH, KH, 1)) return;
@@ -1024,8 +1106,7 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
         }
         const int n = (int)(w.ch1 - w.ch0), total = n * share;
         // step x: chunk x % n of the query heads kh * share + x / n (KH > 1: share is 1)
-        auto issue = [&](int x, unsigned col) {
-            char *st = ring + x % R::kStages * R::kStage;
+        auto issue = [&](char *st, int x, unsigned col) {
             const int h = w.kh * share + (KH == 1 ? x / n : 0);
             R::gather(st, static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, a.qs[2], col, lane);
             R::gather(st + R::kTensor, static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, a.ds[2], col, lane);
@@ -1041,63 +1122,63 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < total) issue(i, chunk_column(chunk(i), lane, a.n_rows));
+            if (i < total) issue(ring + i * R::kStage, i, chunk_column(chunk(i), lane, a.n_rows));
             cp_commit();
         }
         unsigned col = R::kStages - 1 < total ? chunk_column(chunk(R::kStages - 1), lane, a.n_rows) : 0;
         Chunk<VALS> next;
+        float x_next[2][4] = {};
+        const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
         if (total > 0) next.load(w.ch0, g);
+        if constexpr (VALS)
+            if (total > 0) next.values(x_next, vals, c);
+        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
         for (int x = 0; x < total; ++x) {
-            const Chunk<VALS> cur = next;
-            cp_wait<R::kStages - 2>();
-            __syncwarp();
-            if (x + R::kStages - 1 < total) issue(x + R::kStages - 1, col);
-            cp_commit();
-            if (x + R::kStages < total) col = chunk_column(chunk(x + R::kStages), lane, a.n_rows);
-            if (x + 1 < total) next.load(chunk(x + 1), g);
-            const char *stage = ring + x % R::kStages * R::kStage;
-            const unsigned mine[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
-            bool on[2][4];
+            unsigned mine[2] = {next.bits[0] >> (2 * c), next.bits[1] >> (2 * c)}, used = 0;
             float val[2][4];
-            unsigned used = 0;
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    on[blk][e] = mine[e >> 1] & (1u << (8 * blk + (e & 1)));
-                    if constexpr (VALS) {
-                        val[blk][e] = none;
-                        if (on[blk][e])
-                            val[blk][e] = __ldg(a.vals_t + w.b * a.nnz + cur.entry(e >> 1, 8 * blk + 2 * c + (e & 1)));
-                        on[blk][e] = on[blk][e] && val[blk][e] != none;
-                    }
-                }
+                for (int e = 0; e < 4; ++e) val[blk][e] = x_next[blk][e];
+            if (x + 1 < total) next.load(chunk(x + 1), g);
+            cp_wait<R::kStages - 2>();
+            __syncwarp();
+            if (x + R::kStages - 1 < total) issue(ring + st_write, x + R::kStages - 1, col);
+            cp_commit();
+            if (x + R::kStages < total) col = chunk_column(chunk(x + R::kStages), lane, a.n_rows);
+            const char *stage = ring + st_read;
+            st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
+            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
 #pragma unroll
             for (int j = 0; j < KH; ++j) {
                 const int p0 = j * (D / 8);
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, k[j], stage, p0, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], stage + R::kTensor, p0, g, c);
+                if (VALS && j == 0 && x + 1 < total) next.values(x_next, vals, c);
                 const float4 *sp = reinterpret_cast<const float4 *>(stage + 2 * R::kTensor + j * 128);
+                unsigned live[2] = {mine[0], mine[1]};
+                bool out = false;                       // a stored pair without a part: its row or value is left out
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
                     const float4 st = sp[4 * blk + c];              // (lse, D) of the columns 2c and 2c + 1
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float lse = e & 1 ? st.z : st.x, delta = e & 1 ? st.w : st.y;
-                        const bool live = on[blk][e] && lse != none;
-                        if constexpr (VALS) {
-                            used |= (unsigned)live << (2 * blk + (e & 1));
-                            s[blk][e] = fmaf(s[blk][e], scale, val[blk][e]) - lse;
-                        } else {
-                            s[blk][e] = fmaf(s[blk][e], scale, -lse);
+                        if (lse == none || (VALS && val[blk][e] == none)) {
+                            out = out || (live[e >> 1] & pair_bit(blk, e));
+                            live[e >> 1] &= ~pair_bit(blk, e);
                         }
-                        s[blk][e] = live ? exp2_of(s[blk][e]) : 0.0f;
-                        if constexpr (DK) dp[blk][e] = live ? s[blk][e] * (dp[blk][e] - delta) : 0.0f;
+                        const bool on = live[e >> 1] & pair_bit(blk, e);
+                        s[blk][e] = on ? exp2_of(relative<VALS>(s[blk][e], scale, val[blk][e], lse)) : 0.0f;
+                        if constexpr (DK) dp[blk][e] = on ? s[blk][e] * (dp[blk][e] - delta) : 0.0f;
                     }
                 }
-                if constexpr (DV) dv[j].template add_chunk<R::kPitch, VALS>(s, stage + R::kTensor, p0, g, c, used);
-                if constexpr (DK) dk[j].template add_chunk<R::kPitch, VALS>(dp, stage, p0, g, c, used);
+                const bool drop = VALS && __any_sync(kAll, out);
+                used = (live[0] | live[1]) & 0x303u;
+                used = (used | used >> 6) & 15u;
+                if constexpr (DV) dv[j].template add_chunk<R::kPitch>(s, stage + R::kTensor, p0, g, c, drop, used);
+                if constexpr (DK) dk[j].template add_chunk<R::kPitch>(dp, stage, p0, g, c, drop, used);
             }
         }
         bool bad = false;
@@ -1138,14 +1219,21 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
     }
 }
 
-// The values in A^T's order and units of log 2.
+// The values as 32-bit numbers, in A^T's order with perm.
 __global__ void __launch_bounds__(256)
 tile_values_kernel(int64_t nnz, int batch, const int32_t *__restrict__ perm, const void *vals, int f64,
                    float *__restrict__ out) {
     const int64_t t = blockIdx.x * (int64_t)256 + threadIdx.x;
     if (t >= nnz) return;
-    const int64_t e = SLA_IDX((int64_t)__ldg(perm + t), nnz, kBndEntry);
-    for (int b = 0; b < batch; ++b) out[b * nnz + t] = value_log2(load_value<float>(vals, f64, b * nnz + e));
+    const int64_t e = perm ? SLA_IDX((int64_t)__ldg(perm + t), nnz, kBndEntry) : t;
+    for (int b = 0; b < batch; ++b) out[b * nnz + t] = load_value<float>(vals, f64, b * nnz + e);
+}
+
+sla_status tile_values(const AttnArgs &a, const int32_t *perm, float *out, cudaStream_t s) {
+    if (a.nnz == 0) return SLA_OK;
+    tile_values_kernel<<<blocks_of(a.nnz), 256, 0, s>>>(a.nnz, a.batch, perm, a.vals, a.vals_f64, out);
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
 }
 
 // -------------------------------------------------------------- launches ----
@@ -1254,24 +1342,39 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const in
     return SLA_OK;
 }
 
-template <typename T> sla_status attn_tile_forward(const AttnArgs &a, cudaStream_t s) {
+// 32-bit values are read in place; 64-bit ones are rounded to a.vals_w first
+// (the backward's row kernel comes before its column kernel, which reuses it).
+template <typename T> sla_status attn_tile_forward(AttnArgs a, cudaStream_t s) {
+    a.vals_f = static_cast<const float *>(a.vals);
+    if (a.vals && a.vals_f64) {
+        const sla_status st = tile_values(a, nullptr, a.vals_w, s);
+        if (st != SLA_OK) return st;
+        a.vals_f = a.vals_w;
+    }
     return launch_tile_of<T>(kTileFwd, a, s);
 }
-template <typename T> sla_status attn_tile_bwd_rows(const AttnArgs &a, cudaStream_t s) {
+template <typename T> sla_status attn_tile_bwd_rows(AttnArgs a, cudaStream_t s) {
+    a.vals_f = static_cast<const float *>(a.vals);
+    if (a.vals && a.vals_f64) {
+        const sla_status st = tile_values(a, nullptr, a.vals_w, s);
+        if (st != SLA_OK) return st;
+        a.vals_f = a.vals_w;
+    }
     return launch_tile_of<T>(kTileBwdRows, a, s);
 }
-template <typename T> sla_status attn_tile_bwd_cols(const AttnArgs &a, cudaStream_t s) {
-    if (a.vals && a.nnz > 0) {
-        tile_values_kernel<<<blocks_of(a.nnz), 256, 0, s>>>(a.nnz, a.batch, a.perm, a.vals, a.vals_f64, a.vals_t);
-        SLA_CHECK_LAUNCH();
+template <typename T> sla_status attn_tile_bwd_cols(AttnArgs a, cudaStream_t s) {
+    if (a.vals) {
+        const sla_status st = tile_values(a, a.perm, a.vals_w, s);
+        if (st != SLA_OK) return st;
+        a.vals_t = a.vals_w;
     }
     return launch_tile_of<T>(kTileBwdCols, a, s);
 }
-template sla_status attn_tile_forward<__nv_bfloat16>(const AttnArgs &, cudaStream_t);
-template sla_status attn_tile_forward<__half>(const AttnArgs &, cudaStream_t);
-template sla_status attn_tile_bwd_rows<__nv_bfloat16>(const AttnArgs &, cudaStream_t);
-template sla_status attn_tile_bwd_rows<__half>(const AttnArgs &, cudaStream_t);
-template sla_status attn_tile_bwd_cols<__nv_bfloat16>(const AttnArgs &, cudaStream_t);
-template sla_status attn_tile_bwd_cols<__half>(const AttnArgs &, cudaStream_t);
+template sla_status attn_tile_forward<__nv_bfloat16>(AttnArgs, cudaStream_t);
+template sla_status attn_tile_forward<__half>(AttnArgs, cudaStream_t);
+template sla_status attn_tile_bwd_rows<__nv_bfloat16>(AttnArgs, cudaStream_t);
+template sla_status attn_tile_bwd_rows<__half>(AttnArgs, cudaStream_t);
+template sla_status attn_tile_bwd_cols<__nv_bfloat16>(AttnArgs, cudaStream_t);
+template sla_status attn_tile_bwd_cols<__half>(AttnArgs, cudaStream_t);
 
 }  // namespace sla
