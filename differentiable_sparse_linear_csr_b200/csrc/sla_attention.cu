@@ -237,8 +237,9 @@ void free_attn_plans(Csr *h) {
 // A group of L lanes takes one (system, item, head); lane l holds the elements
 // (i * L + l) * VEC + e of the head.  Neighbouring groups take neighbouring
 // heads, so a warp reads consecutive memory of a gathered row.  The entries of
-// the item are walked kStep at a time with their loads issued together.
-// Bound by the gathers: 2 * dim elements an entry and head.
+// the item are walked STEP at a time with their loads issued together.
+// Bound by the gathers (2 * dim elements an entry and head) and, for short rows,
+// by the instructions around them.
 namespace {
 
 constexpr int kAttnThreads = 128;
@@ -256,11 +257,18 @@ __device__ __forceinline__ A group_sum(A v, unsigned mask) {
     return v;
 }
 
-struct Item { int64_t b; int row, t0, t1, slot; };
+// Head blocks: `hb` (a power of two) consecutive heads of an item sit in
+// neighbouring groups; blockIdx.y counts systems and head blocks.
+struct Item { int64_t b; int row, t0, t1, slot, h; };
 
-__device__ __forceinline__ Item load_item(const AttnArgs &a, int64_t b, int64_t it) {
-    Item r;
+template <int L>
+__device__ __forceinline__ bool load_item(Item &r, const AttnArgs &a, unsigned y, int heads, int hb_log) {
+    const unsigned blocks = (unsigned)heads >> hb_log, b = y / blocks;
+    const unsigned group = threadIdx.x / L;
+    const int64_t it = (int64_t)blockIdx.x * ((kAttnThreads / L) >> hb_log) + (group >> hb_log);
+    if (it >= a.n_items) return false;
     r.b = b;
+    r.h = (int)(((y - b * blocks) << hb_log) + (group & ((1u << hb_log) - 1u)));
     r.row = a.item_unit ? __ldg(a.item_unit + it) : (int)it;
     r.t0 = __ldg(a.rowptr + r.row);
     r.t1 = __ldg(a.rowptr + r.row + 1);
@@ -272,52 +280,71 @@ __device__ __forceinline__ Item load_item(const AttnArgs &a, int64_t b, int64_t 
         r.t0 = (int)begin;
         r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);
     }
-    return r;
+    return true;
 }
 
-// The vectors of one head this lane holds.
+// The vectors of one head this lane holds; 32-bit ones in pairs, for the
+// two-wide multiply-add.
 template <typename T, int VEC, int L, int NV>
 struct Frag {
     using A = typename AccOf<T>::type;
-    A x[NV][VEC];
+    static constexpr int N = NV * VEC;
+    static constexpr bool kPairs = sizeof(A) == 4 && N % 2 == 0;
+    A x[N];
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[i][e] = (A)0;
+        for (int e = 0; e < N; ++e) x[e] = (A)0;
     }
     template <typename I>
-    __device__ __forceinline__ void load(const I *p, int dim, int lane, bool on) {
-        zero();
+    __device__ __forceinline__ void load(const I *p, int dim, int lane) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int d = (i * L + lane) * VEC;
-            if (on && d < dim) {
+            if (d < dim) {
                 const Pack<I, VEC> r = load_pack<I, VEC>(p + d);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) x[i][e] = to_acc(r.e[e]);
+                for (int e = 0; e < VEC; ++e) x[i * VEC + e] = to_acc(r.e[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) x[i * VEC + e] = (A)0;
             }
         }
     }
     __device__ __forceinline__ A dot(const Frag &y) const {
-        A s = (A)0;
+        if constexpr (kPairs) {
+            float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int e = 0; e < N; e += 2) s = fma2(make_float2(x[e], x[e + 1]), make_float2(y.x[e], y.x[e + 1]), s);
+            return s.x + s.y;
+        } else {
+            A s = (A)0;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) s = fma(x[i][e], y.x[i][e], s);
-        return s;
+            for (int e = 0; e < N; ++e) s = fma(x[e], y.x[e], s);
+            return s;
+        }
     }
     __device__ __forceinline__ void axpy(A w, const Frag &y) {
+        if constexpr (kPairs) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int e = 0; e < N; e += 2) {
+                const float2 r = fma2(make_float2(w, w), make_float2(y.x[e], y.x[e + 1]), make_float2(x[e], x[e + 1]));
+                x[e] = r.x;
+                x[e + 1] = r.y;
+            }
+        } else {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[i][e] = fma(w, y.x[i][e], x[i][e]);
+            for (int e = 0; e < N; ++e) x[e] = fma(w, y.x[e], x[e]);
+        }
     }
     __device__ __forceinline__ void scale(A w) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int e = 0; e < N; ++e) x[e] *= w;
+    }
+    __device__ __forceinline__ bool bad() const {
+        bool b = false;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) x[i][e] *= w;
+        for (int e = 0; e < N; ++e) b = b || x[e] != x[e];
+        return b;
     }
     template <typename O>
     __device__ __forceinline__ void store(O *p, int dim, int lane) const {
@@ -325,100 +352,113 @@ struct Frag {
         for (int i = 0; i < NV; ++i) {
             const int d = (i * L + lane) * VEC;
             if (d < dim) {
-                if constexpr (sizeof(O) * VEC == 32) {
-                    Pack<O, VEC> r;
+                Pack<O, VEC> r;
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) r.e[e] = from_acc<O>(x[i][e]);
-                    reinterpret_cast<uint4 *>(p + d)[0] = reinterpret_cast<uint4 *>(&r)[0];
-                    reinterpret_cast<uint4 *>(p + d)[1] = reinterpret_cast<uint4 *>(&r)[1];
-                } else if constexpr (sizeof(O) * VEC == 16) {
-                    Pack<O, VEC> r;
+                for (int e = 0; e < VEC; ++e) r.e[e] = from_acc<O>(x[i * VEC + e]);
+                if constexpr (sizeof(O) * VEC % 16 == 0) {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) r.e[e] = from_acc<O>(x[i][e]);
-                    *reinterpret_cast<uint4 *>(p + d) = *reinterpret_cast<uint4 *>(&r);
+                    for (int e = 0; e < (int)sizeof(O) * VEC / 16; ++e)
+                        reinterpret_cast<uint4 *>(p + d)[e] = reinterpret_cast<uint4 *>(&r)[e];
                 } else {
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) p[d + e] = from_acc<O>(x[i][e]);
+                    for (int e = 0; e < VEC; ++e) p[d + e] = r.e[e];
                 }
             }
         }
     }
-};
-
-template <typename T, int VEC, int L, int NV>
-__global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const AttnArgs a) {
-    using A = typename AccOf<T>::type;
-    using F = Frag<T, VEC, L, NV>;
-    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
-    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
-    const int lane = threadIdx.x & (L - 1);
-    const unsigned mask = group_mask<L>();
-    if (g >= (int64_t)a.batch * a.n_items * a.heads) return;
-    const int h = (int)(g % a.heads);
-    const Item it = load_item(a, g / a.heads / a.n_items, g / a.heads % a.n_items);
-    const int kh = h / (a.heads / a.kv_heads);
-    F q, acc;
-    q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane, true);
-    acc.zero();
-    const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
-    const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
-    const A scale = (A)a.scale, none = neg_inf<A>();
-    A m = none, l = (A)0;
-    for (int t = it.t0; t < it.t1; t += kStep) {
-        F kf[kStep], vf[kStep];
-        A s[kStep];
-        bool on[kStep];
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            on[u] = t + u < it.t1;
-            A w = (A)0;
-            int64_t c = 0;
-            if (on[u]) {
-                c = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_cols, kBndColumn);
-                w = load_value<A>(a.vals, a.vals_f64, it.b * a.nnz + t + u);
-                on[u] = w != none;     // a value of -inf leaves the entry out
-            }
-            s[u] = w;
-            kf[u].load(kb + c * a.ks[1], a.dim, lane, on[u]);
-            vf[u].load(vb + c * a.vs[1], a.dim, lane, on[u]);
-        }
-        A top = m;
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            const A d = group_sum<L>(q.dot(kf[u]), mask);
-            s[u] = on[u] ? fma(d, scale, s[u]) : none;
-            top = fmax(top, s[u]);
-        }
-        const A ref = top == none ? (A)0 : top;
-        const A fix = exp_acc(m - ref);
-        acc.scale(fix);
-        l *= fix;
-        m = top;
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            const A p = exp_acc(s[u] - ref);
-            l += p;
-            acc.axpy(p, vf[u]);
-        }
-    }
-    if (it.slot < 0) {
-        const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
-        acc.scale(l > (A)0 || l != l ? (A)1 / l : (A)0);   // no entry left: zeros
-        acc.store(static_cast<T *>(a.out) + at * a.dim, a.dim, lane);
-        if (a.wide) acc.store(static_cast<A *>(a.wide) + at * a.dim, a.dim, lane);
-        if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
-    } else {
-        A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * (a.dim + 2);
+    // Partial sums, wherever they lie.
+    __device__ __forceinline__ void store_odd(A *p, int dim, int lane) const {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int d = (i * L + lane) * VEC + e;
-                if (d < a.dim) p[d] = acc.x[i][e];
+                if (d < dim) p[d] = x[i * VEC + e];
             }
-        if (lane == 0) {
-            p[a.dim] = m;
-            p[a.dim + 1] = l;
+    }
+};
+
+// Values of the STEP entries from t on (the last entry's beyond t1); -inf leaves
+// an entry out, as does a place beyond t1.
+template <typename A, int STEP>
+__device__ __forceinline__ void load_values(A (&w)[STEP], const AttnArgs &a, int64_t b, int t, int t1) {
+    const int64_t at = b * a.nnz;
+    if (!a.vals) {
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) w[u] = (A)0;
+    } else if (!a.vals_f64) {
+        const float *p = static_cast<const float *>(a.vals) + at;
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) w[u] = (A)__ldg(p + min(t + u, t1 - 1));
+    } else {
+#pragma unroll
+        for (int u = 0; u < STEP; ++u) w[u] = load_value<A>(a.vals, 1, at + min(t + u, t1 - 1));
+    }
+#pragma unroll
+    for (int u = 0; u < STEP; ++u) w[u] = t + u < t1 ? w[u] : neg_inf<A>();
+}
+
+template <typename T, int VEC, int L, int NV, int STEP>
+__global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const __grid_constant__ AttnArgs a, int hb_log) {
+    using A = typename AccOf<T>::type;
+    using F = Frag<T, VEC, L, NV>;
+    const int lane = threadIdx.x & (L - 1);
+    const unsigned mask = group_mask<L>(), n_y = ((unsigned)a.heads >> hb_log) * (unsigned)a.batch;
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
+        Item it;
+        if (!load_item<L>(it, a, y, a.heads, hb_log)) return;
+        const int h = it.h, kh = h / (a.heads / a.kv_heads);
+        F q, acc;
+        q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane);
+        acc.zero();
+        const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
+        const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
+        const A scale = (A)a.scale, none = neg_inf<A>();
+        A m = none, l = (A)0;
+        for (int t = it.t0; t < it.t1; t += STEP) {
+            F kf[STEP], vf[STEP];
+            A s[STEP], w[STEP];
+            load_values<A, STEP>(w, a, it.b, t, it.t1);
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                const int64_t c = SLA_IDX((int64_t)__ldg(a.colind + min(t + u, it.t1 - 1)), a.n_cols, kBndColumn);
+                kf[u].load(kb + c * a.ks[1], a.dim, lane);
+                vf[u].load(vb + c * a.vs[1], a.dim, lane);
+            }
+            A top = m;
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                const A d = group_sum<L>(q.dot(kf[u]), mask);
+                s[u] = w[u] == none ? none : fma(d, scale, w[u]);
+                top = fmax(top, s[u]);
+            }
+            const A ref = top == none ? (A)0 : top;
+            if (t > it.t0) {
+                const A fix = exp_acc(m - ref);
+                acc.scale(fix);
+                l *= fix;
+            }
+            m = top;
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                const A p = exp_acc(s[u] - ref);
+                l += p;
+                if (w[u] != none) acc.axpy(p, vf[u]);    // what v holds elsewhere does not matter
+            }
+        }
+        if (it.slot < 0) {
+            const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
+            acc.scale(l > (A)0 || l != l ? (A)1 / l : (A)0);   // no entry left: zeros
+            acc.store(static_cast<T *>(a.out) + at * a.dim, a.dim, lane);
+            if (a.wide) acc.store(static_cast<A *>(a.wide) + at * a.dim, a.dim, lane);
+            if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+        } else {
+            A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * (a.dim + 2);
+            acc.store_odd(p, a.dim, lane);
+            if (lane == 0) {
+                p[a.dim] = m;
+                p[a.dim + 1] = l;
+            }
         }
     }
 }
@@ -513,140 +553,138 @@ attn_join_kernel(const AttnArgs a, int rows, int n_multi, const int32_t *__restr
 }
 
 // Gradients by A's rows: p and ds of every entry and head, and dq.
-template <typename T, int VEC, int L, int NV>
-__global__ void __launch_bounds__(kAttnThreads) attn_bwd_rows_kernel(const AttnArgs a) {
+template <typename T, int VEC, int L, int NV, int STEP>
+__global__ void __launch_bounds__(kAttnThreads) attn_bwd_rows_kernel(const __grid_constant__ AttnArgs a, int hb_log) {
     using A = typename AccOf<T>::type;
     using F = Frag<T, VEC, L, NV>;
-    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
-    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
     const int lane = threadIdx.x & (L - 1);
-    const unsigned mask = group_mask<L>();
-    if (g >= (int64_t)a.batch * a.n_items * a.heads) return;
-    const int h = (int)(g % a.heads);
-    const Item it = load_item(a, g / a.heads / a.n_items, g / a.heads % a.n_items);
-    const int kh = h / (a.heads / a.kv_heads);
-    const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
-    F q, go, acc;
-    q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane, true);
-    go.load(static_cast<const T *>(a.dout) + it.b * a.ds[0] + it.row * a.ds[1] + h * a.ds[2], a.dim, lane, true);
-    acc.load(static_cast<const A *>(a.o) + at * a.dim, a.dim, lane, true);
-    const A delta = group_sum<L>(go.dot(acc), mask);
-    const A lse = static_cast<const A *>(a.lse)[at];
-    acc.zero();
-    const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
-    const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
-    const A scale = (A)a.scale, none = neg_inf<A>();
-    A *pds = static_cast<A *>(a.pds);
-    for (int t = it.t0; t < it.t1; t += kStep) {
-        F kf[kStep], vf[kStep];
-        A s[kStep];
-        bool on[kStep];
+    const unsigned mask = group_mask<L>(), n_y = ((unsigned)a.heads >> hb_log) * (unsigned)a.batch;
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
+        Item it;
+        if (!load_item<L>(it, a, y, a.heads, hb_log)) return;
+        const int h = it.h, kh = h / (a.heads / a.kv_heads);
+        const int64_t at = (it.b * a.n_rows + it.row) * a.heads + h;
+        F q, go, acc;
+        q.load(static_cast<const T *>(a.q) + it.b * a.qs[0] + it.row * a.qs[1] + h * a.qs[2], a.dim, lane);
+        go.load(static_cast<const T *>(a.dout) + it.b * a.ds[0] + it.row * a.ds[1] + h * a.ds[2], a.dim, lane);
+        acc.load(static_cast<const A *>(a.o) + at * a.dim, a.dim, lane);
+        const A delta = group_sum<L>(go.dot(acc), mask);
+        const A lse = static_cast<const A *>(a.lse)[at];
+        acc.zero();
+        const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
+        const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
+        const A scale = (A)a.scale, none = neg_inf<A>();
+        A *pds = static_cast<A *>(a.pds) + (it.b * a.nnz * a.heads + h) * 2;
+        for (int t = it.t0; t < it.t1; t += STEP) {
+            F kf[STEP], vf[STEP];
+            A w[STEP], p[STEP], ds[STEP];
+            load_values<A, STEP>(w, a, it.b, t, it.t1);
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            on[u] = t + u < it.t1;
-            A w = (A)0;
-            int64_t c = 0;
-            if (on[u]) {
-                c = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_cols, kBndColumn);
-                w = load_value<A>(a.vals, a.vals_f64, it.b * a.nnz + t + u);
-                on[u] = w != none && lse != none;
+            for (int u = 0; u < STEP; ++u) {
+                const int64_t c = SLA_IDX((int64_t)__ldg(a.colind + min(t + u, it.t1 - 1)), a.n_cols, kBndColumn);
+                kf[u].load(kb + c * a.ks[1], a.dim, lane);
+                vf[u].load(vb + c * a.vs[1], a.dim, lane);
             }
-            s[u] = w;
-            kf[u].load(kb + c * a.ks[1], a.dim, lane, on[u]);
-            vf[u].load(vb + c * a.vs[1], a.dim, lane, on[u]);
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                p[u] = q.dot(kf[u]);
+                ds[u] = go.dot(vf[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < STEP; ++u) {
+                const bool on = w[u] != none && lse != none;
+                p[u] = group_sum<L>(p[u], mask);
+                ds[u] = group_sum<L>(ds[u], mask);
+                p[u] = on ? exp_acc(fma(p[u], scale, w[u]) - lse) : (A)0;
+                ds[u] = on ? p[u] * (ds[u] - delta) : (A)0;
+                if (on) acc.axpy(ds[u], kf[u]);
+            }
+            if (a.pds) {
+                // lane u writes entry t + u
+#pragma unroll
+                for (int u = 0; u < STEP; ++u)
+                    if (lane == u % L && t + u < it.t1) {
+                        A *e = pds + (int64_t)(t + u) * a.heads * 2;
+                        if constexpr (sizeof(A) == 4) *reinterpret_cast<float2 *>(e) = make_float2(p[u], ds[u]);
+                        else *reinterpret_cast<double2 *>(e) = make_double2(p[u], ds[u]);
+                    }
+            }
         }
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-            const A d = group_sum<L>(q.dot(kf[u]), mask);
-            const A dp = group_sum<L>(go.dot(vf[u]), mask);
-            const A p = on[u] ? exp_acc(fma(d, scale, s[u]) - lse) : (A)0;
-            const A ds = on[u] ? p * (dp - delta) : (A)0;
-            acc.axpy(ds, kf[u]);
-            if (pds && lane == 0 && t + u < it.t1) {
-                A *e = pds + ((it.b * a.nnz + t + u) * a.heads + h) * 2;
-                e[0] = p;
-                e[1] = ds;
-            }
-        }
-    }
-    acc.scale(scale);
-    if (!a.dq) return;
-    if (it.slot < 0) {
-        acc.store(static_cast<T *>(a.dq) + at * a.dim, a.dim, lane);
-    } else {
-        A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * a.dim;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int d = (i * L + lane) * VEC + e;
-                if (d < a.dim) p[d] = acc.x[i][e];
-            }
+        if (!a.dq) continue;
+        acc.scale(scale);
+        if (it.slot < 0) acc.store(static_cast<T *>(a.dq) + at * a.dim, a.dim, lane);
+        else
+            acc.store_odd(static_cast<A *>(a.part) +
+                              part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * a.dim, a.dim, lane);
     }
 }
 
 // Gradients by A^T's rows, from the stored p and ds: dk and dv.  Partial sums
 // of a split row: dk then dv.
-template <typename T, int VEC, int L, int NV>
-__global__ void __launch_bounds__(kAttnThreads) attn_bwd_cols_kernel(const AttnArgs a) {
+template <typename T, int VEC, int L, int NV, int STEP>
+__global__ void __launch_bounds__(kAttnThreads) attn_bwd_cols_kernel(const __grid_constant__ AttnArgs a, int hb_log) {
     using A = typename AccOf<T>::type;
     using F = Frag<T, VEC, L, NV>;
-    constexpr int kStep = NV * VEC * sizeof(A) <= 32 ? 4 : 2;
-    const int64_t g = (blockIdx.x * (int64_t)kAttnThreads + threadIdx.x) / L;
-    const int lane = threadIdx.x & (L - 1);
-    if (g >= (int64_t)a.batch * a.n_items * a.kv_heads) return;
-    const int kh = (int)(g % a.kv_heads), share = a.heads / a.kv_heads;
-    const Item it = load_item(a, g / a.kv_heads / a.n_items, g / a.kv_heads % a.n_items);
-    F dk, dv;
-    dk.zero();
-    dv.zero();
-    const A *pds = static_cast<const A *>(a.pds);
-    for (int h = kh * share; h < (kh + 1) * share; ++h) {
-        const T *qb = static_cast<const T *>(a.q) + it.b * a.qs[0] + h * a.qs[2];
-        const T *gb = static_cast<const T *>(a.dout) + it.b * a.ds[0] + h * a.ds[2];
-        for (int t = it.t0; t < it.t1; t += kStep) {
-            F qf[kStep], gf[kStep];
-            A p[kStep], ds[kStep];
+    const int lane = threadIdx.x & (L - 1), share = a.heads / a.kv_heads;
+    const unsigned n_y = ((unsigned)a.kv_heads >> hb_log) * (unsigned)a.batch;
+    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
+        Item it;
+        if (!load_item<L>(it, a, y, a.kv_heads, hb_log)) return;
+        F dk, dv;
+        // Entries that were left out have p = ds = 0; what q and dout hold there (a
+        // NaN, say) must not matter, but skipping them would make the loads wait for
+        // p, so that is done only when a sum ends as a NaN.
+        auto sums = [&](auto careful) {
+            dk.zero();
+            dv.zero();
+            for (int h = it.h * share; h < (it.h + 1) * share; ++h) {
+                const T *qb = static_cast<const T *>(a.q) + it.b * a.qs[0] + h * a.qs[2];
+                const T *gb = static_cast<const T *>(a.dout) + it.b * a.ds[0] + h * a.ds[2];
+                const A *pds = static_cast<const A *>(a.pds) + (it.b * a.nnz * a.heads + h) * 2;
+                for (int t = it.t0; t < it.t1; t += STEP) {
+                    F qf[STEP], gf[STEP];
+                    A p[STEP], ds[STEP];
 #pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                int64_t i = 0;
-                p[u] = ds[u] = (A)0;
-                if (t + u < it.t1) {
-                    i = SLA_IDX((int64_t)__ldg(a.colind + t + u), a.n_rows, kBndColumn);
-                    const int64_t e = SLA_IDX((int64_t)__ldg(a.perm + t + u), a.nnz, kBndEntry);
-                    const A *x = pds + ((it.b * a.nnz + e) * a.heads + h) * 2;
-                    p[u] = x[0];
-                    ds[u] = x[1];
+                    for (int u = 0; u < STEP; ++u) {
+                        const int at = min(t + u, it.t1 - 1);
+                        const int64_t i = SLA_IDX((int64_t)__ldg(a.colind + at), a.n_rows, kBndColumn);
+                        const int64_t e = SLA_IDX((int64_t)__ldg(a.perm + at), a.nnz, kBndEntry);
+                        qf[u].load(qb + i * a.qs[1], a.dim, lane);
+                        gf[u].load(gb + i * a.ds[1], a.dim, lane);
+                        if constexpr (sizeof(A) == 4) {
+                            const float2 x = __ldg(reinterpret_cast<const float2 *>(pds + e * a.heads * 2));
+                            p[u] = x.x;
+                            ds[u] = x.y;
+                        } else {
+                            const double2 x = __ldg(reinterpret_cast<const double2 *>(pds + e * a.heads * 2));
+                            p[u] = x.x;
+                            ds[u] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < STEP; ++u) {
+                        if constexpr (decltype(careful)::value) {
+                            if (t + u >= it.t1 || p[u] == (A)0) continue;
+                        }
+                        dk.axpy(t + u < it.t1 ? ds[u] : (A)0, qf[u]);
+                        dv.axpy(t + u < it.t1 ? p[u] : (A)0, gf[u]);
+                    }
                 }
-                const bool on = p[u] != (A)0;      // an entry that was left out has no part
-                qf[u].load(qb + i * a.qs[1], a.dim, lane, on);
-                gf[u].load(gb + i * a.ds[1], a.dim, lane, on);
             }
-#pragma unroll
-            for (int u = 0; u < kStep; ++u) {
-                dk.axpy(ds[u], qf[u]);
-                dv.axpy(p[u], gf[u]);
-            }
+        };
+        sums(std::false_type{});
+        if (dk.bad() || dv.bad()) sums(std::true_type{});
+        dk.scale((A)a.scale);
+        if (it.slot < 0) {
+            const int64_t at = ((it.b * a.n_cols + it.row) * a.kv_heads + it.h) * a.dim;
+            if (a.dk) dk.store(static_cast<T *>(a.dk) + at, a.dim, lane);
+            if (a.dv) dv.store(static_cast<T *>(a.dv) + at, a.dim, lane);
+        } else {
+            A *p = static_cast<A *>(a.part) +
+                   part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.kv_heads, it.h) * 2 * a.dim;
+            dk.store_odd(p, a.dim, lane);
+            dv.store_odd(p + a.dim, a.dim, lane);
         }
-    }
-    dk.scale((A)a.scale);
-    if (it.slot < 0) {
-        const int64_t at = ((it.b * a.n_cols + it.row) * a.kv_heads + kh) * a.dim;
-        if (a.dk) dk.store(static_cast<T *>(a.dk) + at, a.dim, lane);
-        if (a.dv) dv.store(static_cast<T *>(a.dv) + at, a.dim, lane);
-    } else {
-        A *p = static_cast<A *>(a.part) +
-               part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.kv_heads, kh) * 2 * a.dim;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int d = (i * L + lane) * VEC + e;
-                if (d < a.dim) {
-                    p[d] = dk.x[i][e];
-                    p[a.dim + d] = dv.x[i][e];
-                }
-            }
     }
 }
 
@@ -751,13 +789,19 @@ enum { kFwd, kBwdRows, kBwdCols };
 
 template <typename T, int VEC, int L, int NV>
 sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
-    const int64_t groups = (int64_t)a.batch * a.n_items * (what == kBwdCols ? a.kv_heads : a.heads);
-    const int64_t blocks = (groups * L + kAttnThreads - 1) / kAttnThreads;
-    SLA_REQUIRE(blocks < INT_MAX, "sla_attention: too many rows, systems and heads");
-    if (blocks == 0) return SLA_OK;
-    if (what == kFwd) attn_fwd_rows_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
-    else if (what == kBwdRows) attn_bwd_rows_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
-    else attn_bwd_cols_kernel<T, VEC, L, NV><<<(unsigned)blocks, kAttnThreads, 0, s>>>(a);
+    // entries in flight: as many as 32 accumulator words of each side hold
+    constexpr int STEP = NV * VEC * (int)sizeof(typename AccOf<T>::type) <= 32 ? 4 : 2;
+    const int heads = what == kBwdCols ? a.kv_heads : a.heads;
+    int hb = 0;                          // the largest power of two that divides the heads and fits a block
+    while ((2 << hb) <= kAttnThreads / L && heads % (2 << hb) == 0) ++hb;
+    const int64_t x = ((int64_t)a.n_items + ((kAttnThreads / L) >> hb) - 1) / ((kAttnThreads / L) >> hb);
+    const int64_t y = (int64_t)(heads >> hb) * a.batch;
+    SLA_REQUIRE(x < INT_MAX && y < INT_MAX, "sla_attention: too many rows, systems and heads");
+    if (x == 0) return SLA_OK;
+    const dim3 grid((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
+    if (what == kFwd) attn_fwd_rows_kernel<T, VEC, L, NV, STEP><<<grid, kAttnThreads, 0, s>>>(a, hb);
+    else if (what == kBwdRows) attn_bwd_rows_kernel<T, VEC, L, NV, STEP><<<grid, kAttnThreads, 0, s>>>(a, hb);
+    else attn_bwd_cols_kernel<T, VEC, L, NV, STEP><<<grid, kAttnThreads, 0, s>>>(a, hb);
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }

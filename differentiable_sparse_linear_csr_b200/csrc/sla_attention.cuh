@@ -121,7 +121,24 @@ __device__ __forceinline__ Pack<T, N> load_pack(const T *p) {
     return r;
 }
 
-__device__ __forceinline__ float exp_acc(float x) { return exp2f(x * 1.4426950408889634f); }
+// Two 32-bit multiply-adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long *>(&a)), "l"(*reinterpret_cast<unsigned long long *>(&b)),
+          "l"(*reinterpret_cast<unsigned long long *>(&c)));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+// The hardware's exponential (2 ulp; results below 2^-126 are zero, which a
+// softmax does not notice).
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float exp_acc(float x) { return exp2_of(x * 1.4426950408889634f); }
 __device__ __forceinline__ double exp_acc(double x) { return exp(x); }
 __device__ __forceinline__ float log_acc(float x) { return logf(x); }
 __device__ __forceinline__ double log_acc(double x) { return log(x); }

@@ -224,16 +224,7 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ float exp_of(float x) { return exp2f(x * 1.4426950408889634f); }
-
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// The hardware's exponential: 2 ulp, results below 2^-126 are zero, which a
-// softmax does not notice.
-__device__ __forceinline__ float exp2_of(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // Scores less a reference (maximum or lse) in units of log 2.  Without values the
 // factor log2 e is part of `scale` and the references have the same unit: one
 // multiply-add.  Values come in natural units, and the difference is taken before
@@ -605,7 +596,7 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
             slow_load(k, kb + col * a.ks[1], a.dim, lane);
             slow_load(v, vb + col * a.vs[1], a.dim, lane);
             const float s = fmaf(slow_dot(q, k), scale, x), top = fmaxf(m, s);
-            const float ref = top == none ? 0.0f : top, fix = exp_of(m - ref), p = exp_of(s - ref);
+            const float ref = top == none ? 0.0f : top, fix = exp_acc(m - ref), p = exp_acc(s - ref);
             m = top;
             l = l * fix + p;
 #pragma unroll
@@ -854,7 +845,7 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
             float k[kSlowVec], v[kSlowVec];
             slow_load(k, kb + col * a.ks[1], a.dim, lane);
             slow_load(v, vb + col * a.vs[1], a.dim, lane);
-            const float p = exp_of(fmaf(slow_dot(q, k), scale, x) - lse);
+            const float p = exp_acc(fmaf(slow_dot(q, k), scale, x) - lse);
             const float ds = p * (slow_dot(go, v) - delta);
 #pragma unroll
             for (int i = 0; i < kSlowVec; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
