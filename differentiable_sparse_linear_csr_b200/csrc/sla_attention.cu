@@ -787,10 +787,8 @@ namespace {
 // -------------------------------------------------------------- launches ----
 enum { kFwd, kBwdRows, kBwdCols };
 
-template <typename T, int VEC, int L, int NV>
+template <typename T, int VEC, int L, int NV, int STEP>
 sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
-    // entries in flight: as many as 32 accumulator words of each side hold
-    constexpr int STEP = NV * VEC * (int)sizeof(typename AccOf<T>::type) <= 32 ? 4 : 2;
     const int heads = what == kBwdCols ? a.kv_heads : a.heads;
     int hb = 0;                          // the largest power of two that divides the heads and fits a block
     while ((2 << hb) <= kAttnThreads / L && heads % (2 << hb) == 0) ++hb;
@@ -806,8 +804,23 @@ sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
     return SLA_OK;
 }
 
-// Lanes and vectors a lane by the head's width: the fewest lanes (fewest
-// shuffles a score) that keep at most 2 vectors a lane.
+// Entries in flight: 4 or 5, whichever leaves fewer places empty on a row of mean
+// length (a 5-point row in one step instead of two); 2 where the registers hold
+// no more.
+template <typename T, int VEC, int L, int NV>
+sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
+    constexpr int bytes = NV * VEC * (int)sizeof(typename AccOf<T>::type);
+    if constexpr (bytes <= 32) {
+        const int64_t rows = what == kBwdCols ? a.n_cols : a.n_rows, mean = (a.nnz + rows - 1) / (rows > 0 ? rows : 1);
+        if ((mean + 4) / 5 * 5 < (mean + 3) / 4 * 4) return launch_rows<T, VEC, L, NV, 5>(what, a, s);
+        return launch_rows<T, VEC, L, NV, 4>(what, a, s);
+    } else {
+        return launch_rows<T, VEC, L, NV, 2>(what, a, s);
+    }
+}
+
+// Lanes and vectors a lane by the head's width: a group's load covers 128
+// consecutive bytes where the head has them.
 template <typename T>
 sla_status launch_rows_of(int what, const AttnArgs &a, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);

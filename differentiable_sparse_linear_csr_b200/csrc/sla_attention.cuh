@@ -13,6 +13,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <cstdlib>
 #include <vector>
 
 #include "sla_common.cuh"
@@ -62,6 +63,7 @@ inline int attn_level(const Csr *h, const sla_attn_opts *o) {
 
 // 16-bit heads of whole 16-element steps go through the tensor cores.
 inline bool attn_tiled(const sla_attn_opts *o) {
+    if (getenv("SLA_ATTN_ROWS")) return false;
     return (o->dtype == SLA_BF16 || o->dtype == SLA_F16) && o->dim % 16 == 0 && o->dim <= 128;
 }
 
