@@ -154,10 +154,13 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+# the current stream's handle without making a Stream object (where torch has it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream=None) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    return _raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def dtype_code(dtype: torch.dtype) -> int:
@@ -363,11 +366,13 @@ def sla_attention_workspace_bytes(h, opts, backward=0) -> int:
     return int(lib().sla_attention_workspace_bytes(h, ctypes.byref(opts), int(backward)))
 
 
-def sla_attention(h, q, k, v, vals, out, out_wide, lse, opts, ws, stream=None) -> None:
-    """q, k and v with the strides of opts (their last dimension contiguous)."""
+def sla_attention(h, q, k, v, vals, out, out_wide, lse, opts, ws, stream=None, lse_ptr=None) -> None:
+    """q, k and v with the strides of opts (their last dimension contiguous).
+    lse_ptr: an address for lse instead of a tensor."""
     _check("sla_attention", lib().sla_attention(
-        h, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(vals), _ptr(out), _ptr(out_wide), _ptr(lse),
-        ctypes.byref(opts), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+        h, q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(vals), _ptr(out), _ptr(out_wide),
+        _ptr(lse) if lse_ptr is None else lse_ptr, ctypes.byref(opts), _ptr(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def sla_attention_grad(h, q, k, v, vals, out, lse, dout, dq, dk, dv, dvals, opts, ws, stream=None) -> None:
@@ -382,12 +387,17 @@ def sla_norm_workspace_bytes(n) -> int:
     return int(lib().sla_norm_workspace_bytes(n))
 
 
-def tensor_list(src, dst=None):
-    """Host array of sla_tensor (four 64-bit words each) for dense tensors, and its length."""
-    words = []
-    for a, b in zip(src, dst if dst is not None else src):
-        words += (a.data_ptr(), b.data_ptr(), a.numel(), TENSOR_DTYPES[a.dtype])
-    return (ctypes.c_int64 * max(len(words), 1))(*words), len(words) // 4
+def tensor_list(src, codes, dst=None):
+    """Host array of sla_tensor (four 64-bit words each) for dense tensors of the
+    sla_dtypes `codes`."""
+    n = len(src)
+    words = [0] * (4 * n)
+    words[0::4] = [t.data_ptr() for t in src]
+    if dst is not None:
+        words[1::4] = [t.data_ptr() for t in dst]
+    words[2::4] = [t.numel() for t in src]
+    words[3::4] = codes
+    return (ctypes.c_int64 * max(4 * n, 1))(*words)
 
 
 def sla_global_norm(n, tensors, kind, norm, ws, stream=None) -> None:

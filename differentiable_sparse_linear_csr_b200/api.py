@@ -14,6 +14,7 @@ the computation runs in libsla.so's kernels (see _lib.py).
 """
 from __future__ import annotations
 
+import contextlib
 import math
 from dataclasses import dataclass
 
@@ -71,6 +72,7 @@ class CSR:
             self.handle = L.sla_csr_create(self.n_rows, self.n_cols, self.nnz, self.rowptr, self.colind,
                                            self.batch, L.dtype_code(dtype), flags)
         self.n_info = self.batch                 # entries of a solve's SolveInfo
+        self._attn_calls = {}
         self.last_info: SolveInfo | None = None
         self.last_adjoint_info: SolveInfo | None = None
 
@@ -184,33 +186,21 @@ class CSR:
         whose rows do not start on 16 bytes; other strides are used as they are.  Returns o shaped like q.  Sums have a fixed order: equal
         calls give equal bits.
         """
-        q4, k4, v4 = self._heads(q, self.n_rows, "q"), self._heads(k, self.n_cols, "k"), \
-            self._heads(v, self.n_cols, "v")
-        if not (q4.dtype == k4.dtype == v4.dtype) or q4.dtype not in L.TENSOR_DTYPES:
-            raise TypeError("q, k and v must share one type: float64, float32, bfloat16 or float16")
-        if k4.shape != v4.shape or k4.shape[3] != q4.shape[3]:
-            raise ValueError(f"k {tuple(k4.shape)} and v {tuple(v4.shape)} must have one shape, with q's "
-                             f"last dimension ({q4.shape[3]})")
-        if k4.shape[2] == 0 or q4.shape[2] == 0 or q4.shape[2] % k4.shape[2]:
-            raise ValueError(f"q's {q4.shape[2]} heads are not a multiple of k's {k4.shape[2]}")
-        if not 1 <= q4.shape[3] <= 256:
-            raise ValueError(f"heads of {q4.shape[3]} elements (1 to 256)")
-        if values is not None:
-            self._values(values)
-        scale = q4.shape[3] ** -0.5 if scale is None else float(scale)
-        if not math.isfinite(scale):
-            raise ValueError("scale must be finite")
-        return _Attention.apply(self, q4, k4, v4, values, scale).reshape(q.shape)
-
-    def _heads(self, x, n, name):
-        want = (self.batch, n)
-        if x.dim() == 3 and self.batch == 1:
-            x = x.unsqueeze(0)
-        if x.dim() != 4 or tuple(x.shape[:2]) != want:
-            raise ValueError(f"{name} must be [{want[0]}, {want[1]}, heads, dim] (got {tuple(x.shape)})")
-        if x.device != self.device:
-            raise TypeError(f"{name} must be on {self.device}")
-        return x
+        # what depends on shapes, strides and types alone is checked and laid out once
+        key = (q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), q.dtype, k.dtype, v.dtype,
+               q.device, k.device, v.device, scale, values is None)
+        call = self._attn_calls.get(key)
+        if call is None:
+            call = _AttentionCall(self, q, k, v, values, scale)
+            if len(self._attn_calls) >= 64:
+                self._attn_calls.clear()
+            self._attn_calls[key] = call
+        if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                        (values is not None and values.requires_grad)):
+            if q.dim() == 3:
+                return _Attention.apply(self, call, q.unsqueeze(0), k.unsqueeze(0), v.unsqueeze(0), values).squeeze(0)
+            return _Attention.apply(self, call, q, k, v, values)
+        return call.forward(self, q, k, v, values, False)[0]
 
 
 class CSRList(CSR):
@@ -242,6 +232,7 @@ class CSRList(CSR):
             self.handle = L.sla_csr_list_create(self.n_items, self.item_rows, self.n_rows, self.nnz,
                                                 self.rowptr, self.colind, L.dtype_code(dtype), flags)
         self.n_info = self.n_items
+        self._attn_calls = {}
         self.last_info = None
         self.last_adjoint_info = None
 
@@ -313,53 +304,116 @@ class _Solve(torch.autograd.Function):
         return None, gv, gb, None
 
 
-def _head_layout(x: torch.Tensor) -> torch.Tensor:
-    """x as the kernels read it: the last dimension contiguous and, in 16 bits,
-    the other strides and the address on 16 bytes; a copy if it is not."""
+def _on_device(device):
+    """The device as the current one; nothing to enter where it is already."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _aligned(x: torch.Tensor) -> bool:
+    """Rows of 16-bit heads start on 16 bytes."""
     st = x.stride()
-    if st[3] != 1 or (x.element_size() == 2 and ((st[0] | st[1] | st[2]) & 7 or x.data_ptr() & 15)
-                      and x.shape[3] % 8 == 0):
+    return not ((st[-2] | st[-3] | (st[0] if x.dim() == 4 else 0)) & 7 or x.data_ptr() & 15)
+
+
+def _head_layout(x: torch.Tensor, whole: bool) -> torch.Tensor:
+    """x as the kernels read it: the last dimension contiguous and, with `whole`,
+    rows on 16 bytes; a copy if it is not."""
+    if x.stride(-1) != 1 or (whole and not _aligned(x)):
         x = x.clone(memory_format=torch.contiguous_format)
     return x
 
 
+class _AttentionCall:
+    """What calls of one set of shapes, strides and types share."""
+
+    def __init__(self, A: CSR, q, k, v, values, scale):
+        for x, n, name in ((q, A.n_rows, "q"), (k, A.n_cols, "k"), (v, A.n_cols, "v")):
+            if tuple(x.shape[:-2]) != (A.batch, n) and not (A.batch == 1 and tuple(x.shape[:-2]) == (n,)):
+                raise ValueError(f"{name} must be [{A.batch}, {n}, heads, dim] (got {tuple(x.shape)})")
+            if x.dim() != q.dim():
+                raise ValueError("q, k and v must have the same number of dimensions")
+            if x.device != A.device:
+                raise TypeError(f"{name} must be on {A.device}")
+        if not (q.dtype == k.dtype == v.dtype) or q.dtype not in L.TENSOR_DTYPES:
+            raise TypeError("q, k and v must share one type: float64, float32, bfloat16 or float16")
+        (H, D), K = q.shape[-2:], k.shape[-2]
+        if k.shape != v.shape or k.shape[-1] != D:
+            raise ValueError(f"k {tuple(k.shape)} and v {tuple(v.shape)} must have one shape, with q's last "
+                             f"dimension ({D})")
+        if K == 0 or H == 0 or H % K:
+            raise ValueError(f"q's {H} heads are not a multiple of k's {K}")
+        if not 1 <= D <= 256:
+            raise ValueError(f"heads of {D} elements (1 to 256)")
+        self.scale = D ** -0.5 if scale is None else float(scale)
+        if not math.isfinite(self.scale):
+            raise ValueError("scale must be finite")
+        self.size = (q.dtype, H, K, D)
+        self.whole = q.element_size() == 2 and D % 8 == 0
+        self.wide = torch.float64 if q.dtype == torch.float64 else torch.float32
+        self.lse = A.batch * A.n_rows * H * (8 if q.dtype == torch.float64 else 4)
+        self.ready = [False, False]
+        self.opts = self.options(q, k, v)
+
+    def options(self, q, k, v, do=None):
+        def strides(x):
+            st = x.stride()
+            return st[:3] if len(st) == 4 else (0, *st[:2])
+
+        return L.make_attn_opts(*self.size, self.scale, strides(q), strides(k), strides(v),
+                                (0, 0, 0) if do is None else strides(do))
+
+    def prepare(self, A, opts, backward):
+        if not self.ready[backward]:
+            L.sla_attention_prepare(A.handle, opts, backward)
+            self.workspace = [L.sla_attention_workspace_bytes(A.handle, opts, x) for x in range(backward + 1)]
+            self.ready[0] = self.ready[backward] = True
+
+    def forward(self, A, q, k, v, values, train):
+        """(o, its 32-bit form or None, lse or None, q, k, v as the kernels read them)"""
+        vals = None if values is None else A._values(values)
+        opts, given = self.opts, (q, k, v)
+        q, k, v = _head_layout(q, self.whole), _head_layout(k, self.whole), _head_layout(v, self.whole)
+        if q is not given[0] or k is not given[1] or v is not given[2]:
+            opts = self.options(q, k, v)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        with _on_device(A.device):
+            self.prepare(A, opts, train)
+            room = self.workspace[0]
+            if train:
+                lse = torch.empty(A.batch, A.n_rows, q.shape[-2], dtype=self.wide, device=A.device)
+                wide = torch.empty(out.shape, dtype=self.wide, device=A.device) if q.element_size() == 2 else None
+                L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts, _workspace(room, A.device))
+                return out, wide, lse, q, k, v
+            ws = _workspace(room + self.lse, A.device)      # lse behind the workspace proper
+            L.sla_attention(A.handle, q, k, v, vals, out, None, None, opts, ws, lse_ptr=ws.data_ptr() + room)
+        return out, None, None, q, k, v
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A: CSR, q, k, v, values, scale):
-        q, k, v = _head_layout(q), _head_layout(k), _head_layout(v)
-        B, n, H, D = q.shape
-        vals = None if values is None else A._values(values)
-        out = torch.empty(B, n, H, D, dtype=q.dtype, device=A.device)
-        lse = torch.empty(B, n, H, dtype=torch.float64 if q.dtype == torch.float64 else torch.float32,
-                          device=A.device)
-        train = any(ctx.needs_input_grad)
-        wide = torch.empty(B, n, H, D, dtype=torch.float32, device=A.device) \
-            if train and q.element_size() == 2 else None
-        with torch.cuda.device(A.device):
-            opts = L.make_attn_opts(q.dtype, H, k.shape[2], D, scale, q.stride()[:3], k.stride()[:3],
-                                    v.stride()[:3])
-            L.sla_attention_prepare(A.handle, opts, train)
-            ws = _workspace(L.sla_attention_workspace_bytes(A.handle, opts, 0), A.device)
-            L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts, ws)
-        ctx.A, ctx.scale = A, scale
+    def forward(ctx, A: CSR, call: _AttentionCall, q, k, v, values):
+        out, wide, lse, q, k, v = call.forward(A, q, k, v, values, True)
+        ctx.A, ctx.call = A, call
         ctx.save_for_backward(q, k, v, values, out if wide is None else wide, lse)
         return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, go):
-        A = ctx.A
+        A, call = ctx.A, ctx.call
         q, k, v, values, out, lse = ctx.saved_tensors
-        go = _head_layout(go)
+        go = _head_layout(go, call.whole)
         vals = None if values is None else A._values(values)
         new = lambda need, t: torch.empty(t.shape, dtype=t.dtype, device=A.device) if need else None  # noqa: E731
-        dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[1:5], (q, k, v, values)))
-        with torch.cuda.device(A.device):
-            opts = L.make_attn_opts(q.dtype, q.shape[2], k.shape[2], q.shape[3], ctx.scale, q.stride()[:3],
-                                    k.stride()[:3], v.stride()[:3], go.stride()[:3])
-            ws = _workspace(L.sla_attention_workspace_bytes(A.handle, opts, 1), A.device)
-            L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals, opts, ws)
-        return None, dq, dk, dv, dvals, None
+        dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[2:6], (q, k, v, values)))
+        with _on_device(A.device):
+            ws = _workspace(call.workspace[1], A.device)
+            L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals,
+                                 call.options(q, k, v, go), ws)
+        return None, None, dq, dk, dv, dvals
 
 
 class EdgeLaplacian:
@@ -596,13 +650,14 @@ def _norm_kind(norm_type) -> int:
     raise ValueError(f"norm_type must be 2 or inf (got {norm_type})")
 
 
-def _one_device(tensors):
-    for t in tensors:
-        if t.device.type != "cuda" or t.device != tensors[0].device:
-            raise ValueError("the tensors must be on one CUDA device")
-        if t.dtype not in L.TENSOR_DTYPES:
-            raise TypeError(f"unsupported dtype {t.dtype} (float64, float32, bfloat16 or float16)")
-    return tensors[0].device
+def _codes(tensors):
+    """The tensors' types as the library's, all on one CUDA device."""
+    if any(not t.is_cuda for t in tensors) or len({t.get_device() for t in tensors}) > 1:
+        raise ValueError("the tensors must be on one CUDA device")
+    try:
+        return [L.TENSOR_DTYPES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError(f"unsupported dtype {e.args[0]} (float64, float32, bfloat16 or float16)") from None
 
 
 def _dense(t: torch.Tensor) -> bool:
@@ -610,68 +665,63 @@ def _dense(t: torch.Tensor) -> bool:
     return t.is_contiguous() or torch.ops.aten.is_non_overlapping_and_dense(t)
 
 
-def _norm_buffers(tensors, device):
-    wide = any(t.dtype == torch.float64 for t in tensors)
-    return (torch.empty((), dtype=torch.float64 if wide else torch.float32, device=device),
-            _workspace(L.sla_norm_workspace_bytes(len(tensors)), device))
+def _norm_buffers(codes, device):
+    return (torch.empty((), dtype=torch.float64 if L.SLA_F64 in codes else torch.float32, device=device),
+            _workspace(L.sla_norm_workspace_bytes(len(codes)), device))
 
 
-@torch.no_grad()
 def global_norm(tensors, norm_type: float = 2.0) -> torch.Tensor:
     """The norm of all elements of all tensors: sqrt(sum x^2), or max |x| for
-    norm_type inf.  A 0-dim tensor, float64 if any tensor is, else float32;
-    squares are summed in 64 bits in a fixed order.  No host synchronisation.
+    norm_type inf.  A 0-dim tensor, float64 if any tensor is, else float32, outside
+    autograd; squares are summed in 64 bits in a fixed order.  No host
+    synchronisation.
     """
     tensors = list(tensors)
     kind = _norm_kind(norm_type)
     if not tensors:
         return torch.zeros(())
-    device = _one_device(tensors)
-    src = [t if _dense(t) else t.contiguous() for t in tensors]
-    with torch.cuda.device(device):
-        norm, ws = _norm_buffers(tensors, device)
-        words, n = L.tensor_list(src)
-        L.sla_global_norm(n, words, kind, norm, ws)
+    codes = _codes(tensors)
+    src = [t if _dense(t) else t.detach().contiguous() for t in tensors]
+    with _on_device(tensors[0].device):
+        norm, ws = _norm_buffers(codes, tensors[0].device)
+        L.sla_global_norm(len(src), L.tensor_list(src, codes), kind, norm, ws)
     return norm
 
 
-@torch.no_grad()
 def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out=None):
     """(clipped, norm): every tensor times min(1, max_norm / (norm + 1e-6)), with
-    the norm of all of them together.  ``out``: the tensors to write (shapes and
-    types of the inputs; ``out=tensors`` clips in place), new ones by default.
-    The outputs may share memory with their own input only.  A NaN makes every
-    output NaN; an infinity makes the factor 0.  No host synchronisation.
+    the norm of all of them together, outside autograd.  ``out``: the tensors to
+    write (shapes and types of the inputs; ``out=tensors`` clips in place), new ones
+    by default.  The outputs may share memory with their own input only.  A NaN
+    makes every output NaN; an infinity makes the factor 0.  No host
+    synchronisation.
     """
     tensors = list(tensors)
     kind = _norm_kind(norm_type)
     max_norm = float(max_norm)
     if not (max_norm >= 0.0 and math.isfinite(max_norm)):
         raise ValueError(f"max_norm must be finite and not negative (got {max_norm})")
-    if out is None:
-        outs = None
-    else:
-        outs = list(out)
-        if len(outs) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype or o.device != t.device
-                                            for o, t in zip(outs, tensors)):
-            raise ValueError("out must match the tensors in number, shapes, types and device")
+    outs = None if out is None else list(out)
+    if outs is not None and (len(outs) != len(tensors) or any(
+            o is not t and (o.shape != t.shape or o.dtype != t.dtype or o.device != t.device)
+            for o, t in zip(outs, tensors))):
+        raise ValueError("out must match the tensors in number, shapes, types and device")
     if not tensors:
         return [], torch.zeros(())
-    device = _one_device(tensors)
-    src = [t if _dense(t) else t.contiguous() for t in tensors]
+    codes = _codes(tensors)
+    src = [t if _dense(t) else t.detach().contiguous() for t in tensors]
     if outs is None:
-        outs = [torch.empty_like(t) for t in src]
-        dst = outs
+        outs = dst = [torch.empty_like(t) for t in src]
     else:
         # an output laid out otherwise than its input is written by way of a copy
-        dst = [o if o.stride() == s.stride() and _dense(o) else torch.empty_like(s) for o, s in zip(outs, src)]
-    with torch.cuda.device(device):
-        norm, ws = _norm_buffers(tensors, device)
-        words, n = L.tensor_list(src, dst)
-        L.sla_clip_norm(n, words, kind, max_norm, norm, ws)
+        dst = [o if o is s or (o.stride() == s.stride() and _dense(o)) else torch.empty_like(s)
+               for o, s in zip(outs, src)]
+    with _on_device(tensors[0].device):
+        norm, ws = _norm_buffers(codes, tensors[0].device)
+        L.sla_clip_norm(len(src), L.tensor_list(src, codes, dst), kind, max_norm, norm, ws)
     for o, d in zip(outs, dst):
         if o is not d:
-            o.copy_(d)
+            o.detach().copy_(d)
     return outs, norm
 
 

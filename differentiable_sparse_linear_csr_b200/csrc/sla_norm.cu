@@ -220,6 +220,17 @@ clip_scale_kernel(const __grid_constant__ Table<N> t, const double *part, int n_
     table_scale(t, blockIdx.x, gridDim.x, clip_factor(v, max_norm));
 }
 
+// Both passes of a short list in one block: one launch, nothing to join.
+template <int KIND, int N>
+__global__ void __launch_bounds__(kNormThreads)
+clip_small_kernel(const __grid_constant__ Table<N> t, double max_norm, void *norm, int f64) {
+    __shared__ double red[kNormThreads / 32];
+    double v = block_join<KIND>(table_norm<KIND>(t, 0, 1), red);
+    if (KIND == kNormL2) v = sqrt(v);
+    if (threadIdx.x == 0) store_norm(norm, f64, v);
+    if (max_norm >= 0.0) table_scale(t, 0, 1, clip_factor(v, max_norm));
+}
+
 template <int N>
 int fill(Table<N> &t, const sla_tensor *list, int from, int n) {
     t.n = 0;
@@ -246,12 +257,20 @@ int num_sms() {
     return n;
 }
 
+// Chunks that one block takes faster than two launches would.
+constexpr int kSmallChunks = 4;
+
 // Pass 1 over the list, tables of N tensors at a time; then the norm alone, or
 // pass 2.  Partial results: at most kMaxPartials a table.
 template <int KIND, int N>
 sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, void *norm, int f64, double *part,
                     cudaStream_t s) {
     Table<N> t;
+    if (fill(t, list, 0, n) == n && t.chunk0[t.n] <= (unsigned)kSmallChunks) {
+        clip_small_kernel<KIND, N><<<1, kNormThreads, 0, s>>>(t, clip ? max_norm : -1.0, norm, f64);
+        SLA_CHECK_LAUNCH();
+        return SLA_OK;
+    }
     const unsigned most = std::min(kMaxPartials, num_sms() * 4);
     int n_part = 0;
     for (int i = 0; i < n;) {
@@ -262,7 +281,7 @@ sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, v
         SLA_CHECK_LAUNCH();
         n_part += (int)grid;
     }
-    if (!clip || n_part == 0) {
+    if (!clip) {
         norm_finish_kernel<KIND><<<1, kNormThreads, 0, s>>>(part, n_part, norm, f64);
         SLA_CHECK_LAUNCH();
         return SLA_OK;
