@@ -43,7 +43,8 @@ __global__ void unit_split_kernel(int n_units, int seg_len, const unsigned *__re
 
 __global__ void unit_fill_kernel(int n_units, const unsigned *__restrict__ item0, const unsigned *__restrict__ slot0,
                                  const unsigned *__restrict__ multi0, int32_t *item_unit, int32_t *item_seg,
-                                 int32_t *item_slot, int32_t *multi_unit, int32_t *multi_slot) {
+                                 int32_t *item_slot, int32_t *multi_unit, int32_t *multi_slot, int seg_len,
+                                 const int32_t *__restrict__ chunk0, int2 *item_chunks) {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;
     if (u > n_units) return;
     if (u == n_units) {
@@ -55,6 +56,10 @@ __global__ void unit_fill_kernel(int n_units, const unsigned *__restrict__ item0
         item_unit[i0 + k] = u;
         item_seg[i0 + k] = (int32_t)k;
         item_slot[i0 + k] = n > 1 ? (int32_t)(slot0[u] + k) : -1;
+        if (item_chunks) {
+            const long long from = chunk0[u] + (long long)k * seg_len, to = from + seg_len;
+            item_chunks[i0 + k] = make_int2((int)from, (int)min(to, (long long)chunk0[u + 1]));
+        }
     }
     if (n > 1) {
         multi_unit[multi0[u]] = u;
@@ -66,6 +71,7 @@ void free_plan(AttnPlan *p) {
     cudaFree(p->item_unit);
     cudaFree(p->item_seg);
     cudaFree(p->item_slot);
+    cudaFree(p->item_chunks);
     cudaFree(p->multi_unit);
     cudaFree(p->multi_slot);
     *p = AttnPlan();
@@ -80,7 +86,8 @@ __global__ void tile_len_kernel(int n_units, const int32_t *__restrict__ chunk0,
 // Items of units with the lengths len (device, [n_units + 1]).  seg_len > 0: a
 // given segment length; else one that makes about `fill` items when the units
 // are few, and at least `least`.
-sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, cudaStream_t s) {
+sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, const int32_t *chunk0,
+                       cudaStream_t s) {
     const int U = p->n_units;
     DeviceScratch tmp;
     unsigned *nseg = tmp.get<unsigned>((size_t)U + 1), *slots = tmp.get<unsigned>((size_t)U + 1),
@@ -120,12 +127,13 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
     if (p->n_multi > 0) {
         if (!alloc_array(&p->item_unit, tot[0]) || !alloc_array(&p->item_seg, tot[0]) ||
             !alloc_array(&p->item_slot, tot[0]) || !alloc_array(&p->multi_unit, tot[2]) ||
-            !alloc_array(&p->multi_slot, (size_t)tot[2] + 1)) {
+            !alloc_array(&p->multi_slot, (size_t)tot[2] + 1) || (chunk0 && !alloc_array(&p->item_chunks, tot[0]))) {
             set_error("attention plan: out of device memory");
             return SLA_ERR_OOM;
         }
         unit_fill_kernel<<<blocks_of((int64_t)U + 1), 256, 0, s>>>(U, nseg, slots, multi, p->item_unit, p->item_seg,
-                                                                   p->item_slot, p->multi_unit, p->multi_slot);
+                                                                   p->item_slot, p->multi_unit, p->multi_slot, seg_len,
+                                                                   chunk0, p->item_chunks);
         SLA_CHECK_LAUNCH();
         SLA_CHECK_CUDA(cudaStreamSynchronize(s));
     }
@@ -169,7 +177,7 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
             // columns are gathered by parts of 256 entries of a tile's longest row
             AttnPlan parts;
             parts.n_units = U;
-            st = build_items(&parts, len, 256, 0, 0, s);
+            st = build_items(&parts, len, 256, 0, 0, nullptr, s);
             if (st == SLA_OK) st = build_tiles(tiles, parts, n, rowptr, colind, s);
             free_plan(&parts);
             if (st != SLA_OK) return st;
@@ -177,7 +185,7 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
         tile_len_kernel<<<grid, 256, 0, s>>>(U, tiles->chunk0, len);
         SLA_CHECK_LAUNCH();
     }
-    st = build_items(p, len, 0, fill_of(h, level), tiled ? 64 / 16 : 64, s);
+    st = build_items(p, len, 0, fill_of(h, level), tiled ? 64 / 16 : 64, tiled ? tiles->chunk0 : nullptr, s);
     if (st == SLA_OK) p->built = true;
     return st;
 }
@@ -214,6 +222,7 @@ void use_plan(AttnArgs &a, const AttnPlan &p) {
     a.item_unit = p.item_unit;
     a.item_seg = p.item_seg;
     a.item_slot = p.item_slot;
+    a.item_chunks = p.item_chunks;
 }
 
 static void use_tiles(AttnArgs &a, const AttnTiles &t) {

@@ -13,7 +13,6 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
-#include <cstdlib>
 #include <vector>
 
 #include "sla_common.cuh"
@@ -28,6 +27,7 @@ struct AttnPlan {
     bool built = false;
     int32_t rows = 1, n_units = 0, n_items = 0, n_slots = 0, n_multi = 0, seg_len = 0, most_segs = 1;
     int32_t *item_unit = nullptr, *item_seg = nullptr, *item_slot = nullptr;   // [n_items]
+    int2 *item_chunks = nullptr;       // tiles: [n_items] first and last (excluded) chunk
     int32_t *multi_unit = nullptr;                                             // [n_multi]
     int32_t *multi_slot = nullptr;                                             // [n_multi + 1]
 };
@@ -63,7 +63,6 @@ inline int attn_level(const Csr *h, const sla_attn_opts *o) {
 
 // 16-bit heads of whole 16-element steps go through the tensor cores.
 inline bool attn_tiled(const sla_attn_opts *o) {
-    if (getenv("SLA_ATTN_ROWS")) return false;
     return (o->dtype == SLA_BF16 || o->dtype == SLA_F16) && o->dim % 16 == 0 && o->dim <= 128;
 }
 
@@ -75,7 +74,8 @@ struct AttnArgs {
     const int32_t *rowptr, *colind, *perm;
     int32_t n_items, n_slots, seg_len;
     const int32_t *item_unit, *item_seg, *item_slot;
-    const int32_t *chunk0;                 // tiles
+    const int32_t *chunk0;                 // tiles: chunks of each unit, and of each item of a split plan
+    const int2 *item_chunks;
     const TileChunk *chunks;
     const void *q, *k, *v, *o, *dout;
     int64_t qs[3], ks[3], vs[3], ds[3];    // system, row, head

@@ -269,26 +269,6 @@ struct Own {
             }
         }
     }
-    // Row g + 8 i's dot product with the same elements of 32-bit rows, this
-    // thread's share.
-    template <typename T>
-    __device__ __forceinline__ float dot(const float *p, int i, int c) const {
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            // k step j: elements 32 (j / 2) + 8 c + 4 (j % 2) + 0..3, or 4 c + 0..3 of the last 16
-            const int d = j / 2 < D / 32 ? 32 * (j / 2) + 8 * c + 4 * (j % 2) : D / 32 * 32 + 4 * c;
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(p + d));
-            uint32_t e0, e1, e2, e3;
-            widen<T>(a[j][i], e0, e1);
-            widen<T>(a[j][2 + i], e2, e3);
-            s = fmaf(__uint_as_float(e0), x.x, s);
-            s = fmaf(__uint_as_float(e1), x.y, s);
-            s = fmaf(__uint_as_float(e2), x.z, s);
-            s = fmaf(__uint_as_float(e3), x.w, s);
-        }
-        return s;
-    }
 };
 
 // s[2][4]: the products of the 16 own rows with the 16 staged columns of a chunk,
@@ -430,7 +410,7 @@ struct Sums {
     }
 };
 
-// A warp's work: chunks [ch0, ch1) of a tile, heads h (and following) of one
+// A piece of work: chunks [ch0, ch1) of a tile, heads h (and following) of one
 // system, whose key heads start at kh.
 struct TileWork {
     int64_t row0;
@@ -438,28 +418,79 @@ struct TileWork {
     const TileChunk *ch0, *ch1;
 };
 
-// Head groups of n_h heads; y counts systems and the groups of key heads (n_kh
-// of them each), x items and, within a key head, the groups of its query heads.
-__device__ __forceinline__ bool tile_item(TileWork &w, const AttnArgs &a, unsigned x, unsigned y, unsigned n_h,
-                                          unsigned n_kh, unsigned groups) {
-    const unsigned it = x / groups, ky = (unsigned)a.kv_heads / n_kh;
-    if (it >= (unsigned)a.n_items) return false;
-    w.b = (int)(y / ky);
-    w.kh = (int)((y - (unsigned)w.b * ky) * n_kh);
-    w.h = w.kh * (a.heads / a.kv_heads) + (int)((x - it * groups) * n_h);
-    int unit = (int)it, seg = 0;
-    w.slot = -1;
-    if (a.item_unit) {
-        unit = __ldg(a.item_unit + it);
-        seg = __ldg(a.item_seg + it);
-        w.slot = __ldg(a.item_slot + it);
+// The pieces of work a warp takes, every `stride`-th of the list ordered by
+// system, key head, tile and query head: the warps of the GPU sweep the pattern
+// together, one key head (or group) after the other, so that the rows it gathers
+// stay in the L2 cache.
+struct Cursor {
+    unsigned x;                // place within a (system, key head group): item * groups + group
+    int b, kh;                 // system, first key head
+    __device__ __forceinline__ unsigned item(unsigned groups) const { return groups == 1 ? x : x / groups; }
+    __device__ __forceinline__ int head(unsigned groups, int share, int n_h) const {
+        return kh * share + (groups == 1 ? 0 : (int)(x % groups) * n_h);
     }
-    w.row0 = (int64_t)unit * kTileRows;
-    const int c0 = __ldg(a.chunk0 + unit), c1 = __ldg(a.chunk0 + unit + 1);
-    const int64_t from = (int64_t)c0 + (int64_t)seg * a.seg_len, to = from + a.seg_len;
-    w.ch0 = a.chunks + from;
-    w.ch1 = a.chunks + (to < c1 ? to : (int64_t)c1);
-    return true;
+};
+struct Stride {
+    unsigned per_y, x;         // the stride in the cursor's three digits
+    int b, kh, n_kh, kv_heads;
+    __device__ __forceinline__ Stride(unsigned by, unsigned items, unsigned groups, int n_kh_, int kv_heads_)
+        : per_y(items * groups), n_kh(n_kh_), kv_heads(kv_heads_) {
+        const Cursor c = at(by);
+        x = c.x;
+        b = c.b;
+        kh = c.kh;
+    }
+    __device__ __forceinline__ Cursor at(unsigned place) const {
+        const unsigned y = place / per_y, ky = (unsigned)(kv_heads / n_kh);
+        Cursor c;
+        c.x = place - y * per_y;
+        c.b = (int)(y / ky);
+        c.kh = (int)(y - (unsigned)c.b * ky) * n_kh;
+        return c;
+    }
+    __device__ __forceinline__ void move(Cursor &c) const {
+        c.x += x;
+        c.kh += kh;
+        c.b += b;
+        if (c.x >= per_y) {
+            c.x -= per_y;
+            c.kh += n_kh;
+        }
+        if (c.kh >= kv_heads) {
+            c.kh -= kv_heads;
+            ++c.b;
+        }
+    }
+};
+
+__device__ __forceinline__ int2 item_range(const AttnArgs &a, unsigned it) {
+    if (a.item_chunks) return __ldg(a.item_chunks + it);
+    return make_int2(__ldg(a.chunk0 + it), __ldg(a.chunk0 + it + 1));
+}
+
+__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c, unsigned groups, int share, int n_h) {
+    TileWork w;
+    const unsigned it = c.item(groups);
+    w.b = c.b;
+    w.kh = c.kh;
+    w.h = c.head(groups, share, n_h);
+    w.row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+    w.slot = a.item_unit ? __ldg(a.item_slot + it) : -1;
+    const int2 r = item_range(a, it);
+    w.ch0 = a.chunks + r.x;
+    w.ch1 = a.chunks + r.y;
+    return w;
+}
+
+// Brings the lines of rows that will be loaded soon into the L2 cache: lane r < 16
+// names row r's D elements.
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_rows(const T *base, int64_t stride, int64_t row0, int n_rows, int lane) {
+    if (lane < kTileRows && row0 + lane < n_rows) {
+        const T *p = base + (row0 + lane) * stride;
+#pragma unroll
+        for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+    }
 }
 
 // What a thread keeps of a chunk: rows g's and g + 8's bits and, with ENTRIES,
@@ -626,33 +657,106 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
     }
 }
 
+// The producing side of a warp's ring: copies chunk after chunk, across the
+// pieces of work, ahead of the consuming loop.  `open(cursor)` is called at the
+// first chunk of a piece, `copy(stage, col)` for every chunk.
+template <typename R>
+struct Feed {
+    Cursor cur;
+    unsigned left, col;                    // pieces of work not yet begun; columns of the chunk at `at`
+    const TileChunk *at, *end;
+    int2 next;                             // chunks of the piece after this one
+    int write;
+    bool more;
+
+    // The next chunk, if there is one, and its columns (a load that is due only at
+    // the next copy).
+    template <typename Open>
+    __device__ __forceinline__ void seek(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, Open &&open) {
+        while (at == end) {
+            if (left == 0) {
+                more = false;
+                return;
+            }
+            --left;
+            at = a.chunks + next.x;
+            end = a.chunks + next.y;
+            open(cur);
+            if (left > 0) {
+                stride.move(cur);
+                next = item_range(a, cur.item(groups));
+            }
+        }
+        col = chunk_column(at, lane, n_cols);
+    }
+    template <typename Open>
+    __device__ __forceinline__ void start(const AttnArgs &a, const Cursor &c, unsigned count, const Stride &stride, unsigned groups,
+                                          int lane, int n_cols, Open &&open) {
+        cur = c;
+        left = count;
+        at = end = nullptr;
+        write = 0;
+        more = true;
+        if (count > 0) next = item_range(a, cur.item(groups));
+        seek(a, stride, groups, lane, n_cols, open);
+    }
+    template <typename Open, typename Copy>
+    __device__ __forceinline__ void advance(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, char *ring,
+                                            Open &&open, Copy &&copy) {
+        if (more) {
+            copy(ring + write, col);
+            write = write == (R::kStages - 1) * R::kStage ? 0 : write + R::kStage;
+            ++at;
+            seek(a, stride, groups, lane, n_cols, open);
+        }
+        cp_commit();
+    }
+};
+
+// Pieces of work of this warp out of `total`.
+__device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, unsigned &stride) {
+    first = blockIdx.x * kTileWarps + (threadIdx.x >> 5);
+    stride = gridDim.x * kTileWarps;
+    return first < total ? (total - first + stride - 1) / stride : 0;
+}
+
 // H heads a warp, on KH key heads (H: one each; 1: one for all).
 template <typename T, int D, int H, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kTileThreads, D * H <= 64 ? 3 : 2)
+tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
+    const unsigned groups = (unsigned)share * KH / H;
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
-    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
-        TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
-        const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
-        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
-        const int n = (int)(w.ch1 - w.ch0);
-        auto issue = [&](char *st, unsigned col) {
-            R::gather(st, kb, kst, a.ks[2], col, lane);
-            R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
-        };
-        __syncwarp();
+    unsigned first, by;
+    const unsigned count = my_share(total, first, by);
+    if (count == 0) return;
+    const Stride stride(by, (unsigned)a.n_items, groups, KH, a.kv_heads);
+    Cursor now = stride.at(first);
+    Feed<R> feed;
+    const T *kb = nullptr, *vb = nullptr;                // of the piece the feed is at
+    auto open = [&](const Cursor &f) {
+        kb = static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2];
+        vb = static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2];
+        const unsigned it = f.item(groups);
+        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+        prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + f.head(groups, share, H) * a.qs[2], a.qs[1],
+                                row0, a.n_rows, lane);
+    };
+    auto copy = [&](char *st, unsigned col) {
+        R::gather(st, kb, kst, a.ks[2], col, lane);
+        R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
+    };
+    feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
 #pragma unroll
-        for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < n) issue(ring + i * R::kStage, chunk_column(w.ch0 + i, lane, a.n_cols));
-            cp_commit();
-        }
-        unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
+    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    int st_read = 0;
+    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
+        const TileWork w = tile_work(a, now, groups, share, H);
+        const int n = (int)(w.ch1 - w.ch0);
         Own<D> q[H];
 #pragma unroll
         for (int j = 0; j < H; ++j)
@@ -674,7 +778,6 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
             if (n > 0) cur.values(x_next, vals, c);
             if (n > 1) next.load(w.ch0 + 1, g);
         }
-        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
         for (int ch = 0; ch < n; ++ch) {
             // bookkeeping of this chunk, and loads of the next one's
             float x[2][4];
@@ -696,12 +799,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_forward_kernel(const __grid
             }
             cp_wait<R::kStages - 2>();
             __syncwarp();
-            if (ch + R::kStages - 1 < n) issue(ring + st_write, col);
-            cp_commit();
-            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
+            feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
             const char *stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
-            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
             unsigned mine[2] = {bits[0] >> (2 * c), bits[1] >> (2 * c)}, used = 0;
             bool drop = false;
             if constexpr (VALS) {
@@ -862,33 +962,75 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
     }
 }
 
-// By A's rows: (lse, D) of every row, dq, and ds of every entry if asked for.
+// (lse, D = dout . o) of every row and head, for both kernels below; lse in the unit
+// of relative().  G lanes a row and head, 8 elements each.
+template <typename T, int G>
+__global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__ AttnArgs a, int64_t count, float unit) {
+    const int64_t x = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
+    const int l = threadIdx.x % G;
+    if (x - threadIdx.x % 32 / G >= count) return;       // whole warps
+    const int64_t row = x / a.heads, b = row / a.n_rows;
+    const int h = (int)(x - row * a.heads);
+    float s = 0.0f;
+    if (x < count && l * 8 < a.dim) {
+        const uint4 d = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dout) + b * a.ds[0] +
+                                                              (row - b * a.n_rows) * a.ds[1] + h * a.ds[2]) + l);
+        const float4 *o = reinterpret_cast<const float4 *>(static_cast<const float *>(a.o) + x * a.dim) + 2 * l;
+        const float4 o0 = __ldg(o), o1 = __ldg(o + 1);
+        uint32_t e[8];
+        widen<T>(d.x, e[0], e[1]);
+        widen<T>(d.y, e[2], e[3]);
+        widen<T>(d.z, e[4], e[5]);
+        widen<T>(d.w, e[6], e[7]);
+        const float y[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s = fmaf(__uint_as_float(e[i]), y[i], s);
+    }
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    if (x < count && l == 0)
+        a.stat[(b * a.heads + h) * a.n_rows + (row - b * a.n_rows)] =
+            make_float2(__ldg(static_cast<const float *>(a.lse) + x) * unit, s);
+}
+
+// By A's rows: dq, and ds of every entry if asked for.
 template <typename T, int D, int H, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kTileThreads, D * H <= 64 ? 3 : 2)
+tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)(a.heads / a.kv_heads) * KH / H, n_y = (unsigned)a.batch * (a.kv_heads / KH);
+    const unsigned groups = (unsigned)share * KH / H;
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
-    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
-        TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, H, KH, groups)) return;
-        const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
-        const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
-        const int n = (int)(w.ch1 - w.ch0);
-        auto issue = [&](char *st, unsigned col) {
-            R::gather(st, kb, kst, a.ks[2], col, lane);
-            R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
-        };
-        __syncwarp();
+    unsigned first, by;
+    const unsigned count = my_share(total, first, by);
+    if (count == 0) return;
+    const Stride stride(by, (unsigned)a.n_items, groups, KH, a.kv_heads);
+    Cursor now = stride.at(first);
+    Feed<R> feed;
+    const T *kb = nullptr, *vb = nullptr;
+    auto open = [&](const Cursor &f) {
+        kb = static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2];
+        vb = static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2];
+        const unsigned it = f.item(groups);
+        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+        const int h = f.head(groups, share, H);
+        prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + h * a.qs[2], a.qs[1], row0, a.n_rows, lane);
+        prefetch_rows<T, D * H>(static_cast<const T *>(a.dout) + f.b * a.ds[0] + h * a.ds[2], a.ds[1], row0, a.n_rows, lane);
+    };
+    auto copy = [&](char *st, unsigned col) {
+        R::gather(st, kb, kst, a.ks[2], col, lane);
+        R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
+    };
+    feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
 #pragma unroll
-        for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < n) issue(ring + i * R::kStage, chunk_column(w.ch0 + i, lane, a.n_cols));
-            cp_commit();
-        }
-        unsigned col = R::kStages - 1 < n ? chunk_column(w.ch0 + R::kStages - 1, lane, a.n_cols) : 0;
+    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    int st_read = 0;
+    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
+        const TileWork w = tile_work(a, now, groups, share, H);
+        const int n = (int)(w.ch1 - w.ch0);
         Own<D> q[H], go[H];
         float lse[H][2], delta[H][2];
         bool dead[H][2];
@@ -901,19 +1043,12 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
             acc[j].zero();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t row = w.row0 + g + 8 * i, at = ((int64_t)w.b * a.n_rows + row) * a.heads + h;
-                lse[j][i] = none;
-                delta[j][i] = 0.0f;
-                if (row < a.n_rows) {
-                    lse[j][i] = __ldg(static_cast<const float *>(a.lse) + at);
-                    delta[j][i] = go[j].template dot<T>(static_cast<const float *>(a.o) + at * D, i, c);
-                }
-                delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 1);
-                delta[j][i] += __shfl_xor_sync(kAll, delta[j][i], 2);
-                dead[j][i] = lse[j][i] == none;
-                if constexpr (!VALS) lse[j][i] *= kLog2e;       // the unit of relative()
-                if (row < a.n_rows && c == 0)
-                    a.stat[((int64_t)w.b * a.heads + h) * a.n_rows + row] = make_float2(lse[j][i], delta[j][i]);
+                const int64_t row = w.row0 + g + 8 * i;
+                float2 st = make_float2(none, 0.0f);
+                if (row < a.n_rows) st = __ldg(a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows + row);
+                lse[j][i] = st.x;
+                delta[j][i] = st.y;
+                dead[j][i] = st.x == none;
             }
         }
         float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
@@ -923,7 +1058,6 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
         if (n > 0) next.load(w.ch0, g);
         if constexpr (VALS)
             if (n > 0) next.values(x_next, vals, c);
-        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
         for (int ch = 0; ch < n; ++ch) {
             cur = next;
             float x[2][4];
@@ -934,12 +1068,9 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_rows_kernel(const __gri
             if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
             cp_wait<R::kStages - 2>();
             __syncwarp();
-            if (ch + R::kStages - 1 < n) issue(ring + st_write, col);
-            cp_commit();
-            if (ch + R::kStages < n) col = chunk_column(w.ch0 + ch + R::kStages, lane, a.n_cols);
+            feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
             const char *stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
-            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
             const unsigned there[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
             unsigned mine[2] = {there[0], there[1]}, used = 0;
             bool drop = false;
@@ -1073,17 +1204,64 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 // both sums and both own operands would not fit the registers.  The values come in
 // A^T's order (tile_values_kernel).
 template <typename T, int D, int KH, bool DK, bool DV, bool VALS>
-__global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kTileThreads, 2)
+tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, true>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned n_y = (unsigned)a.batch * (a.kv_heads / KH);
     const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
-    for (unsigned y = blockIdx.y; y < n_y; y += gridDim.y) {
-        TileWork w;
-        if (!tile_item(w, a, blockIdx.x * kTileWarps + (threadIdx.x >> 5), y, KH, KH, 1)) return;
+    unsigned first, by;
+    const unsigned count = my_share(total, first, by);
+    if (count == 0) return;
+    // A piece is a tile with one of the query heads of its key heads; the shared heads
+    // of a tile follow each other and its sums are written after the last one.
+    const Stride stride(by, (unsigned)a.n_items, 1, KH, a.kv_heads);
+    Cursor now = stride.at(first);
+    Feed<R> feed = {};
+    const T *qb = nullptr, *gb = nullptr;
+    const float2 *stat = nullptr;
+    const TileChunk *begin = nullptr;                    // of the feed's tile, and its shared head
+    int fh = 0;
+    auto open_head = [&](int b, int h) {
+        qb = static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2];
+        gb = static_cast<const T *>(a.dout) + b * a.ds[0] + h * a.ds[2];
+        stat = a.stat + ((int64_t)b * a.heads + h) * a.n_rows;
+    };
+    int fb = 0, fkh = 0;
+    auto open = [&](const Cursor &f) {
+        begin = feed.at;
+        fh = 0;
+        fb = f.b;
+        fkh = f.kh;
+        open_head(f.b, f.kh * share);
+        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + f.x) : (int)f.x) * kTileRows;
+        prefetch_rows<T, D * KH>(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[1], row0, a.n_cols, lane);
+        if (DK)
+            prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], row0, a.n_cols, lane);
+    };
+    auto copy = [&](char *st, unsigned col) {
+        R::gather(st, qb, qst, a.qs[2], col, lane);
+        R::gather(st + R::kTensor, gb, dst, a.ds[2], col, lane);
+#pragma unroll
+        for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
+            const int jj = KH == 1 ? 0 : j + (lane >> 4);
+            if (KH > 1 || lane < 16)
+                cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8, stat + (int64_t)jj * a.n_rows + col);
+        }
+        if (KH == 1 && feed.at + 1 == feed.end && fh + 1 < share) {     // the tile again, with its next head
+            ++fh;
+            open_head(fb, fkh * share + fh);
+            feed.at = begin - 1;
+        }
+    };
+    feed.start(a, now, count, stride, 1, lane, a.n_rows, open);
+#pragma unroll
+    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
+    int st_read = 0;
+    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
+        const TileWork w = tile_work(a, now, 1, share, KH);
         Own<D> k[KH], v[DK ? KH : 1];
         Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
@@ -1095,58 +1273,35 @@ __global__ void __launch_bounds__(kTileThreads) tile_bwd_cols_kernel(const __gri
             }
             if constexpr (DV) dv[j].zero();
         }
-        const int n = (int)(w.ch1 - w.ch0), total = n * share;
-        // step x: chunk x % n of the query heads kh * share + x / n (KH > 1: share is 1)
-        auto issue = [&](char *st, int x, unsigned col) {
-            const int h = w.kh * share + (KH == 1 ? x / n : 0);
-            R::gather(st, static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, a.qs[2], col, lane);
-            R::gather(st + R::kTensor, static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, a.ds[2], col, lane);
-            const float2 *stat = a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows + col;
-#pragma unroll
-            for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
-                const int jj = KH == 1 ? 0 : j + (lane >> 4);
-                if (KH > 1 || lane < 16)
-                    cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8, stat + (int64_t)jj * a.n_rows);
-            }
-        };
-        auto chunk = [&](int x) { return w.ch0 + (KH == 1 ? x % n : x); };
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < R::kStages - 1; ++i) {
-            if (i < total) issue(ring + i * R::kStage, i, chunk_column(chunk(i), lane, a.n_rows));
-            cp_commit();
-        }
-        unsigned col = R::kStages - 1 < total ? chunk_column(chunk(R::kStages - 1), lane, a.n_rows) : 0;
+        const int n = (int)(w.ch1 - w.ch0), steps = n * (KH == 1 ? share : 1);
+        int ci = 0;                                      // chunk of the step
         Chunk<VALS> next;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
-        if (total > 0) next.load(w.ch0, g);
+        if (n > 0) next.load(w.ch0, g);
         if constexpr (VALS)
-            if (total > 0) next.values(x_next, vals, c);
-        int st_read = 0, st_write = (R::kStages - 1) * R::kStage;
-        for (int x = 0; x < total; ++x) {
+            if (n > 0) next.values(x_next, vals, c);
+        for (int x = 0; x < steps; ++x) {
             unsigned mine[2] = {next.bits[0] >> (2 * c), next.bits[1] >> (2 * c)}, used = 0;
             float val[2][4];
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) val[blk][e] = x_next[blk][e];
-            if (x + 1 < total) next.load(chunk(x + 1), g);
+            ci = ci + 1 == n ? 0 : ci + 1;
+            if (x + 1 < steps) next.load(w.ch0 + ci, g);
             cp_wait<R::kStages - 2>();
             __syncwarp();
-            if (x + R::kStages - 1 < total) issue(ring + st_write, x + R::kStages - 1, col);
-            cp_commit();
-            if (x + R::kStages < total) col = chunk_column(chunk(x + R::kStages), lane, a.n_rows);
+            feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
             const char *stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
-            st_write = st_write == (R::kStages - 1) * R::kStage ? 0 : st_write + R::kStage;
 #pragma unroll
             for (int j = 0; j < KH; ++j) {
                 const int p0 = j * (D / 8);
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, k[j], stage, p0, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], stage + R::kTensor, p0, g, c);
-                if (VALS && j == 0 && x + 1 < total) next.values(x_next, vals, c);
+                if (VALS && j == 0 && x + 1 < steps) next.values(x_next, vals, c);
                 const float4 *sp = reinterpret_cast<const float4 *>(stage + 2 * R::kTensor + j * 128);
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
@@ -1234,16 +1389,20 @@ enum { kTileFwd, kTileBwdRows, kTileBwdCols };
 template <typename T, int D, int H, int KH, bool VALS>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
     const bool cols = what == kTileBwdCols;
-    const int64_t warps = (int64_t)a.n_items * (cols ? 1 : a.heads / a.kv_heads * KH / H);
-    const int64_t x = (warps + kTileWarps - 1) / kTileWarps, y = (int64_t)a.batch * (a.kv_heads / KH);
-    SLA_REQUIRE(x < INT_MAX / kTileWarps && y < INT_MAX, "sla_attention: too many rows, systems and heads");
-    if (x == 0) return SLA_OK;
-    const dim3 grid((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
+    const int64_t total = (int64_t)a.n_items * (cols ? 1 : a.heads / a.kv_heads * KH / H) * a.batch * (a.kv_heads / KH);
+    SLA_REQUIRE(total < INT_MAX, "sla_attention: too many rows, systems and heads");
+    if (total == 0) return SLA_OK;
+    // as many blocks as run at once, each warp going through the work in strides
     auto go = [&](auto *kernel, int ring) -> sla_status {
         const int bytes = ring * kTileWarps;
         if (bytes > 48 * 1024)
             SLA_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-        kernel<<<grid, kTileThreads, bytes, s>>>(a);
+        int per_sm = 0, dev = 0, sms = 0;
+        SLA_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kTileThreads, bytes));
+        SLA_CHECK_CUDA(cudaGetDevice(&dev));
+        SLA_CHECK_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        const int64_t blocks = (total + kTileWarps - 1) / kTileWarps, most = (int64_t)(per_sm > 0 ? per_sm : 1) * sms;
+        kernel<<<(unsigned)(blocks < most ? blocks : most), kTileThreads, bytes, s>>>(a, (unsigned)total);
         SLA_CHECK_LAUNCH();
         return SLA_OK;
     };
@@ -1260,6 +1419,22 @@ sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
         }
     }
     return SLA_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+sla_status launch_delta(const AttnArgs &a, cudaStream_t s) {
+    const int64_t count = (int64_t)a.batch * a.n_rows * a.heads;
+    if (count == 0) return SLA_OK;
+    const float unit = a.vals ? 1.0f : kLog2e;
+    auto go = [&](auto *kernel, int lanes) -> sla_status {
+        kernel<<<blocks_of(count * lanes), 256, 0, s>>>(a, count, unit);
+        SLA_CHECK_LAUNCH();
+        return SLA_OK;
+    };
+    if (a.dim <= 16) return go(tile_delta_kernel<T, 2>, 2);
+    if (a.dim <= 32) return go(tile_delta_kernel<T, 4>, 4);
+    if (a.dim <= 64) return go(tile_delta_kernel<T, 8>, 8);
+    return go(tile_delta_kernel<T, 16>, 16);
 }
 
 // Heads a warp: as many as fill 128 bytes of a gathered row, if their number
@@ -1351,6 +1526,8 @@ template <typename T> sla_status attn_tile_bwd_rows(AttnArgs a, cudaStream_t s) 
         if (st != SLA_OK) return st;
         a.vals_f = a.vals_w;
     }
+    const sla_status st = launch_delta<T>(a, s);
+    if (st != SLA_OK || (!a.dq && !a.ds_out)) return st;
     return launch_tile_of<T>(kTileBwdRows, a, s);
 }
 template <typename T> sla_status attn_tile_bwd_cols(AttnArgs a, cudaStream_t s) {
