@@ -11,11 +11,12 @@
 // Each warp copies the chunk's rows into its own ring of shared-memory stages
 // (cp.async, a few chunks ahead: the loads' latency is what the kernels wait for)
 // and reads them from there twice, as columns of the scores and as rows of the
-// sums.  The 16-byte pieces of a row are permuted by its number so that both
-// reads are free of bank conflicts.  A dot product does not depend on the order of
-// its terms, so thread (g, c) of a quad layout (g = lane / 4, c = lane % 4) takes
-// piece 4 i + c of a column as its places of the k steps 2 i and 2 i + 1, and in
+// sums.  A dot product does not depend on the order of its terms, so thread (g, c)
+// of a quad layout (g = lane / 4, c = lane % 4) takes the 16-byte pieces 8 i + 2c
+// and 8 i + 2c + 1 of a column as its places of the k steps 4 i to 4 i + 3, and in
 // the sums piece 8 i + g, element e, as output block 8 i + e: whole 16-byte reads.
+// Rows lie an odd number of pieces apart (1 modulo 8), which keeps both reads free
+// of bank conflicts and every address a constant away from one number a lane.
 // Narrow heads go several to a warp, so that a gathered row is at least 128
 // consecutive bytes and the chunk's bookkeeping is shared; so do heads that
 // share their key head, which is then fetched once.
@@ -132,52 +133,62 @@ __global__ void tile_chunks_kernel(int n_units, int n_parts, const unsigned *__r
 }
 
 // ------------------------------------------------------------ operands ----
-__device__ __forceinline__ uint4 lds16(const char *p) { return *reinterpret_cast<const uint4 *>(p); }
-__device__ __forceinline__ uint2 lds8(const char *p) { return *reinterpret_cast<const uint2 *>(p); }
+__device__ __forceinline__ uint4 lds16(unsigned p) {
+    uint4 x;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(p));
+    return x;
+}
+__device__ __forceinline__ uint2 lds8(unsigned p) {
+    uint2 x;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(p));
+    return x;
+}
+__device__ __forceinline__ uint32_t lds4(unsigned p) {
+    uint32_t x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(p));
+    return x;
+}
 
 // One head's row: D elements in pieces of 8 (16 bytes).  What a thread takes of it:
-//   scores: pieces 4 i + c (i < D / 32), then 8 bytes of the last two pieces if
-//           D is not a multiple of 32;  word 2 s, 2 s + 1 belong to k step s;
-//   sums:   pieces 8 i + g (i < D / 64), then 8 bytes of the next four pieces,
-//           then 4 bytes of the next two; word w holds output blocks 2 w, 2 w + 1.
-// A staged row r starts at r * pitch; its piece p is found at p ^ swizzle(r).
-__device__ __forceinline__ int swizzle(int r) { return ((r ^ (r >> 2)) & 1) << 2 | (r & 2); }
-__device__ __forceinline__ int piece_at(int p, int r) { return (p ^ swizzle(r)) * 16; }
-
+//   scores: pieces 8 i + 2c, 8 i + 2c + 1 (i < D / 64), piece c of the next four,
+//           8 bytes of the last two;  words 2 s, 2 s + 1 belong to k step s;
+//   sums:   pieces 8 i + g (i < D / 64), 8 bytes of the next four, 4 bytes of the
+//           last two;  word w holds output blocks 2 w, 2 w + 1.
+// Addresses are shared-memory ones; `row` includes nothing of c or g.
 template <int D>
-__device__ __forceinline__ void read_score(uint32_t (&w)[D / 8], const char *row, int r, int p0, int c) {
+__device__ __forceinline__ void read_score(uint32_t (&w)[D / 8], unsigned row, int c) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-        const uint4 x = lds16(row + piece_at(p0 + 4 * i + c, r));
+        const uint4 x = i < D / 64 * 2 ? lds16(row + c * 32 + (i >> 1) * 128 + (i & 1) * 16)
+                                       : lds16(row + c * 16 + D / 64 * 128);
         w[4 * i] = x.x;
         w[4 * i + 1] = x.y;
         w[4 * i + 2] = x.z;
         w[4 * i + 3] = x.w;
     }
     if constexpr (D % 32 != 0) {
-        const uint2 x = lds8(row + piece_at(p0 + D / 8 - 2 + (c >> 1), r) + (c & 1) * 8);
+        const uint2 x = lds8(row + c * 8 + D / 32 * 64);
         w[D / 8 - 2] = x.x;
         w[D / 8 - 1] = x.y;
     }
 }
 
 template <int D>
-__device__ __forceinline__ void read_sum(uint32_t (&w)[D / 16], const char *row, int r, int p0, int g) {
+__device__ __forceinline__ void read_sum(uint32_t (&w)[D / 16], unsigned row, int g) {
 #pragma unroll
     for (int i = 0; i < D / 64; ++i) {
-        const uint4 x = lds16(row + piece_at(p0 + 8 * i + g, r));
+        const uint4 x = lds16(row + g * 16 + i * 128);
         w[4 * i] = x.x;
         w[4 * i + 1] = x.y;
         w[4 * i + 2] = x.z;
         w[4 * i + 3] = x.w;
     }
     if constexpr (D % 64 >= 32) {
-        const uint2 x = lds8(row + piece_at(p0 + D / 64 * 8 + (g >> 1), r) + (g & 1) * 8);
+        const uint2 x = lds8(row + g * 8 + D / 64 * 128);
         w[D / 64 * 4] = x.x;
         w[D / 64 * 4 + 1] = x.y;
     }
-    if constexpr (D % 32 != 0)
-        w[D / 16 - 1] = *reinterpret_cast<const uint32_t *>(row + piece_at(p0 + D / 8 - 2 + (g >> 2), r) + (g & 3) * 4);
+    if constexpr (D % 32 != 0) w[D / 16 - 1] = lds4(row + g * 4 + D / 32 * 64);
 }
 
 template <typename T>
@@ -256,7 +267,8 @@ struct Own {
             const char *p = reinterpret_cast<const char *>(base + (row0 + g + 8 * i) * stride);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
-                const uint4 x = on ? __ldg(reinterpret_cast<const uint4 *>(p) + 4 * j + c) : make_uint4(0, 0, 0, 0);
+                const int at = j < D / 64 * 2 ? c * 2 + (j >> 1) * 8 + (j & 1) : c + D / 64 * 8;
+                const uint4 x = on ? __ldg(reinterpret_cast<const uint4 *>(p) + at) : make_uint4(0, 0, 0, 0);
                 a[2 * j][i] = x.x;
                 a[2 * j][2 + i] = x.y;
                 a[2 * j + 1][i] = x.z;
@@ -274,12 +286,11 @@ struct Own {
 // s[2][4]: the products of the 16 own rows with the 16 staged columns of a chunk,
 // the columns 8 blk + (2c, 2c + 1) of rows g and g + 8 in this thread.
 template <typename T, int D, int PITCH>
-__device__ __forceinline__ void score_products(float (&s)[2][4], const Own<D> &own, const char *stage, int p0, int g,
-                                               int c) {
+__device__ __forceinline__ void score_products(float (&s)[2][4], const Own<D> &own, unsigned stage, int g, int c) {
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
         uint32_t k[D / 8];
-        read_score<D>(k, stage + (8 * blk + g) * PITCH, 8 * blk + g, p0, c);
+        read_score<D>(k, stage + g * PITCH + 8 * blk * PITCH, c);
         s[blk][0] = s[blk][1] = s[blk][2] = s[blk][3] = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) mma16<T>(s[blk], own.a[i], k[2 * i], k[2 * i + 1]);
@@ -343,25 +354,26 @@ struct Sums {
             }
         }
     }
+    // A NaN among the sums of any thread (or infinities of both signs).
     __device__ __forceinline__ bool bad() const {
-        bool b = false;
+        float2 t = make_float2(0.0f, 0.0f);
+        const float2 one = make_float2(1.0f, 1.0f);
 #pragma unroll
-        for (int nb = 0; nb < D / 8; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) b = b || o[nb][i] != o[nb][i];
-        return __any_sync(kAll, b);
+        for (int nb = 0; nb < D / 8; ++nb) {
+            t = fma2(make_float2(o[nb][0], o[nb][1]), one, t);
+            t = fma2(make_float2(o[nb][2], o[nb][3]), one, t);
+        }
+        const float u = t.x + t.y;
+        return __any_sync(kAll, u != u);
     }
     // All of a chunk: the weights w[2][4] with the staged rows.  drop, used: see
     // drop_unused.
     template <int PITCH>
-    __device__ __forceinline__ void add_chunk(const float (&w)[2][4], const char *stage, int p0, int g, int c,
-                                              bool drop, unsigned used) {
+    __device__ __forceinline__ void add_chunk(const float (&w)[2][4], unsigned stage, int g, int c, bool drop,
+                                              unsigned used) {
         uint32_t x[4][D / 16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 8 * (j >> 1) + 2 * c + (j & 1);
-            read_sum<D>(x[j], stage + r * PITCH, r, p0, g);
-        }
+        for (int j = 0; j < 4; ++j) read_sum<D>(x[j], stage + 2 * c * PITCH + (8 * (j >> 1) + (j & 1)) * PITCH, g);
         if (drop) drop_unused(x, used);
         add(w[0], x[0], x[1]);
         add(w[1], x[2], x[3]);
@@ -527,13 +539,11 @@ struct Chunk {
     }
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;"
-                 :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async16(unsigned dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
-                 :: "r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+__device__ __forceinline__ void cp_async8(unsigned dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
@@ -543,24 +553,31 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 template <int D, int HEADS, bool STAT>
 struct Ring {
     static constexpr int kPieces = D / 8 * HEADS;                       // of a row
-    static constexpr int kPitch = (kPieces + 7) / 8 * 128;
+    static constexpr int kPitch = (kPieces + 7) / 8 * 128 + 16;
     static constexpr int kTensor = 16 * kPitch;
     static constexpr int kStage = 2 * kTensor + (STAT ? 16 * 8 * HEADS : 0);
-    static constexpr int kStages = kStage <= 4608 ? 3 : 2;
+    static constexpr int kStages = kStage <= 5120 ? 3 : 2;
     static constexpr int kBytes = kStage * kStages;
+    static constexpr bool kEven = 32 % kPieces == 0;                    // a lane has one piece of every row it copies
 
-    // Copies of one tensor's rows of the columns in `col` (lane r: column r).
-    template <typename T>
-    static __device__ __forceinline__ void gather(char *stage, const T *base, unsigned stride, int64_t head_stride,
-                                                  unsigned col, int lane) {
+    // Where this lane's pieces start in a tensor, with a head's stride in bytes.
+    static __device__ __forceinline__ const char *source(const void *base, int64_t head_bytes, int lane) {
+        const char *p = static_cast<const char *>(base);
+        if constexpr (!kEven) return p;
+        const int x = lane % kPieces;
+        return p + x / (D / 8) * head_bytes + x % (D / 8) * 16;
+    }
+    // Copies of both tensors' rows of the columns in `col` (lane r: column r).
+    static __device__ __forceinline__ void gather(unsigned stage, const char *p0, unsigned stride0, const char *p1,
+                                                  unsigned stride1, unsigned col, int lane) {
 #pragma unroll
         for (int i = 0; i < kPieces / 2; ++i) {
-            const int x = i * 32 + lane, r = x / kPieces, p = x - r * kPieces;
-            const unsigned cl = __shfl_sync(kAll, col, r);
-            const char *src = reinterpret_cast<const char *>(base) + (uint64_t)cl * stride;
-            if constexpr (HEADS == 1) src += p * 16;
-            else src += p / (D / 8) * head_stride * 2 + p % (D / 8) * 16;
-            cp_async16(stage + r * kPitch + piece_at(p, r), src);
+            const int x = i * 32 + lane, r = kEven ? lane / kPieces + i * (32 / kPieces) : x / kPieces;
+            const int p = kEven ? lane % kPieces : x - r * kPieces;
+            const unsigned cl = __shfl_sync(kAll, col, r), dst = stage + r * kPitch + p * 16;
+            const int more = kEven ? 0 : p * 16;       // several heads are even (whole powers of two)
+            cp_async16(dst, p0 + (uint64_t)cl * stride0 + more);
+            cp_async16(dst + kTensor, p1 + (uint64_t)cl * stride1 + more);
         }
     }
 };
@@ -701,7 +718,7 @@ struct Feed {
         seek(a, stride, groups, lane, n_cols, open);
     }
     template <typename Open, typename Copy>
-    __device__ __forceinline__ void advance(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, char *ring,
+    __device__ __forceinline__ void advance(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, unsigned ring,
                                             Open &&open, Copy &&copy) {
         if (more) {
             copy(ring + write, col);
@@ -727,7 +744,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)share * KH / H;
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
@@ -737,19 +754,16 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const Stride stride(by, (unsigned)a.n_items, groups, KH, a.kv_heads);
     Cursor now = stride.at(first);
     Feed<R> feed;
-    const T *kb = nullptr, *vb = nullptr;                // of the piece the feed is at
+    const char *kb = nullptr, *vb = nullptr;             // of the piece the feed is at
     auto open = [&](const Cursor &f) {
-        kb = static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2];
-        vb = static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2];
+        kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
+        vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
         const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
         prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + f.head(groups, share, H) * a.qs[2], a.qs[1],
                                 row0, a.n_rows, lane);
     };
-    auto copy = [&](char *st, unsigned col) {
-        R::gather(st, kb, kst, a.ks[2], col, lane);
-        R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
-    };
+    auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
 #pragma unroll
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
@@ -800,7 +814,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
-            const char *stage = ring + st_read;
+            const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
             unsigned mine[2] = {bits[0] >> (2 * c), bits[1] >> (2 * c)}, used = 0;
             bool drop = false;
@@ -823,9 +837,9 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             }
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                const int p0 = KH == 1 ? 0 : j * (D / 8);
+                const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
                 float s[2][4], t[2][4], far = none;
-                score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
+                score_products<T, D, R::kPitch>(s, q[j], at, g, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -872,7 +886,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                         s[blk][e] = exp2_of(t[blk][e]);
                         l[j][e >> 1] += s[blk][e];
                     }
-                acc[j].template add_chunk<R::kPitch>(s, stage + R::kTensor, p0, g, c, VALS && drop, used);
+                acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used);
             }
         }
         bool bad = false;
@@ -1000,7 +1014,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)share * KH / H;
     const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
@@ -1010,20 +1024,17 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const Stride stride(by, (unsigned)a.n_items, groups, KH, a.kv_heads);
     Cursor now = stride.at(first);
     Feed<R> feed;
-    const T *kb = nullptr, *vb = nullptr;
+    const char *kb = nullptr, *vb = nullptr;
     auto open = [&](const Cursor &f) {
-        kb = static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2];
-        vb = static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2];
+        kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
+        vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
         const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
         const int h = f.head(groups, share, H);
         prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + h * a.qs[2], a.qs[1], row0, a.n_rows, lane);
         prefetch_rows<T, D * H>(static_cast<const T *>(a.dout) + f.b * a.ds[0] + h * a.ds[2], a.ds[1], row0, a.n_rows, lane);
     };
-    auto copy = [&](char *st, unsigned col) {
-        R::gather(st, kb, kst, a.ks[2], col, lane);
-        R::gather(st + R::kTensor, vb, vst, a.vs[2], col, lane);
-    };
+    auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
 #pragma unroll
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
@@ -1069,7 +1080,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
-            const char *stage = ring + st_read;
+            const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
             const unsigned there[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
             unsigned mine[2] = {there[0], there[1]}, used = 0;
@@ -1092,10 +1103,10 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             }
 #pragma unroll
             for (int j = 0; j < H; ++j) {
-                const int p0 = KH == 1 ? 0 : j * (D / 8);
+                const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
                 float s[2][4], dp[2][4];
-                score_products<T, D, R::kPitch>(s, q[j], stage, p0, g, c);
-                score_products<T, D, R::kPitch>(dp, go[j], stage + R::kTensor, p0, g, c);
+                score_products<T, D, R::kPitch>(s, q[j], at, g, c);
+                score_products<T, D, R::kPitch>(dp, go[j], at + R::kTensor, g, c);
                 if (VALS && j == 0 && ch + 1 < n) next.values(x_next, vals, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
@@ -1115,7 +1126,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                             if (there[i] & pair_bit(blk, 1)) p[there[i] >> (8 * blk) & 1] = s[blk][2 * i + 1];
                         }
                 }
-                acc[j].template add_chunk<R::kPitch>(s, stage, p0, g, c, VALS && drop, used);
+                acc[j].template add_chunk<R::kPitch>(s, at, g, c, VALS && drop, used);
             }
         }
         if (!a.dq) continue;
@@ -1209,7 +1220,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, true>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    char *ring = smem + (threadIdx.x >> 5) * R::kBytes;
+    const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
@@ -1220,13 +1231,13 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const Stride stride(by, (unsigned)a.n_items, 1, KH, a.kv_heads);
     Cursor now = stride.at(first);
     Feed<R> feed = {};
-    const T *qb = nullptr, *gb = nullptr;
+    const char *qb = nullptr, *gb = nullptr;
     const float2 *stat = nullptr;
     const TileChunk *begin = nullptr;                    // of the feed's tile, and its shared head
     int fh = 0;
     auto open_head = [&](int b, int h) {
-        qb = static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2];
-        gb = static_cast<const T *>(a.dout) + b * a.ds[0] + h * a.ds[2];
+        qb = R::source(static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2], a.qs[2] * 2, lane);
+        gb = R::source(static_cast<const T *>(a.dout) + b * a.ds[0] + h * a.ds[2], a.ds[2] * 2, lane);
         stat = a.stat + ((int64_t)b * a.heads + h) * a.n_rows;
     };
     int fb = 0, fkh = 0;
@@ -1241,9 +1252,8 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         if (DK)
             prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], row0, a.n_cols, lane);
     };
-    auto copy = [&](char *st, unsigned col) {
-        R::gather(st, qb, qst, a.qs[2], col, lane);
-        R::gather(st + R::kTensor, gb, dst, a.ds[2], col, lane);
+    auto copy = [&](unsigned st, unsigned col) {
+        R::gather(st, qb, qst, gb, dst, col, lane);
 #pragma unroll
         for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
             const int jj = KH == 1 ? 0 : j + (lane >> 4);
@@ -1293,21 +1303,23 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
-            const char *stage = ring + st_read;
+            const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
 #pragma unroll
             for (int j = 0; j < KH; ++j) {
-                const int p0 = j * (D / 8);
+                const unsigned at = stage + j * (D * 2);
                 float s[2][4], dp[2][4];
-                score_products<T, D, R::kPitch>(s, k[j], stage, p0, g, c);
-                if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], stage + R::kTensor, p0, g, c);
+                score_products<T, D, R::kPitch>(s, k[j], at, g, c);
+                if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], at + R::kTensor, g, c);
                 if (VALS && j == 0 && x + 1 < steps) next.values(x_next, vals, c);
-                const float4 *sp = reinterpret_cast<const float4 *>(stage + 2 * R::kTensor + j * 128);
+                const unsigned sp = stage + 2 * R::kTensor + j * 128 + c * 16;
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk) {
-                    const float4 st = sp[4 * blk + c];              // (lse, D) of the columns 2c and 2c + 1
+                    const uint4 su = lds16(sp + blk * 64);          // (lse, D) of the columns 2c and 2c + 1
+                    const float4 st = make_float4(__uint_as_float(su.x), __uint_as_float(su.y), __uint_as_float(su.z),
+                                                  __uint_as_float(su.w));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float lse = e & 1 ? st.z : st.x, delta = e & 1 ? st.w : st.y;
@@ -1323,8 +1335,8 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 const bool drop = VALS && __any_sync(kAll, out);
                 used = (live[0] | live[1]) & 0x303u;
                 used = (used | used >> 6) & 15u;
-                if constexpr (DV) dv[j].template add_chunk<R::kPitch>(s, stage + R::kTensor, p0, g, c, drop, used);
-                if constexpr (DK) dk[j].template add_chunk<R::kPitch>(dp, stage, p0, g, c, drop, used);
+                if constexpr (DV) dv[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, drop, used);
+                if constexpr (DK) dk[j].template add_chunk<R::kPitch>(dp, at, g, c, drop, used);
             }
         }
         bool bad = false;
