@@ -236,15 +236,18 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Scores less a reference (maximum or lse) in units of log 2.  Without values the
-// factor log2 e is part of `scale` and the references have the same unit: one
-// multiply-add.  Values come in natural units, and the difference is taken before
-// the factor, so that the lowest finite value does not overflow.
+// Scores less a reference (a number near the maximum, or lse), and their
+// exponential.  Without values both are in units of log 2: the factor log2 e is
+// part of `scale`, so that the difference is one multiply-add.  Values come in
+// natural units, and the factor is applied to the difference, so that the lowest
+// finite value does not overflow.
 template <bool VALS>
 __device__ __forceinline__ float relative(float dot, float scale, float val, float ref) {
-    if constexpr (VALS) return (fmaf(dot, scale, val) - ref) * kLog2e;
+    if constexpr (VALS) return fmaf(dot, scale, val) - ref;
     else return fmaf(dot, scale, -ref);
 }
+template <bool VALS>
+__device__ __forceinline__ float weight(float t) { return exp2_of(VALS ? t * kLog2e : t); }
 template <bool VALS>
 __device__ __forceinline__ float score_scale(double scale) {
     return VALS ? (float)scale : (float)(scale * 1.4426950408889634);
@@ -259,12 +262,13 @@ __device__ __forceinline__ unsigned pair_bit(int blk, int e) { return 1u << (8 *
 template <int D>
 struct Own {
     uint32_t a[D / 16][4];
+    // `stride`: bytes from row to row, below 2^32.
     template <typename T>
-    __device__ __forceinline__ void load(const T *base, int64_t stride, int64_t row0, int n_rows, int g, int c) {
+    __device__ __forceinline__ void load(const T *base, unsigned stride, int row0, int n_rows, int g, int c) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bool on = row0 + g + 8 * i < n_rows;
-            const char *p = reinterpret_cast<const char *>(base + (row0 + g + 8 * i) * stride);
+            const char *p = reinterpret_cast<const char *>(base) + (uint64_t)(unsigned)(row0 + g + 8 * i) * stride;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
                 const int at = j < D / 64 * 2 ? c * 2 + (j >> 1) * 8 + (j & 1) : c + D / 64 * 8;
@@ -425,9 +429,7 @@ struct Sums {
 // A piece of work: chunks [ch0, ch1) of a tile, heads h (and following) of one
 // system, whose key heads start at kh.
 struct TileWork {
-    int64_t row0;
-    int b, h, kh, slot;
-    const TileChunk *ch0, *ch1;
+    int row0, b, h, kh, slot, ch0, ch1;
 };
 
 // The pieces of work a warp takes, every `stride`-th of the list ordered by
@@ -486,20 +488,20 @@ __device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c
     w.b = c.b;
     w.kh = c.kh;
     w.h = c.head(groups, share, n_h);
-    w.row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+    w.row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
     w.slot = a.item_unit ? __ldg(a.item_slot + it) : -1;
     const int2 r = item_range(a, it);
-    w.ch0 = a.chunks + r.x;
-    w.ch1 = a.chunks + r.y;
+    w.ch0 = r.x;
+    w.ch1 = r.y;
     return w;
 }
 
 // Brings the lines of rows that will be loaded soon into the L2 cache: lane r < 16
 // names row r's D elements.
 template <typename T, int D>
-__device__ __forceinline__ void prefetch_rows(const T *base, int64_t stride, int64_t row0, int n_rows, int lane) {
+__device__ __forceinline__ void prefetch_rows(const T *base, int64_t stride, int row0, int n_rows, int lane) {
     if (lane < kTileRows && row0 + lane < n_rows) {
-        const T *p = base + (row0 + lane) * stride;
+        const T *p = base + (int64_t)(row0 + lane) * stride;
 #pragma unroll
         for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
     }
@@ -511,7 +513,8 @@ template <bool ENTRIES>
 struct Chunk {
     unsigned bits[2];
     int at[2];
-    __device__ __forceinline__ void load(const TileChunk *p, int g) {
+    __device__ __forceinline__ void load(const TileChunk *chunks, int ch, int g) {
+        const TileChunk *p = chunks + ch;
         bits[0] = __ldg(p->bits + g);
         bits[1] = __ldg(p->bits + 8 + g);
         if constexpr (ENTRIES) {
@@ -582,21 +585,21 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ unsigned chunk_column(const TileChunk *ch, int lane, int n_cols) {
+__device__ __forceinline__ unsigned chunk_column(const TileChunk *chunks, int ch, int lane, int n_cols) {
 #if SLA_DEBUG_BOUNDS
-    return (unsigned)SLA_IDX(__ldg(ch->col + (lane & 15)), n_cols, kBndColumn);
+    return (unsigned)SLA_IDX(__ldg(chunks[ch].col + (lane & 15)), n_cols, kBndColumn);
 #else
     (void)n_cols;
-    return (unsigned)__ldg(ch->col + (lane & 15));
+    return (unsigned)__ldg(chunks[ch].col + (lane & 15));
 #endif
 }
 
 // Entry range of row r of the tile in the item (every lane r < 16 its own row).
-__device__ __forceinline__ void row_range(const TileWork &w, int lane, int &t0, int &t1) {
+__device__ __forceinline__ void row_range(const TileChunk *chunks, const TileWork &w, int lane, int &t0, int &t1) {
     t0 = t1 = 0;
     if (lane < kTileRows && w.ch0 < w.ch1) {
-        t0 = t1 = __ldg(w.ch0->start + lane);
-        for (const TileChunk *ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(ch->bits + lane));
+        t0 = t1 = __ldg(chunks[w.ch0].start + lane);
+        for (int ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(chunks[ch].bits + lane));
     }
 }
 
@@ -627,7 +630,7 @@ template <typename T>
 __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(w, lane, s0, s1);
+    row_range(a.chunks, w, lane, s0, s1);
     const T *qb = static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2];
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
@@ -681,52 +684,54 @@ template <typename R>
 struct Feed {
     Cursor cur;
     unsigned left, col;                    // pieces of work not yet begun; columns of the chunk at `at`
-    const TileChunk *at, *end;
+    int at, end;
     int2 next;                             // chunks of the piece after this one
     int write;
     bool more;
 
-    // The next chunk, if there is one, and its columns (a load that is due only at
-    // the next copy).
+    // The next chunk, if there is one.
     template <typename Open>
-    __device__ __forceinline__ void seek(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, Open &&open) {
+    __device__ __forceinline__ void seek(const AttnArgs &a, const Stride &stride, unsigned groups, Open &&open) {
         while (at == end) {
             if (left == 0) {
                 more = false;
+                at = end > 0 ? end - 1 : 0;      // some chunk, for the load that follows
                 return;
             }
             --left;
-            at = a.chunks + next.x;
-            end = a.chunks + next.y;
+            at = next.x;
+            end = next.y;
             open(cur);
             if (left > 0) {
                 stride.move(cur);
                 next = item_range(a, cur.item(groups));
             }
         }
-        col = chunk_column(at, lane, n_cols);
     }
     template <typename Open>
     __device__ __forceinline__ void start(const AttnArgs &a, const Cursor &c, unsigned count, const Stride &stride, unsigned groups,
                                           int lane, int n_cols, Open &&open) {
         cur = c;
         left = count;
-        at = end = nullptr;
+        at = end = 0;
         write = 0;
         more = true;
         if (count > 0) next = item_range(a, cur.item(groups));
-        seek(a, stride, groups, lane, n_cols, open);
+        seek(a, stride, groups, open);
+        col = chunk_column(a.chunks, at, lane, n_cols);
     }
+    // The columns are loaded in every call, needed or not: a load under a condition
+    // would be waited for where its paths join, not where it is used.
     template <typename Open, typename Copy>
     __device__ __forceinline__ void advance(const AttnArgs &a, const Stride &stride, unsigned groups, int lane, int n_cols, unsigned ring,
                                             Open &&open, Copy &&copy) {
         if (more) {
             copy(ring + write, col);
             write = write == (R::kStages - 1) * R::kStage ? 0 : write + R::kStage;
-            ++at;
-            seek(a, stride, groups, lane, n_cols, open);
+            if (++at == end) seek(a, stride, groups, open);
         }
         cp_commit();
+        col = chunk_column(a.chunks, at, lane, n_cols);
     }
 };
 
@@ -746,7 +751,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)share * KH / H;
-    const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
+    const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
     const unsigned count = my_share(total, first, by);
@@ -759,7 +764,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
-        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
         prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + f.head(groups, share, H) * a.qs[2], a.qs[1],
                                 row0, a.n_rows, lane);
     };
@@ -770,27 +775,26 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
         const TileWork w = tile_work(a, now, groups, share, H);
-        const int n = (int)(w.ch1 - w.ch0);
+        const int n = w.ch1 - w.ch0;
         Own<D> q[H];
 #pragma unroll
         for (int j = 0; j < H; ++j)
-            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h + j) * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h + j) * a.qs[2], qst, w.row0, a.n_rows, g, c);
         Sums<T, D> acc[H];
         float m[H][2], l[H][2];
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             acc[j].zero();
-            m[j][0] = m[j][1] = none;
-            l[j][0] = l[j][1] = 0.0f;
+            m[j][0] = m[j][1] = l[j][0] = l[j][1] = 0.0f;
         }
         Chunk<VALS> next, cur;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, g);
         if constexpr (VALS) {
             cur = next;
             if (n > 0) cur.values(x_next, vals, c);
-            if (n > 1) next.load(w.ch0 + 1, g);
+            if (n > 0) next.load(a.chunks, w.ch0 + min(1, n - 1), g);
         }
         for (int ch = 0; ch < n; ++ch) {
             // bookkeeping of this chunk, and loads of the next one's
@@ -804,12 +808,12 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
                 cur = next;
-                if (ch + 1 < n) cur.values(x_next, vals, c);
-                if (ch + 2 < n) next.load(w.ch0 + ch + 2, g);
+                cur.values(x_next, vals, c);
+                next.load(a.chunks, w.ch0 + min(ch + 2, n - 1), g);
             } else {
                 bits[0] = next.bits[0];
                 bits[1] = next.bits[1];
-                if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+                next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), g);
             }
             cp_wait<R::kStages - 2>();
             __syncwarp();
@@ -838,7 +842,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
-                float s[2][4], t[2][4], far = none;
+                float s[2][4], t[2][4], far[2] = {none, none};
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
@@ -846,31 +850,30 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                     for (int e = 0; e < 4; ++e) {
                         t[blk][e] = relative<VALS>(s[blk][e], scale, x[blk][e], m[j][e >> 1]);
                         t[blk][e] = mine[e >> 1] & pair_bit(blk, e) ? t[blk][e] : none;
-                        far = fmaxf(far, t[blk][e]);
+                        far[e >> 1] = fmaxf(far[e >> 1], t[blk][e]);
                     }
-                // The reference moves only when a score is 2^8 above it (or the first of
-                // its row): any reference near the maximum does, and most chunks skip this.
-                if (__any_sync(kAll, far > 8.0f)) {
-                    float top[2] = {m[j][0], m[j][1]};
-#pragma unroll
-                    for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float u = relative<false>(s[blk][e], scale, 0.0f, VALS ? -x[blk][e] : 0.0f);
-                            top[e >> 1] = fmaxf(top[e >> 1], mine[e >> 1] & pair_bit(blk, e) ? u : none);
-                        }
+                // Any reference that keeps a row's first weights between 2^-20 and 2^8 will
+                // do; 0 mostly is one.  It moves when a score is beyond: up at any time,
+                // down only while the row has no weight.
+                constexpr float kUnit = VALS ? kLn2 : 1.0f;
+                const bool up = far[0] > 8.0f * kUnit || far[1] > 8.0f * kUnit;
+                const bool down = (far[0] < -20.0f * kUnit && l[j][0] == 0.0f && far[0] != none) ||
+                                  (far[1] < -20.0f * kUnit && l[j][1] == 0.0f && far[1] != none);
+                if (__any_sync(kAll, up || down)) {
+                    float sum[2] = {l[j][0], l[j][1]}, f[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 1));
-                        top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], 2));
+#pragma unroll
+                        for (int o = 1; o < 4; o += o) {
+                            far[i] = fmaxf(far[i], __shfl_xor_sync(kAll, far[i], o));
+                            sum[i] += __shfl_xor_sync(kAll, sum[i], o);
+                        }
+                        const float by = far[i] == none ? 0.0f : (sum[i] == 0.0f ? far[i] : fmaxf(far[i], 0.0f));
+                        f[i] = by == 0.0f || sum[i] == 0.0f ? 1.0f : weight<VALS>(-by);
+                        l[j][i] *= f[i];
+                        m[j][i] += by;
                     }
-                    const float f0 = m[j][0] == none ? 0.0f : exp2_of((m[j][0] - top[0]) * (VALS ? kLog2e : 1.0f));
-                    const float f1 = m[j][1] == none ? 0.0f : exp2_of((m[j][1] - top[1]) * (VALS ? kLog2e : 1.0f));
-                    acc[j].scale(f0, f1);
-                    l[j][0] *= f0;
-                    l[j][1] *= f1;
-                    m[j][0] = top[0];
-                    m[j][1] = top[1];
+                    acc[j].scale(f[0], f[1]);
 #pragma unroll
                     for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -883,15 +886,17 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[blk][e] = exp2_of(t[blk][e]);
+                        s[blk][e] = weight<VALS>(t[blk][e]);
                         l[j][e >> 1] += s[blk][e];
                     }
                 acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used);
             }
         }
+        // A NaN among the sums, or a sum of weights that is none (which the outputs
+        // would not show).
         bool bad = false;
 #pragma unroll
-        for (int j = 0; j < H; ++j) bad = acc[j].bad() || bad;
+        for (int j = 0; j < H; ++j) bad = acc[j].bad() || __any_sync(kAll, l[j][0] != l[j][0] || l[j][1] != l[j][1]) || bad;
         if (bad) {
             for (int j = 0; j < H; ++j) {
                 TileWork one = w;
@@ -901,31 +906,34 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             }
             continue;
         }
+        const int64_t at0 = ((int64_t)w.b * a.n_rows + w.row0) * a.heads + w.h;     // row row0, head h
+        const unsigned step = (unsigned)a.heads;
 #pragma unroll
         for (int j = 0; j < H; ++j) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 l[j][i] += __shfl_xor_sync(kAll, l[j][i], 1);
                 l[j][i] += __shfl_xor_sync(kAll, l[j][i], 2);
-                if constexpr (!VALS) m[j][i] *= kLn2;
             }
-            if (w.slot < 0)
-                acc[j].scale(l[j][0] > 0.0f ? 1.0f / l[j][0] : 0.0f, l[j][1] > 0.0f ? 1.0f / l[j][1] : 0.0f);
+            if (w.slot < 0) acc[j].scale(l[j][0] > 0.0f ? __fdividef(1.0f, l[j][0]) : 0.0f,
+                                         l[j][1] > 0.0f ? __fdividef(1.0f, l[j][1]) : 0.0f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int r = g + 8 * i;
                 if (w.row0 + r >= a.n_rows) continue;
+                // no weight: lse is -inf
+                const float top = l[j][i] == 0.0f ? none : (VALS ? m[j][i] : m[j][i] * kLn2);
                 if (w.slot < 0) {
-                    const int64_t o = ((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h + j;
+                    const int64_t o = at0 + (uint64_t)(unsigned)r * step + j;
                     acc[j].store(static_cast<T *>(a.out) + o * D, i, c);
                     if (a.wide) acc[j].store(static_cast<float *>(a.wide) + o * D, i, c);
-                    if (c == 0) static_cast<float *>(a.lse)[o] = l[j][i] == 0.0f ? none : m[j][i] + logf(l[j][i]);
+                    if (c == 0) static_cast<float *>(a.lse)[o] = top + __log2f(l[j][i] == 0.0f ? 1.0f : l[j][i]) * kLn2;
                 } else {
                     float *p = static_cast<float *>(a.part) +
                                part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h + j) * (D + 2);
                     acc[j].store_odd(p, i, c);          // D + 2 numbers a partial
                     if (c == 0) {
-                        p[D] = m[j][i];
+                        p[D] = top;
                         p[D + 1] = l[j][i];
                     }
                 }
@@ -940,7 +948,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(w, lane, s0, s1);
+    row_range(a.chunks, w, lane, s0, s1);
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
     const float scale = (float)a.scale, none = neg_inf<float>();
@@ -1016,7 +1024,8 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned groups = (unsigned)share * KH / H;
-    const unsigned kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
+    const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
+                   dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
     const unsigned count = my_share(total, first, by);
@@ -1029,7 +1038,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
-        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
         const int h = f.head(groups, share, H);
         prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + h * a.qs[2], a.qs[1], row0, a.n_rows, lane);
         prefetch_rows<T, D * H>(static_cast<const T *>(a.dout) + f.b * a.ds[0] + h * a.ds[2], a.ds[1], row0, a.n_rows, lane);
@@ -1041,7 +1050,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
         const TileWork w = tile_work(a, now, groups, share, H);
-        const int n = (int)(w.ch1 - w.ch0);
+        const int n = w.ch1 - w.ch0;
         Own<D> q[H], go[H];
         float lse[H][2], delta[H][2];
         bool dead[H][2];
@@ -1049,8 +1058,8 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
             const int h = w.h + j;
-            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], a.qs[1], w.row0, a.n_rows, g, c);
-            go[j].load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], a.ds[1], w.row0, a.n_rows, g, c);
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, w.row0, a.n_rows, g, c);
+            go[j].load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, w.row0, a.n_rows, g, c);
             acc[j].zero();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -1066,7 +1075,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         Chunk<VALS> next, cur;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, g);
         if constexpr (VALS)
             if (n > 0) next.values(x_next, vals, c);
         for (int ch = 0; ch < n; ++ch) {
@@ -1076,7 +1085,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
-            if (ch + 1 < n) next.load(w.ch0 + ch + 1, g);
+            next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), g);
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
@@ -1107,13 +1116,13 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
                 score_products<T, D, R::kPitch>(dp, go[j], at + R::kTensor, g, c);
-                if (VALS && j == 0 && ch + 1 < n) next.values(x_next, vals, c);
+                if (VALS && j == 0) next.values(x_next, vals, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e >> 1;
-                        s[blk][e] = exp2_of(relative<VALS>(s[blk][e], scale, x[blk][e], lse[j][i])) * (dp[blk][e] - delta[j][i]);
+                        s[blk][e] = weight<VALS>(relative<VALS>(s[blk][e], scale, x[blk][e], lse[j][i])) * (dp[blk][e] - delta[j][i]);
                         s[blk][e] = mine[i] & pair_bit(blk, e) && !dead[j][i] ? s[blk][e] : 0.0f;
                     }
                 if (VALS && ds_out) {
@@ -1165,7 +1174,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w, bool want_dk, bool want_dv) {
     const int lane = threadIdx.x & 31, share = a.heads / a.kv_heads;
     int s0, s1;
-    row_range(w, lane, s0, s1);
+    row_range(a.chunks, w, lane, s0, s1);
     const float scale = (float)a.scale, none = neg_inf<float>();
     for (int r = 0; r < kTileRows && w.row0 + r < a.n_cols; ++r) {
         const int t0 = __shfl_sync(kAll, s0, r), t1 = __shfl_sync(kAll, s1, r);
@@ -1221,7 +1230,8 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned qst = (unsigned)a.qs[1] * 2, dst = (unsigned)a.ds[1] * 2;
+    const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
+                   dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
     const unsigned count = my_share(total, first, by);
@@ -1233,8 +1243,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     Feed<R> feed = {};
     const char *qb = nullptr, *gb = nullptr;
     const float2 *stat = nullptr;
-    const TileChunk *begin = nullptr;                    // of the feed's tile, and its shared head
-    int fh = 0;
+    int begin = 0, fh = 0;                               // first chunk of the feed's tile, its shared head
     auto open_head = [&](int b, int h) {
         qb = R::source(static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2], a.qs[2] * 2, lane);
         gb = R::source(static_cast<const T *>(a.dout) + b * a.ds[0] + h * a.ds[2], a.ds[2] * 2, lane);
@@ -1247,7 +1256,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         fb = f.b;
         fkh = f.kh;
         open_head(f.b, f.kh * share);
-        const int64_t row0 = (int64_t)(a.item_unit ? __ldg(a.item_unit + f.x) : (int)f.x) * kTileRows;
+        const int row0 = (a.item_unit ? __ldg(a.item_unit + f.x) : (int)f.x) * kTileRows;
         prefetch_rows<T, D * KH>(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[1], row0, a.n_cols, lane);
         if (DK)
             prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], row0, a.n_cols, lane);
@@ -1276,19 +1285,19 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
-            k[j].load(static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.kh + j) * a.ks[2], a.ks[1], w.row0, a.n_cols, g, c);
+            k[j].load(static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.kh + j) * a.ks[2], kst, w.row0, a.n_cols, g, c);
             if constexpr (DK) {
-                v[j].load(static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.kh + j) * a.vs[2], a.vs[1], w.row0, a.n_cols, g, c);
+                v[j].load(static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.kh + j) * a.vs[2], vst, w.row0, a.n_cols, g, c);
                 dk[j].zero();
             }
             if constexpr (DV) dv[j].zero();
         }
-        const int n = (int)(w.ch1 - w.ch0), steps = n * (KH == 1 ? share : 1);
+        const int n = w.ch1 - w.ch0, steps = n * (KH == 1 ? share : 1);
         int ci = 0;                                      // chunk of the step
         Chunk<VALS> next;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, g);
         if constexpr (VALS)
             if (n > 0) next.values(x_next, vals, c);
         for (int x = 0; x < steps; ++x) {
@@ -1299,7 +1308,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) val[blk][e] = x_next[blk][e];
             ci = ci + 1 == n ? 0 : ci + 1;
-            if (x + 1 < steps) next.load(w.ch0 + ci, g);
+            next.load(a.chunks, w.ch0 + ci, g);
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
@@ -1311,7 +1320,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, k[j], at, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], at + R::kTensor, g, c);
-                if (VALS && j == 0 && x + 1 < steps) next.values(x_next, vals, c);
+                if (VALS && j == 0) next.values(x_next, vals, c);
                 const unsigned sp = stage + 2 * R::kTensor + j * 128 + c * 16;
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
@@ -1328,7 +1337,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                             live[e >> 1] &= ~pair_bit(blk, e);
                         }
                         const bool on = live[e >> 1] & pair_bit(blk, e);
-                        s[blk][e] = on ? exp2_of(relative<VALS>(s[blk][e], scale, val[blk][e], lse)) : 0.0f;
+                        s[blk][e] = on ? weight<VALS>(relative<VALS>(s[blk][e], scale, val[blk][e], lse)) : 0.0f;
                         if constexpr (DK) dp[blk][e] = on ? s[blk][e] * (dp[blk][e] - delta) : 0.0f;
                     }
                 }
@@ -1511,7 +1520,7 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const in
         set_error("attention plan: out of device memory");
         return SLA_ERR_OOM;
     }
-    SLA_CHECK_CUDA(cudaMemsetAsync(t->chunks, 0, (size_t)total * sizeof(TileChunk), s));
+    SLA_CHECK_CUDA(cudaMemsetAsync(t->chunks, 0, (size_t)(total > 0 ? total : 1) * sizeof(TileChunk), s));
     tile_columns_kernel<true><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
                                                    parts.item_seg, nullptr, count, t->chunk0, t->chunks);
     SLA_CHECK_LAUNCH();
