@@ -407,7 +407,7 @@ class _Attention(torch.autograd.Function):
         q, k, v, values, out, lse = ctx.saved_tensors
         go = _head_layout(go, call.whole)
         vals = None if values is None else A._values(values)
-        new = lambda need, t: torch.empty(t.shape, dtype=t.dtype, device=A.device) if need else None  # noqa: E731
+        new = lambda need, t: torch.empty_like(t, memory_format=torch.contiguous_format) if need else None  # noqa: E731
         dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[2:6], (q, k, v, values)))
         with _on_device(A.device):
             ws = _workspace(call.workspace[1], A.device)

@@ -89,7 +89,7 @@ __global__ void tile_len_kernel(int n_units, const int32_t *__restrict__ chunk0,
 sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, const int32_t *chunk0,
                        cudaStream_t s) {
     const int U = p->n_units;
-    DeviceScratch tmp;
+    DeviceScratch tmp(s);
     unsigned *nseg = tmp.get<unsigned>((size_t)U + 1), *slots = tmp.get<unsigned>((size_t)U + 1),
              *multi = tmp.get<unsigned>((size_t)U + 1);
     void *ws = tmp.get<char>(scan_ws_bytes((int64_t)U + 1));
@@ -146,8 +146,9 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 // heads as the one before, so it splits 8 times less.
 int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 8 >> (3 * level)); }
 
-// All levels of one direction's row plans (tiled == false) or its tiles and
-// their plans.  The lengths are the same for every level.
+sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s);
+
+// One level of one direction's row plans, or (tiled) its tiles and their plan.
 sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
     AttnPlan *p = &(tiled ? h->attn->tile : h->attn->row)[transposed][level];
     AttnTiles *tiles = &h->attn->tiles[transposed];
@@ -156,11 +157,23 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
     p->rows = tiled ? kTileRows : 1;
     p->n_units = (n + p->rows - 1) / p->rows;
     const int U = p->n_units;
-    if (U == 0) {
+    constexpr int kLeast = 64;           // entries of a row, columns of a tile
+    // no row that any level would split (the lengths of A's rows are known)
+    if (U == 0 || (!tiled && !transposed && h->row_max <= kLeast)) {
+        p->n_items = U;
         p->built = true;
         return SLA_OK;
     }
-    DeviceScratch tmp;
+    if (level > 0) {                     // a level splits what the one before it splits, or less
+        const sla_status st = ensure_plan(h, tiled, transposed, 0, s);
+        if (st != SLA_OK) return st;
+        const AttnPlan &finest = (tiled ? h->attn->tile : h->attn->row)[transposed][0];
+        if (finest.n_multi == 0) {
+            *p = finest;                 // no arrays
+            return SLA_OK;
+        }
+    }
+    DeviceScratch tmp(s);
     unsigned *len = tmp.get<unsigned>((size_t)U + 1);
     if (!len) {
         set_error("attention plan: out of device memory");
@@ -185,7 +198,7 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
         tile_len_kernel<<<grid, 256, 0, s>>>(U, tiles->chunk0, len);
         SLA_CHECK_LAUNCH();
     }
-    st = build_items(p, len, 0, fill_of(h, level), tiled ? 64 / 16 : 64, tiled ? tiles->chunk0 : nullptr, s);
+    st = build_items(p, len, 0, fill_of(h, level), tiled ? kLeast / 16 : kLeast, tiled ? tiles->chunk0 : nullptr, s);
     if (st == SLA_OK) p->built = true;
     return st;
 }

@@ -189,16 +189,19 @@ template <typename T> sla_status attn_tile_bwd_cols(AttnArgs a, cudaStream_t s);
 
 inline unsigned blocks_of(int64_t n, int t = 256) { return (unsigned)((n + t - 1) / t); }
 
-// Device memory freed when the scope ends.
+// Device memory for the work queued on a stream, given back to the stream's pool
+// when the scope ends.
 struct DeviceScratch {
+    cudaStream_t stream;
     std::vector<void *> held;
+    explicit DeviceScratch(cudaStream_t s) : stream(s) {}
     ~DeviceScratch() {
-        for (void *p : held) cudaFree(p);
+        for (void *p : held) cudaFreeAsync(p, stream);
     }
     template <typename U>
     U *get(size_t count) {
         void *p = nullptr;
-        if (cudaMalloc(&p, (count > 0 ? count : 1) * sizeof(U)) != cudaSuccess) {
+        if (cudaMallocAsync(&p, (count > 0 ? count : 1) * sizeof(U), stream) != cudaSuccess) {
             cudaGetLastError();
             return nullptr;
         }

@@ -22,9 +22,12 @@
 // share their key head, which is then fetched once.
 //
 // Scores: 16-bit products, exact, summed in 32 bits.  Weights are not rounded to
-// 16 bits: they multiply as tf32 (the 16-bit operand is exact in it), rounded to
-// 11 bits for bfloat16 outputs (8 bits) and as a sum of two 11-bit parts for
-// float16 outputs (11 bits), which keeps the outputs as good as 32-bit products.
+// 16 bits: they multiply as tf32 (the 16-bit operand is exact in it), as a sum of
+// two 11-bit parts in the forward pass and for float16 gradients (11 bits), rounded
+// to 11 bits for bfloat16 gradients (8 bits), which keeps the outputs as good as
+// 32-bit products.  The forward pass needs both parts whatever its type: the
+// backward subtracts D = dout . o from numbers of its size, and the values' gradient
+// shows the difference in 32 bits.
 //
 // Masked pairs have weight 0, but 0 times an infinity or a NaN is a NaN.  A column
 // that every row leaves out (values of -inf: padding, which may hold anything) is
@@ -333,17 +336,16 @@ struct Sums {
             o[nb][3] *= hi;
         }
     }
-    __device__ __forceinline__ void add(const float (&w)[4], const uint32_t (&x0)[D / 16], const uint32_t (&x1)[D / 16]) {
+    // The weights in two parts, or one.
+    __device__ __forceinline__ void add(const float (&w)[4], const uint32_t (&x0)[D / 16], const uint32_t (&x1)[D / 16],
+                                        bool two) {
         const float v[4] = {w[0], w[2], w[1], w[3]};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-                asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(v[i]));
-            } else {
-                hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
-                lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i]));
-            }
+            if (two) hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
+            else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(v[i]));
+            lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i]));
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -352,7 +354,7 @@ struct Sums {
             widen<T>(x1[i], b0, b1);
             mma_tf32(o[2 * i], hi, a0, b0);
             mma_tf32(o[2 * i + 1], hi, a1, b1);
-            if constexpr (!std::is_same_v<T, __nv_bfloat16>) {
+            if (two) {
                 mma_tf32(o[2 * i], lo, a0, b0);
                 mma_tf32(o[2 * i + 1], lo, a1, b1);
             }
@@ -374,13 +376,13 @@ struct Sums {
     // drop_unused.
     template <int PITCH>
     __device__ __forceinline__ void add_chunk(const float (&w)[2][4], unsigned stage, int g, int c, bool drop,
-                                              unsigned used) {
+                                              unsigned used, bool two = std::is_same_v<T, __half>) {
         uint32_t x[4][D / 16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) read_sum<D>(x[j], stage + 2 * c * PITCH + (8 * (j >> 1) + (j & 1)) * PITCH, g);
         if (drop) drop_unused(x, used);
-        add(w[0], x[0], x[1]);
-        add(w[1], x[2], x[3]);
+        add(w[0], x[0], x[1], two);
+        add(w[1], x[2], x[3], two);
     }
     // Row g (i = 0) or g + 8 (i = 1) to its D elements at p.  Of every group of
     // blocks this thread holds consecutive elements, first those of column 2c.
@@ -889,7 +891,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                         s[blk][e] = weight<VALS>(t[blk][e]);
                         l[j][e >> 1] += s[blk][e];
                     }
-                acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used);
+                acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used, true);
             }
         }
         // A NaN among the sums, or a sum of weights that is none (which the outputs
@@ -1496,7 +1498,7 @@ sla_status launch_tile_of(int what, const AttnArgs &a, cudaStream_t s) {
 sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s) {
     const int n = parts.n_items, U = parts.n_units;
-    DeviceScratch tmp;
+    DeviceScratch tmp(s);
     unsigned *count = tmp.get<unsigned>((size_t)n + 1), *chunks = tmp.get<unsigned>((size_t)U + 1);
     void *ws = tmp.get<char>(scan_ws_bytes((int64_t)n + 1));
     if (!count || !chunks || !ws || !alloc_array(&t->chunk0, (size_t)U + 1)) {
