@@ -162,12 +162,18 @@ class CSR:
 
 
     # --------------------------------------------------------- attention
-    def prepare_attention(self, backward: bool = False) -> None:
+    def prepare_attention(self, backward: bool = False, heads_per_key: int = 1) -> None:
         """Build the work plan of ``attention`` (and, with ``backward``, A^T's
         pattern and plan) now instead of at the first call: needed before the
-        calls are captured into a CUDA graph.  Synchronises the host."""
-        with torch.cuda.device(self.device):
+        calls are captured into a CUDA graph.  heads_per_key: H // K of the calls.
+        Synchronises the host."""
+        if heads_per_key < 1:
+            raise ValueError("heads_per_key must be positive")
+        with _on_device(self.device):
             L.sla_attention_prepare(self.handle, None, backward)
+            if heads_per_key > 1:
+                opts = L.make_attn_opts(torch.bfloat16, heads_per_key, 1, 16, 1.0, (0, 0, 0), (0, 0, 0), (0, 0, 0))
+                L.sla_attention_prepare(self.handle, opts, backward)
 
     def attention(self, q, k, v, values=None, *, scale: float | None = None) -> torch.Tensor:
         """Attention over the pattern: row i of A is a query that attends to the

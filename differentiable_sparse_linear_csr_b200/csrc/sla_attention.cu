@@ -146,15 +146,22 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 // heads as the one before, so it splits 8 times less.
 int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 8 >> (3 * level)); }
 
-sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s);
+constexpr int kRowKind = -1;             // plans of rows; tiles of 16 >> kind rows
 
-// One level of one direction's row plans, or (tiled) its tiles and their plan.
-sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
-    AttnPlan *p = &(tiled ? h->attn->tile : h->attn->row)[transposed][level];
-    AttnTiles *tiles = &h->attn->tiles[transposed];
+AttnPlan &plan_at(Csr *h, int kind, bool transposed, int level) {
+    return kind == kRowKind ? h->attn->row[transposed][level] : h->attn->tile[transposed][kind][level];
+}
+
+sla_status ensure_plan(Csr *h, int kind, bool transposed, int level, cudaStream_t s);
+
+// One level of one direction's row plans, or of a kind of tiles (and the tiles).
+sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_t s) {
+    const bool tiled = kind != kRowKind;
+    AttnPlan *p = &plan_at(h, kind, transposed, level);
+    AttnTiles *tiles = tiled ? &h->attn->tiles[transposed][kind] : nullptr;
     const int n = transposed ? h->n_cols : h->n_rows;
     const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr, *colind = transposed ? h->colindT : h->colind;
-    p->rows = tiled ? kTileRows : 1;
+    p->rows = tiled ? kTileRows >> kind : 1;
     p->n_units = (n + p->rows - 1) / p->rows;
     const int U = p->n_units;
     constexpr int kLeast = 64;           // entries of a row, columns of a tile
@@ -165,9 +172,9 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
         return SLA_OK;
     }
     if (level > 0) {                     // a level splits what the one before it splits, or less
-        const sla_status st = ensure_plan(h, tiled, transposed, 0, s);
+        const sla_status st = ensure_plan(h, kind, transposed, 0, s);
         if (st != SLA_OK) return st;
-        const AttnPlan &finest = (tiled ? h->attn->tile : h->attn->row)[transposed][0];
+        const AttnPlan &finest = plan_at(h, kind, transposed, 0);
         if (finest.n_multi == 0) {
             *p = finest;                 // no arrays
             return SLA_OK;
@@ -191,7 +198,7 @@ sla_status build_plans(Csr *h, bool tiled, bool transposed, int level, cudaStrea
             AttnPlan parts;
             parts.n_units = U;
             st = build_items(&parts, len, 256, 0, 0, nullptr, s);
-            if (st == SLA_OK) st = build_tiles(tiles, parts, n, rowptr, colind, s);
+            if (st == SLA_OK) st = build_tiles(tiles, parts, p->rows, n, rowptr, colind, s);
             free_plan(&parts);
             if (st != SLA_OK) return st;
         }
@@ -209,19 +216,19 @@ void free_tiles(AttnTiles *t) {
     *t = AttnTiles();
 }
 
-sla_status ensure_plan(Csr *h, bool tiled, bool transposed, int level, cudaStream_t s) {
-    AttnPlan *p = &(tiled ? h->attn->tile : h->attn->row)[transposed][level];
+sla_status ensure_plan(Csr *h, int kind, bool transposed, int level, cudaStream_t s) {
+    AttnPlan *p = &plan_at(h, kind, transposed, level);
     if (p->built) return SLA_OK;
     sla_status st = SLA_ERR_OOM;
     try {
-        st = build_plans(h, tiled, transposed, level, s);
+        st = build_plans(h, kind, transposed, level, s);
     } catch (const std::bad_alloc &) {
         set_error("sla_attention_prepare: out of host memory");
     }
     if (st != SLA_OK) {
         cudaStreamSynchronize(s);
         free_plan(p);
-        if (!h->attn->tiles[transposed].built) free_tiles(&h->attn->tiles[transposed]);
+        if (kind != kRowKind && !h->attn->tiles[transposed][kind].built) free_tiles(&h->attn->tiles[transposed][kind]);
     }
     return st;
 }
@@ -238,7 +245,9 @@ void use_plan(AttnArgs &a, const AttnPlan &p) {
     a.item_chunks = p.item_chunks;
 }
 
-static void use_tiles(AttnArgs &a, const AttnTiles &t) {
+static void use_tiles(AttnArgs &a, const Csr *h, bool transposed, int kind) {
+    const AttnTiles &t = h->attn->tiles[transposed][kind];
+    a.rows_log = 4 - kind;
     a.chunk0 = t.chunk0;
     a.chunks = t.chunks;
 }
@@ -248,9 +257,10 @@ void free_attn_plans(Csr *h) {
     for (int t = 0; t < 2; ++t)
         for (int l = 0; l < kAttnLevels; ++l) {
             free_plan(&h->attn->row[t][l]);
-            free_plan(&h->attn->tile[t][l]);
+            for (int k = 0; k < kTileKinds; ++k) free_plan(&h->attn->tile[t][k][l]);
         }
-    for (AttnTiles &t : h->attn->tiles) free_tiles(&t);
+    for (int t = 0; t < 2; ++t)
+        for (AttnTiles &x : h->attn->tiles[t]) free_tiles(&x);
     delete h->attn;
     h->attn = nullptr;
 }
@@ -869,10 +879,10 @@ bool on_16_bytes(const void *p, const int64_t st[3], size_t size) {
 size_t acc_size(int32_t dt) { return dt == SLA_F64 ? 8 : 4; }
 
 template <typename T>
-sla_status attn_forward(const Csr *h, const AttnPlan &p, AttnArgs a, bool tiled, cudaStream_t s) {
+sla_status attn_forward(const Csr *h, const AttnPlan &p, AttnArgs a, bool tiled, int kind, cudaStream_t s) {
     using A = typename AccOf<T>::type;
     use_plan(a, p);
-    use_tiles(a, h->attn->tiles[0]);
+    use_tiles(a, h, false, kind);
     sla_status st;
     if constexpr (sizeof(T) == 2) {
         if (tiled) {
@@ -903,7 +913,8 @@ sla_status attn_dvals(const AttnArgs &a, bool tiled, cudaStream_t s) {
 }
 
 template <typename T>
-sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, AttnArgs a, bool tiled, cudaStream_t s) {
+sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, AttnArgs a, bool tiled, int kind,
+                         cudaStream_t s) {
     using A = typename AccOf<T>::type;
     const int64_t dense[3] = {(int64_t)a.dim, (int64_t)a.dim, (int64_t)a.dim};
     const bool vec = a.dim % (16 / (int)sizeof(T)) == 0 && on_16_bytes(a.q, a.qs, sizeof(T)) &&
@@ -912,7 +923,7 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
                      on_16_bytes(a.dq, dense, sizeof(T)) && on_16_bytes(a.dk, dense, sizeof(T)) &&
                      on_16_bytes(a.dv, dense, sizeof(T));
     use_plan(a, p);
-    use_tiles(a, h->attn->tiles[0]);
+    use_tiles(a, h, false, kind);
     sla_status st;
     if constexpr (sizeof(T) == 2) st = tiled ? attn_tile_bwd_rows<T>(a, s) : launch_rows_of<T>(kBwdRows, a, vec, s);
     else st = launch_rows_of<T>(kBwdRows, a, vec, s);
@@ -924,7 +935,7 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
     }
     if (!a.dk && !a.dv) return SLA_OK;
     use_plan(a, pt);
-    use_tiles(a, h->attn->tiles[1]);
+    use_tiles(a, h, true, 0);
     a.rowptr = h->rowptrT;
     a.colind = h->colindT;
     a.perm = h->permT;
@@ -942,7 +953,9 @@ struct AttnWs {
 };
 
 const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
-    return (attn_tiled(o) ? h->attn->tile : h->attn->row)[transposed][attn_level(h, o)];
+    const int l = attn_level(h, o);
+    if (!attn_tiled(o)) return h->attn->row[transposed][l];
+    return h->attn->tile[transposed][transposed ? 0 : attn_tile_kind(o)][l];
 }
 
 AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
@@ -985,18 +998,10 @@ sla_status check_device(const char *fn, const Csr *h) {
 
 bool plans_ready(const Csr *h, const sla_attn_opts *o, bool backward) {
     if (!h->attn || (backward && !h->has_transpose)) return false;
-    for (int l = 0; l < kAttnLevels; ++l)
-        for (int tiled = 0; tiled < 2; ++tiled) {
-            if (o && (l != attn_level(h, o) || (bool)tiled != attn_tiled(o))) continue;
-            const auto &p = tiled ? h->attn->tile : h->attn->row;
-            if (!p[0][l].built || (backward && !p[1][l].built)) return false;
-        }
-    return true;
+    return plan_of(h, o, false).built && (!backward || plan_of(h, o, true).built);
 }
 
-// The plans these options need; every one without options.
 sla_status prepare(Csr *h, const sla_attn_opts *o, bool backward, cudaStream_t s) {
-    if (plans_ready(h, o, backward)) return SLA_OK;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(s, &cap) != cudaSuccess || cap != cudaStreamCaptureStatusNone) {
         cudaGetLastError();
@@ -1015,9 +1020,11 @@ sla_status prepare(Csr *h, const sla_attn_opts *o, bool backward, cudaStream_t s
     if (backward && (st = ensure_transpose(h, s)) != SLA_OK) return st;
     for (int l = 0; l < kAttnLevels; ++l)
         for (int tiled = 0; tiled < 2; ++tiled) {
-            if (o && (l != attn_level(h, o) || (bool)tiled != attn_tiled(o))) continue;
-            for (int t = 0; t <= (backward ? 1 : 0); ++t)
-                if ((st = ensure_plan(h, tiled != 0, t != 0, l, s)) != SLA_OK) return st;
+            if (o && (bool)tiled != attn_tiled(o)) continue;
+            const int kind = tiled ? (o ? attn_tile_kind(o) : 0) : kRowKind;
+            st = ensure_plan(h, kind, false, l, s);
+            if (st == SLA_OK && backward) st = ensure_plan(h, tiled ? 0 : kRowKind, true, l, s);
+            if (st != SLA_OK) return st;
         }
     return SLA_OK;
 }
@@ -1075,7 +1082,8 @@ extern "C" sla_status sla_attention_prepare(sla_csr_t hh, const sla_attn_opts *o
     Csr *h = reinterpret_cast<Csr *>(hh);
     sla_status st = check_device("sla_attention_prepare", h);
     if (st == SLA_OK && o) st = check_opts("sla_attention_prepare", o);
-    return st != SLA_OK ? st : prepare(h, o, backward != 0, as_stream(stream));
+    if (st != SLA_OK || (o && plans_ready(h, o, backward != 0))) return st;
+    return prepare(h, o, backward != 0, as_stream(stream));
 }
 
 extern "C" size_t sla_attention_workspace_bytes(sla_csr_t hh, const sla_attn_opts *o, int32_t backward) {
@@ -1100,8 +1108,7 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     st = check_tiled("sla_attention", o, {out, out_wide}, {{q, o->q_stride}, {k, o->k_stride}, {v, o->v_stride}});
     if (st != SLA_OK) return st;
     cudaStream_t s = as_stream(stream);
-    st = prepare(h, o, false, s);
-    if (st != SLA_OK) return st;
+    if (!plans_ready(h, o, false) && (st = prepare(h, o, false, s)) != SLA_OK) return st;
     const AttnWs ww = attn_ws(h, o, false);
     const size_t need = ww.total();
     SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention: workspace too small (%zu < %zu)", ws_bytes, need);
@@ -1115,11 +1122,12 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     a.part = c.take<char>(ww.part);
     const AttnPlan &p = plan_of(h, o, false);
     const bool tiled = attn_tiled(o);
+    const int kind = attn_tile_kind(o);
     switch (o->dtype) {
-        case SLA_F64: return attn_forward<double>(h, p, a, tiled, s);
-        case SLA_F32: return attn_forward<float>(h, p, a, tiled, s);
-        case SLA_BF16: return attn_forward<__nv_bfloat16>(h, p, a, tiled, s);
-        default: return attn_forward<__half>(h, p, a, tiled, s);
+        case SLA_F64: return attn_forward<double>(h, p, a, tiled, kind, s);
+        case SLA_F32: return attn_forward<float>(h, p, a, tiled, kind, s);
+        case SLA_BF16: return attn_forward<__nv_bfloat16>(h, p, a, tiled, kind, s);
+        default: return attn_forward<__half>(h, p, a, tiled, kind, s);
     }
 }
 
@@ -1141,8 +1149,7 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     if (st != SLA_OK) return st;
     cudaStream_t s = as_stream(stream);
     if (!dq && !dk && !dv && !dvals) return SLA_OK;
-    st = prepare(h, o, true, s);
-    if (st != SLA_OK) return st;
+    if (!plans_ready(h, o, true) && (st = prepare(h, o, true, s)) != SLA_OK) return st;
     const AttnWs w = attn_ws(h, o, true);
     SLA_REQUIRE(w.total() == 0 || (ws && ws_bytes >= w.total()), "sla_attention_grad: workspace too small (%zu < %zu)",
                 ws_bytes, w.total());
@@ -1164,10 +1171,11 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     if (!dk && !dv && !dvals) a.pds = nullptr;
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
     const bool tiled = attn_tiled(o);
+    const int kind = attn_tile_kind(o);
     switch (o->dtype) {
-        case SLA_F64: return attn_backward<double>(h, p, pt, a, tiled, s);
-        case SLA_F32: return attn_backward<float>(h, p, pt, a, tiled, s);
-        case SLA_BF16: return attn_backward<__nv_bfloat16>(h, p, pt, a, tiled, s);
-        default: return attn_backward<__half>(h, p, pt, a, tiled, s);
+        case SLA_F64: return attn_backward<double>(h, p, pt, a, tiled, kind, s);
+        case SLA_F32: return attn_backward<float>(h, p, pt, a, tiled, kind, s);
+        case SLA_BF16: return attn_backward<__nv_bfloat16>(h, p, pt, a, tiled, kind, s);
+        default: return attn_backward<__half>(h, p, pt, a, tiled, kind, s);
     }
 }

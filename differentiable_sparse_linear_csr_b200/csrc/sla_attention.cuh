@@ -32,8 +32,10 @@ struct AttnPlan {
     int32_t *multi_slot = nullptr;                                             // [n_multi + 1]
 };
 
-// The tiles (kTileRows rows each) of one direction: the columns that any row of
-// the tile stores, in increasing order, 16 to a chunk.
+// The tiles of one direction: the columns that any row of a tile stores, in
+// increasing order, 16 to a chunk.  A tile is the left side of a 16-row matrix
+// product: 16 rows, or fewer rows with several of the query heads that share a key
+// head (16 / 2^k rows with 2^k heads).
 struct AttnTiles {
     bool built = false;
     int32_t *chunk0 = nullptr;         // [n_units + 1]: first chunk of each tile
@@ -41,7 +43,7 @@ struct AttnTiles {
 };
 struct TileChunk {
     int32_t col[16];                   // a tile's last chunk is padded with valid columns
-    uint16_t bits[16];                 // row r: the columns it stores
+    uint16_t bits[16];                 // row r of the tile: the columns it stores
     int32_t start[16];                 // row r: its first entry in this chunk
 };
 
@@ -50,20 +52,31 @@ constexpr int kTileRows = 16;
 // the GPU: a plan for few, some and many of them.
 constexpr int kAttnLevels = 3;
 
+constexpr int kTileKinds = 5;          // tiles of 16, 8, 4, 2, 1 rows (A^T's have 16)
+
 struct AttnPlans {
     AttnPlan row[2][kAttnLevels];      // one row a unit: A, A^T
-    AttnPlan tile[2][kAttnLevels];     // kTileRows rows a unit
-    AttnTiles tiles[2];
+    AttnPlan tile[2][kTileKinds][kAttnLevels];
+    AttnTiles tiles[2][kTileKinds];
 };
 
-inline int attn_level(const Csr *h, const sla_attn_opts *o) {
-    const int64_t share = (int64_t)h->batch * o->heads;
-    return share >= 64 ? 2 : (share >= 8 ? 1 : 0);
+// Tiles of a forward pass: k with 2^k query heads in a tile, the largest power of
+// two that divides the heads sharing a key head.
+inline int attn_tile_kind(const sla_attn_opts *o) {
+    const int share = o->heads / o->kv_heads;
+    int k = 0;
+    while (k < kTileKinds - 1 && share % (2 << k) == 0) ++k;
+    return k;
 }
 
 // 16-bit heads of whole 16-element steps go through the tensor cores.
 inline bool attn_tiled(const sla_attn_opts *o) {
     return (o->dtype == SLA_BF16 || o->dtype == SLA_F16) && o->dim % 16 == 0 && o->dim <= 128;
+}
+
+inline int attn_level(const Csr *h, const sla_attn_opts *o) {
+    const int64_t share = (int64_t)h->batch * (attn_tiled(o) ? o->heads >> attn_tile_kind(o) : o->heads);
+    return share >= 64 ? 2 : (share >= 8 ? 1 : 0);
 }
 
 // What every kernel gets (strides in elements, heads of `dim` consecutive elements).
@@ -74,7 +87,8 @@ struct AttnArgs {
     const int32_t *rowptr, *colind, *perm;
     int32_t n_items, n_slots, seg_len;
     const int32_t *item_unit, *item_seg, *item_slot;
-    const int32_t *chunk0;                 // tiles: chunks of each unit, and of each item of a split plan
+    int32_t rows_log;                      // tiles: rows of one, as a power of two
+    const int32_t *chunk0;                 // chunks of each unit, and of each item of a split plan
     const int2 *item_chunks;
     const TileChunk *chunks;
     const void *q, *k, *v, *o, *dout;
@@ -181,7 +195,7 @@ sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int 
                           cudaStream_t s);
 
 // Tile kernels (sla_attention_tile.cu): plan arrays of a tile plan, and the calls.
-sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s);
 template <typename T> sla_status attn_tile_forward(AttnArgs a, cudaStream_t s);
 template <typename T> sla_status attn_tile_bwd_rows(AttnArgs a, cudaStream_t s);

@@ -18,8 +18,9 @@
 // Rows lie an odd number of pieces apart (1 modulo 8), which keeps both reads free
 // of bank conflicts and every address a constant away from one number a lane.
 // Narrow heads go several to a warp, so that a gathered row is at least 128
-// consecutive bytes and the chunk's bookkeeping is shared; so do heads that
-// share their key head, which is then fetched once.
+// consecutive bytes and the chunk's bookkeeping is shared.  Query heads that share
+// a key head are rows of one matrix product: 2^k of them with 16 / 2^k rows of the
+// pattern, which store fewer different columns, and what is gathered serves all.
 //
 // Scores: 16-bit products, exact, summed in 32 bits.  Weights are not rounded to
 // 16 bits: they multiply as tf32 (the 16-bit operand is exact in it), as a sum of
@@ -47,12 +48,12 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // ----------------------------------------------------------------- plan ----
 // One warp a part of a tile: the columns from one entry of the tile's longest
-// row to the entry seg_len further on.  Lane r < 16 walks row r's entries
+// row to the entry seg_len further on.  Lane r < rows walks row r's entries
 // there, and the smallest column any row is at is the next one.  FILL == false
 // counts the columns; FILL writes them, at[part] columns after the first part's.
 template <bool FILL>
 __global__ void __launch_bounds__(128)
-tile_columns_kernel(int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_parts,
+tile_columns_kernel(int rows, int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_parts,
                     int seg_len, const int32_t *__restrict__ part_unit, const int32_t *__restrict__ part_seg,
                     unsigned *count, const unsigned *__restrict__ at, const int32_t *__restrict__ chunk0,
                     TileChunk *chunks) {
@@ -63,9 +64,9 @@ tile_columns_kernel(int n_rows, const int32_t *__restrict__ rowptr, const int32_
         return;
     }
     const int unit = part_unit ? part_unit[part] : part, seg = part_seg ? part_seg[part] : 0;
-    const int64_t row = (int64_t)unit * kTileRows + lane;
+    const int64_t row = (int64_t)unit * rows + lane;
     int t0 = 0, t1 = 0;
-    if (lane < kTileRows && row < n_rows) {
+    if (lane < rows && row < n_rows) {
         t0 = rowptr[row];
         t1 = rowptr[row + 1];
     }
@@ -261,17 +262,30 @@ __device__ __forceinline__ float score_scale(double scale) {
 __device__ __forceinline__ unsigned pair_bit(int blk, int e) { return 1u << (8 * blk + (e & 1)); }
 
 
+// The rows g and g + 8 of a tile's matrix product: row of the tile and query head.
+struct TileRows {
+    int r[2], h[2];
+    __device__ __forceinline__ TileRows(int rows_log, int g) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            r[i] = (g + 8 * i) & ((1 << rows_log) - 1);
+            h[i] = (g + 8 * i) >> rows_log;
+        }
+    }
+};
+
 // The tile's own 16 rows as the left operand of score products.
 template <int D>
 struct Own {
     uint32_t a[D / 16][4];
-    // `stride`: bytes from row to row, below 2^32.
+    // `stride`: bytes from row to row, below 2^32; `head`: elements between heads.
     template <typename T>
-    __device__ __forceinline__ void load(const T *base, unsigned stride, int row0, int n_rows, int g, int c) {
+    __device__ __forceinline__ void load(const T *base, unsigned stride, int64_t head, const TileRows &t, int row0, int n_rows,
+                                         int c) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool on = row0 + g + 8 * i < n_rows;
-            const char *p = reinterpret_cast<const char *>(base) + (uint64_t)(unsigned)(row0 + g + 8 * i) * stride;
+            const bool on = row0 + t.r[i] < n_rows;
+            const char *p = reinterpret_cast<const char *>(base + t.h[i] * head) + (uint64_t)(unsigned)(row0 + t.r[i]) * stride;
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
                 const int at = j < D / 64 * 2 ? c * 2 + (j >> 1) * 8 + (j & 1) : c + D / 64 * 8;
@@ -442,8 +456,8 @@ struct Cursor {
     unsigned x;                // place within a (system, key head group): item * groups + group
     int b, kh;                 // system, first key head
     __device__ __forceinline__ unsigned item(unsigned groups) const { return groups == 1 ? x : x / groups; }
-    __device__ __forceinline__ int head(unsigned groups, int share, int n_h) const {
-        return kh * share + (groups == 1 ? 0 : (int)(x % groups) * n_h);
+    __device__ __forceinline__ int head(unsigned groups, int share) const {
+        return kh * share + (groups == 1 ? 0 : (int)(x % groups) * (share / (int)groups));
     }
 };
 struct Stride {
@@ -484,13 +498,13 @@ __device__ __forceinline__ int2 item_range(const AttnArgs &a, unsigned it) {
     return make_int2(__ldg(a.chunk0 + it), __ldg(a.chunk0 + it + 1));
 }
 
-__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c, unsigned groups, int share, int n_h) {
+__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c, unsigned groups, int share) {
     TileWork w;
     const unsigned it = c.item(groups);
     w.b = c.b;
     w.kh = c.kh;
-    w.h = c.head(groups, share, n_h);
-    w.row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
+    w.h = c.head(groups, share);
+    w.row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) << a.rows_log;
     w.slot = a.item_unit ? __ldg(a.item_slot + it) : -1;
     const int2 r = item_range(a, it);
     w.ch0 = r.x;
@@ -498,12 +512,14 @@ __device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c
     return w;
 }
 
-// Brings the lines of rows that will be loaded soon into the L2 cache: lane r < 16
-// names row r's D elements.
+// Brings the lines of a tile's rows, which will be loaded soon, into the L2 cache:
+// lane m < 16 names row m of its matrix product, of D elements.
 template <typename T, int D>
-__device__ __forceinline__ void prefetch_rows(const T *base, int64_t stride, int row0, int n_rows, int lane) {
-    if (lane < kTileRows && row0 + lane < n_rows) {
-        const T *p = base + (int64_t)(row0 + lane) * stride;
+__device__ __forceinline__ void prefetch_rows(const T *base, int64_t stride, int64_t head, int rows_log, int row0, int n_rows,
+                                              int lane) {
+    const int r = row0 + (lane & ((1 << rows_log) - 1));
+    if (lane < kTileRows && r < n_rows) {
+        const T *p = base + (int64_t)r * stride + (lane >> rows_log) * head;
 #pragma unroll
         for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
     }
@@ -515,13 +531,12 @@ template <bool ENTRIES>
 struct Chunk {
     unsigned bits[2];
     int at[2];
-    __device__ __forceinline__ void load(const TileChunk *chunks, int ch, int g) {
+    __device__ __forceinline__ void load(const TileChunk *chunks, int ch, const TileRows &t) {
         const TileChunk *p = chunks + ch;
-        bits[0] = __ldg(p->bits + g);
-        bits[1] = __ldg(p->bits + 8 + g);
-        if constexpr (ENTRIES) {
-            at[0] = __ldg(p->start + g);
-            at[1] = __ldg(p->start + 8 + g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            bits[i] = __ldg(p->bits + t.r[i]);
+            if constexpr (ENTRIES) at[i] = __ldg(p->start + t.r[i]);
         }
     }
     // Entries of rows g and g + 8 at columns 8 blk + 2c (the next column's entry
@@ -637,7 +652,7 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
     const float scale = (float)a.scale, none = neg_inf<float>();
-    for (int r = 0; r < kTileRows && w.row0 + r < a.n_rows; ++r) {
+    for (int r = 0; r < 1 << a.rows_log && w.row0 + r < a.n_rows; ++r) {
         const int t0 = __shfl_sync(kAll, s0, r), t1 = __shfl_sync(kAll, s1, r);
         float q[kSlowVec], acc[kSlowVec] = {}, m = none, l = 0.0f;
         slow_load(q, qb + (w.row0 + r) * a.qs[1], a.dim, lane);
@@ -667,7 +682,7 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
             if (lane == 0) static_cast<float *>(a.lse)[at] = l == 0.0f ? none : m + logf(l);
         } else {
             float *p = static_cast<float *>(a.part) +
-                       part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h) * (a.dim + 2);
+                       part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h) * (a.dim + 2);
 #pragma unroll
             for (int i = 0; i < kSlowVec; ++i)
                 if (i * 32 + lane < a.dim) p[i * 32 + lane] = acc[i];
@@ -744,15 +759,16 @@ __device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, un
     return first < total ? (total - first + stride - 1) / stride : 0;
 }
 
-// H heads a warp, on KH key heads (H: one each; 1: one for all).
-template <typename T, int D, int H, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads, D * H <= 64 ? 3 : 2)
+// KH key heads a warp; with one, the query heads of the tile share it.
+template <typename T, int D, int KH, bool VALS>
+__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 ? 3 : 2)
 tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)share * KH / H;
+    const unsigned groups = (unsigned)share >> (4 - a.rows_log);     // of query heads on a key head
+    const TileRows rows(a.rows_log, g);
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
@@ -766,9 +782,9 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
-        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
-        prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + f.head(groups, share, H) * a.qs[2], a.qs[1],
-                                row0, a.n_rows, lane);
+        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) << a.rows_log;
+        prefetch_rows<T, D * KH>(static_cast<const T *>(a.q) + f.b * a.qs[0] + f.head(groups, share) * a.qs[2], a.qs[1],
+                                 a.qs[2], a.rows_log, row0, a.n_rows, lane);
     };
     auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
@@ -776,27 +792,27 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share, H);
+        const TileWork w = tile_work(a, now, groups, share);
         const int n = w.ch1 - w.ch0;
-        Own<D> q[H];
+        Own<D> q[KH];
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h + j) * a.qs[2], qst, w.row0, a.n_rows, g, c);
-        Sums<T, D> acc[H];
-        float m[H][2], l[H][2];
+        for (int j = 0; j < KH; ++j)
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + (w.h + j) * a.qs[2], qst, a.qs[2], rows, w.row0, a.n_rows, c);
+        Sums<T, D> acc[KH];
+        float m[KH][2], l[KH][2];
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
+        for (int j = 0; j < KH; ++j) {
             acc[j].zero();
             m[j][0] = m[j][1] = l[j][0] = l[j][1] = 0.0f;
         }
         Chunk<VALS> next, cur;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, rows);
         if constexpr (VALS) {
             cur = next;
             if (n > 0) cur.values(x_next, vals, c);
-            if (n > 0) next.load(a.chunks, w.ch0 + min(1, n - 1), g);
+            if (n > 0) next.load(a.chunks, w.ch0 + min(1, n - 1), rows);
         }
         for (int ch = 0; ch < n; ++ch) {
             // bookkeeping of this chunk, and loads of the next one's
@@ -811,11 +827,11 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                     for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
                 cur = next;
                 cur.values(x_next, vals, c);
-                next.load(a.chunks, w.ch0 + min(ch + 2, n - 1), g);
+                next.load(a.chunks, w.ch0 + min(ch + 2, n - 1), rows);
             } else {
                 bits[0] = next.bits[0];
                 bits[1] = next.bits[1];
-                next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), g);
+                next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), rows);
             }
             cp_wait<R::kStages - 2>();
             __syncwarp();
@@ -842,7 +858,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
+            for (int j = 0; j < KH; ++j) {
                 const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
                 float s[2][4], t[2][4], far[2] = {none, none};
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
@@ -898,9 +914,10 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         // would not show).
         bool bad = false;
 #pragma unroll
-        for (int j = 0; j < H; ++j) bad = acc[j].bad() || __any_sync(kAll, l[j][0] != l[j][0] || l[j][1] != l[j][1]) || bad;
+        for (int j = 0; j < KH; ++j) bad = acc[j].bad() || __any_sync(kAll, l[j][0] != l[j][0] || l[j][1] != l[j][1]) || bad;
         if (bad) {
-            for (int j = 0; j < H; ++j) {
+            const int heads = KH == 1 ? kTileRows >> a.rows_log : KH;
+            for (int j = 0; j < heads; ++j) {
                 TileWork one = w;
                 one.h = w.h + j;
                 one.kh = KH == 1 ? w.kh : w.kh + j;
@@ -911,7 +928,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         const int64_t at0 = ((int64_t)w.b * a.n_rows + w.row0) * a.heads + w.h;     // row row0, head h
         const unsigned step = (unsigned)a.heads;
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
+        for (int j = 0; j < KH; ++j) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 l[j][i] += __shfl_xor_sync(kAll, l[j][i], 1);
@@ -921,18 +938,18 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                                          l[j][1] > 0.0f ? __fdividef(1.0f, l[j][1]) : 0.0f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = g + 8 * i;
+                const int r = rows.r[i], h = rows.h[i] + j;
                 if (w.row0 + r >= a.n_rows) continue;
                 // no weight: lse is -inf
                 const float top = l[j][i] == 0.0f ? none : (VALS ? m[j][i] : m[j][i] * kLn2);
                 if (w.slot < 0) {
-                    const int64_t o = at0 + (uint64_t)(unsigned)r * step + j;
+                    const int64_t o = at0 + (uint64_t)(unsigned)r * step + h;
                     acc[j].store(static_cast<T *>(a.out) + o * D, i, c);
                     if (a.wide) acc[j].store(static_cast<float *>(a.wide) + o * D, i, c);
                     if (c == 0) static_cast<float *>(a.lse)[o] = top + __log2f(l[j][i] == 0.0f ? 1.0f : l[j][i]) * kLn2;
                 } else {
                     float *p = static_cast<float *>(a.part) +
-                               part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h + j) * (D + 2);
+                               part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h + h) * (D + 2);
                     acc[j].store_odd(p, i, c);          // D + 2 numbers a partial
                     if (c == 0) {
                         p[D] = top;
@@ -954,7 +971,7 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
     const float scale = (float)a.scale, none = neg_inf<float>();
-    for (int r = 0; r < kTileRows && w.row0 + r < a.n_rows; ++r) {
+    for (int r = 0; r < 1 << a.rows_log && w.row0 + r < a.n_rows; ++r) {
         const int t0 = __shfl_sync(kAll, s0, r), t1 = __shfl_sync(kAll, s1, r);
         const int64_t row = w.row0 + r, at = ((int64_t)w.b * a.n_rows + row) * a.heads + w.h;
         float q[kSlowVec], go[kSlowVec], o[kSlowVec], acc[kSlowVec] = {};
@@ -980,7 +997,7 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
                 const int d = i * 32 + lane;
                 if (w.slot < 0) static_cast<T *>(a.dq)[at * a.dim + d] = from_acc<T>(acc[i] * scale);
                 else
-                    static_cast<float *>(a.part)[part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h) * a.dim + d] =
+                    static_cast<float *>(a.part)[part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h) * a.dim + d] =
                         acc[i] * scale;
             }
     }
@@ -1018,14 +1035,15 @@ __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__
 }
 
 // By A's rows: dq, and ds of every entry if asked for.
-template <typename T, int D, int H, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads, D * H <= 64 ? 3 : 2)
+template <typename T, int D, int KH, bool VALS>
+__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 ? 3 : 2)
 tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)share * KH / H;
+    const unsigned groups = (unsigned)share >> (4 - a.rows_log);     // of query heads on a key head
+    const TileRows rows(a.rows_log, g);
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
                    dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
@@ -1040,10 +1058,12 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
-        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) * kTileRows;
-        const int h = f.head(groups, share, H);
-        prefetch_rows<T, D * H>(static_cast<const T *>(a.q) + f.b * a.qs[0] + h * a.qs[2], a.qs[1], row0, a.n_rows, lane);
-        prefetch_rows<T, D * H>(static_cast<const T *>(a.dout) + f.b * a.ds[0] + h * a.ds[2], a.ds[1], row0, a.n_rows, lane);
+        const int row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) << a.rows_log;
+        const int h = f.head(groups, share);
+        prefetch_rows<T, D * KH>(static_cast<const T *>(a.q) + f.b * a.qs[0] + h * a.qs[2], a.qs[1], a.qs[2], a.rows_log,
+                                 row0, a.n_rows, lane);
+        prefetch_rows<T, D * KH>(static_cast<const T *>(a.dout) + f.b * a.ds[0] + h * a.ds[2], a.ds[1], a.ds[2], a.rows_log,
+                                 row0, a.n_rows, lane);
     };
     auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
@@ -1051,23 +1071,23 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share, H);
+        const TileWork w = tile_work(a, now, groups, share);
         const int n = w.ch1 - w.ch0;
-        Own<D> q[H], go[H];
-        float lse[H][2], delta[H][2];
-        bool dead[H][2];
-        Sums<T, D> acc[H];
+        Own<D> q[KH], go[KH];
+        float lse[KH][2], delta[KH][2];
+        bool dead[KH][2];
+        Sums<T, D> acc[KH];
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
+        for (int j = 0; j < KH; ++j) {
             const int h = w.h + j;
-            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, w.row0, a.n_rows, g, c);
-            go[j].load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, w.row0, a.n_rows, g, c);
+            q[j].load(static_cast<const T *>(a.q) + w.b * a.qs[0] + h * a.qs[2], qst, a.qs[2], rows, w.row0, a.n_rows, c);
+            go[j].load(static_cast<const T *>(a.dout) + w.b * a.ds[0] + h * a.ds[2], dst, a.ds[2], rows, w.row0, a.n_rows, c);
             acc[j].zero();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t row = w.row0 + g + 8 * i;
+                const int64_t row = w.row0 + rows.r[i];
                 float2 st = make_float2(none, 0.0f);
-                if (row < a.n_rows) st = __ldg(a.stat + ((int64_t)w.b * a.heads + h) * a.n_rows + row);
+                if (row < a.n_rows) st = __ldg(a.stat + ((int64_t)w.b * a.heads + h + rows.h[i]) * a.n_rows + row);
                 lse[j][i] = st.x;
                 delta[j][i] = st.y;
                 dead[j][i] = st.x == none;
@@ -1077,7 +1097,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         Chunk<VALS> next, cur;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, rows);
         if constexpr (VALS)
             if (n > 0) next.values(x_next, vals, c);
         for (int ch = 0; ch < n; ++ch) {
@@ -1087,7 +1107,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
-            next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), g);
+            next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), rows);
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
@@ -1113,7 +1133,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 }
             }
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
+            for (int j = 0; j < KH; ++j) {
                 const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
@@ -1132,7 +1152,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int blk = 0; blk < 2; ++blk) {
-                            float *p = ds_out + j * a.nnz + cur.entry(i, blk, c);
+                            float *p = ds_out + (j + rows.h[i]) * a.nnz + cur.entry(i, blk, c);
                             if (there[i] & pair_bit(blk, 0)) p[0] = s[blk][2 * i];
                             if (there[i] & pair_bit(blk, 1)) p[there[i] >> (8 * blk) & 1] = s[blk][2 * i + 1];
                         }
@@ -1143,9 +1163,10 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         if (!a.dq) continue;
         bool bad = false;
 #pragma unroll
-        for (int j = 0; j < H; ++j) bad = acc[j].bad() || bad;
+        for (int j = 0; j < KH; ++j) bad = acc[j].bad() || bad;
         if (bad) {
-            for (int j = 0; j < H; ++j) {
+            const int heads = KH == 1 ? kTileRows >> a.rows_log : KH;
+            for (int j = 0; j < heads; ++j) {
                 TileWork one = w;
                 one.h = w.h + j;
                 one.kh = KH == 1 ? w.kh : w.kh + j;
@@ -1154,18 +1175,17 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             continue;
         }
 #pragma unroll
-        for (int j = 0; j < H; ++j) {
+        for (int j = 0; j < KH; ++j) {
             acc[j].scale((float)a.scale, (float)a.scale);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int r = g + 8 * i;
+                const int r = rows.r[i], h = w.h + rows.h[i] + j;
                 if (w.row0 + r >= a.n_rows) continue;
                 if (w.slot < 0)
-                    acc[j].store(static_cast<T *>(a.dq) +
-                                     (((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + w.h + j) * D, i, c);
+                    acc[j].store(static_cast<T *>(a.dq) + (((int64_t)w.b * a.n_rows + w.row0 + r) * a.heads + h) * D, i, c);
                 else
                     acc[j].store(static_cast<float *>(a.part) +
-                                     part_index(w.slot, a.n_slots, w.b, kTileRows, r, a.heads, w.h + j) * D, i, c);
+                                     part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, h) * D, i, c);
             }
         }
     }
@@ -1231,6 +1251,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, true>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
+    const TileRows rows(4, g);
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
                    dst = (unsigned)a.ds[1] * 2;
@@ -1259,9 +1280,9 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         fkh = f.kh;
         open_head(f.b, f.kh * share);
         const int row0 = (a.item_unit ? __ldg(a.item_unit + f.x) : (int)f.x) * kTileRows;
-        prefetch_rows<T, D * KH>(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[1], row0, a.n_cols, lane);
+        prefetch_rows<T, D * KH>(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[1], 0, 4, row0, a.n_cols, lane);
         if (DK)
-            prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], row0, a.n_cols, lane);
+            prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], 0, 4, row0, a.n_cols, lane);
     };
     auto copy = [&](unsigned st, unsigned col) {
         R::gather(st, qb, qst, gb, dst, col, lane);
@@ -1282,14 +1303,14 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, 1, share, KH);
+        const TileWork w = tile_work(a, now, 1, share);
         Own<D> k[KH], v[DK ? KH : 1];
         Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
-            k[j].load(static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.kh + j) * a.ks[2], kst, w.row0, a.n_cols, g, c);
+            k[j].load(static_cast<const T *>(a.k) + w.b * a.ks[0] + (w.kh + j) * a.ks[2], kst, 0, rows, w.row0, a.n_cols, c);
             if constexpr (DK) {
-                v[j].load(static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.kh + j) * a.vs[2], vst, w.row0, a.n_cols, g, c);
+                v[j].load(static_cast<const T *>(a.v) + w.b * a.vs[0] + (w.kh + j) * a.vs[2], vst, 0, rows, w.row0, a.n_cols, c);
                 dk[j].zero();
             }
             if constexpr (DV) dv[j].zero();
@@ -1299,7 +1320,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         Chunk<VALS> next;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, g);
+        if (n > 0) next.load(a.chunks, w.ch0, rows);
         if constexpr (VALS)
             if (n > 0) next.values(x_next, vals, c);
         for (int x = 0; x < steps; ++x) {
@@ -1310,7 +1331,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) val[blk][e] = x_next[blk][e];
             ci = ci + 1 == n ? 0 : ci + 1;
-            next.load(a.chunks, w.ch0 + ci, g);
+            next.load(a.chunks, w.ch0 + ci, rows);
             cp_wait<R::kStages - 2>();
             __syncwarp();
             feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
@@ -1408,11 +1429,12 @@ sla_status tile_values(const AttnArgs &a, const int32_t *perm, float *out, cudaS
 // -------------------------------------------------------------- launches ----
 enum { kTileFwd, kTileBwdRows, kTileBwdCols };
 
-// H heads a warp on KH key heads; for the columns KH of them.
-template <typename T, int D, int H, int KH, bool VALS>
+// KH key heads a warp.
+template <typename T, int D, int KH, bool VALS>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
     const bool cols = what == kTileBwdCols;
-    const int64_t total = (int64_t)a.n_items * (cols ? 1 : a.heads / a.kv_heads * KH / H) * a.batch * (a.kv_heads / KH);
+    const int64_t total = (int64_t)a.n_items * (cols ? 1 : (a.heads / a.kv_heads) >> (4 - a.rows_log)) * a.batch *
+                          (a.kv_heads / KH);
     SLA_REQUIRE(total < INT_MAX, "sla_attention: too many rows, systems and heads");
     if (total == 0) return SLA_OK;
     // as many blocks as run at once, each warp going through the work in strides
@@ -1429,19 +1451,16 @@ sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
         SLA_CHECK_LAUNCH();
         return SLA_OK;
     };
-    if (what == kTileFwd) return go(tile_forward_kernel<T, D, H, KH, VALS>, Ring<D, KH, false>::kBytes);
-    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, H, KH, VALS>, Ring<D, KH, false>::kBytes);
-    if constexpr (H == KH) {
-        constexpr int bytes = Ring<D, KH, true>::kBytes;
-        if constexpr (D * KH <= 64) {
-            return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS>, bytes);
-        } else {
-            sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS>, bytes) : SLA_OK;
-            if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS>, bytes);
-            return st;
-        }
+    if (what == kTileFwd) return go(tile_forward_kernel<T, D, KH, VALS>, Ring<D, KH, false>::kBytes);
+    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, KH, VALS>, Ring<D, KH, false>::kBytes);
+    constexpr int bytes = Ring<D, KH, true>::kBytes;
+    if constexpr (D * KH <= 64) {
+        return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS>, bytes);
+    } else {
+        sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS>, bytes) : SLA_OK;
+        if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS>, bytes);
+        return st;
     }
-    return SLA_ERR_UNSUPPORTED;
 }
 
 template <typename T>
@@ -1460,18 +1479,15 @@ sla_status launch_delta(const AttnArgs &a, cudaStream_t s) {
     return go(tile_delta_kernel<T, 16>, 16);
 }
 
-// Heads a warp: as many as fill 128 bytes of a gathered row, if their number
-// allows; two that share a key head while their sums fit the registers.
+// Key heads a warp: as many as fill 128 bytes of a gathered row, if every query
+// head has its own and their number allows.
 template <typename T, int D, bool VALS>
 sla_status launch_tile_heads(int what, const AttnArgs &a, cudaStream_t s) {
-    const int share = a.heads / a.kv_heads;
     if constexpr (D <= 32) {
         constexpr int K = 64 / D;
-        if (share == 1 && a.kv_heads % K == 0) return launch_tile<T, D, K, K, VALS>(what, a, s);
+        if (a.heads == a.kv_heads && a.kv_heads % K == 0) return launch_tile<T, D, K, VALS>(what, a, s);
     }
-    if constexpr (D <= 64)
-        if (what != kTileBwdCols && share % 2 == 0) return launch_tile<T, D, 2, 1, VALS>(what, a, s);
-    return launch_tile<T, D, 1, 1, VALS>(what, a, s);
+    return launch_tile<T, D, 1, VALS>(what, a, s);
 }
 
 template <typename T, int D>
@@ -1495,7 +1511,7 @@ sla_status launch_tile_of(int what, const AttnArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const int32_t *rowptr, const int32_t *colind,
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s) {
     const int n = parts.n_items, U = parts.n_units;
     DeviceScratch tmp(s);
@@ -1506,7 +1522,7 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const in
         return SLA_ERR_OOM;
     }
     const unsigned grid = blocks_of(((int64_t)n + 1) * 32, 128);
-    tile_columns_kernel<false><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+    tile_columns_kernel<false><<<grid, 128, 0, s>>>(rows, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
                                                     parts.item_seg, count, nullptr, nullptr, nullptr);
     SLA_CHECK_LAUNCH();
     sla_status st = exclusive_scan(count, count, (int64_t)n + 1, ws, s);
@@ -1523,7 +1539,7 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int n_rows, const in
         return SLA_ERR_OOM;
     }
     SLA_CHECK_CUDA(cudaMemsetAsync(t->chunks, 0, (size_t)(total > 0 ? total : 1) * sizeof(TileChunk), s));
-    tile_columns_kernel<true><<<grid, 128, 0, s>>>(n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+    tile_columns_kernel<true><<<grid, 128, 0, s>>>(rows, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
                                                    parts.item_seg, nullptr, count, t->chunk0, t->chunks);
     SLA_CHECK_LAUNCH();
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));

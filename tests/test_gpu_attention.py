@@ -102,7 +102,8 @@ def test_patterns(name, code):
 
 @pytest.mark.parametrize("heads,kv,dim", [(1, 1, 16), (4, 4, 64), (8, 2, 32), (6, 3, 48), (3, 1, 80), (2, 2, 96), (2, 1, 112),
                                           (2, 1, 128), (2, 2, 20), (1, 1, 1), (5, 5, 33), (2, 1, 100), (1, 1, 256),
-                                          (1, 1, 255), (16, 1, 8), (33, 11, 4)])
+                                          (1, 1, 255), (16, 1, 8), (33, 11, 4), (16, 1, 64), (24, 2, 32), (32, 1, 16),
+                                          (8, 1, 128), (10, 5, 64), (8, 8, 16), (4, 4, 32)])
 @pytest.mark.parametrize("code", ["f64", "f32", "bf16", "f16"])
 def test_head_layouts(heads, kv, dim, code):
     compare(*inputs("hub", 1, heads, kv, dim, code, True, seed=dim), code)
