@@ -262,14 +262,16 @@ __device__ __forceinline__ float score_scale(double scale) {
 __device__ __forceinline__ unsigned pair_bit(int blk, int e) { return 1u << (8 * blk + (e & 1)); }
 
 
-// The rows g and g + 8 of a tile's matrix product: row of the tile and query head.
+// The rows g and g + 8 of a tile's matrix product: row of the tile and query head
+// (PACK: several heads; else row g + 8 i of head 0).
+template <bool PACK>
 struct TileRows {
     int r[2], h[2];
     __device__ __forceinline__ TileRows(int rows_log, int g) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            r[i] = (g + 8 * i) & ((1 << rows_log) - 1);
-            h[i] = (g + 8 * i) >> rows_log;
+            r[i] = PACK ? (g + 8 * i) & ((1 << rows_log) - 1) : g + 8 * i;
+            h[i] = PACK ? (g + 8 * i) >> rows_log : 0;
         }
     }
 };
@@ -279,8 +281,8 @@ template <int D>
 struct Own {
     uint32_t a[D / 16][4];
     // `stride`: bytes from row to row, below 2^32; `head`: elements between heads.
-    template <typename T>
-    __device__ __forceinline__ void load(const T *base, unsigned stride, int64_t head, const TileRows &t, int row0, int n_rows,
+    template <typename T, bool PACK>
+    __device__ __forceinline__ void load(const T *base, unsigned stride, int64_t head, const TileRows<PACK> &t, int row0, int n_rows,
                                          int c) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -531,7 +533,8 @@ template <bool ENTRIES>
 struct Chunk {
     unsigned bits[2];
     int at[2];
-    __device__ __forceinline__ void load(const TileChunk *chunks, int ch, const TileRows &t) {
+    template <bool PACK>
+    __device__ __forceinline__ void load(const TileChunk *chunks, int ch, const TileRows<PACK> &t) {
         const TileChunk *p = chunks + ch;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -760,15 +763,15 @@ __device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, un
 }
 
 // KH key heads a warp; with one, the query heads of the tile share it.
-template <typename T, int D, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 ? 3 : 2)
+template <typename T, int D, int KH, bool VALS, bool PACK>
+__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 && !(PACK && VALS) ? 3 : 2)
 tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)share >> (4 - a.rows_log);     // of query heads on a key head
-    const TileRows rows(a.rows_log, g);
+    const unsigned groups = PACK ? (unsigned)share >> (4 - a.rows_log) : (unsigned)share;    // of query heads on a key head
+    const TileRows<PACK> rows(a.rows_log, g);
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
     unsigned first, by;
@@ -1035,15 +1038,15 @@ __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__
 }
 
 // By A's rows: dq, and ds of every entry if asked for.
-template <typename T, int D, int KH, bool VALS>
-__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 ? 3 : 2)
+template <typename T, int D, int KH, bool VALS, bool PACK>
+__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 && !(PACK && VALS) ? 3 : 2)
 tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
-    const unsigned groups = (unsigned)share >> (4 - a.rows_log);     // of query heads on a key head
-    const TileRows rows(a.rows_log, g);
+    const unsigned groups = PACK ? (unsigned)share >> (4 - a.rows_log) : (unsigned)share;    // of query heads on a key head
+    const TileRows<PACK> rows(a.rows_log, g);
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
                    dst = (unsigned)a.ds[1] * 2;
     const float scale = score_scale<VALS>(a.scale), none = neg_inf<float>();
@@ -1075,7 +1078,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH], go[KH];
         float lse[KH][2], delta[KH][2];
-        bool dead[KH][2];
+        unsigned live[KH][2];                            // all ones, or 0: the row has no weights
         Sums<T, D> acc[KH];
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
@@ -1090,7 +1093,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 if (row < a.n_rows) st = __ldg(a.stat + ((int64_t)w.b * a.heads + h + rows.h[i]) * a.n_rows + row);
                 lse[j][i] = st.x;
                 delta[j][i] = st.y;
-                dead[j][i] = st.x == none;
+                live[j][i] = st.x == none ? 0u : ~0u;
             }
         }
         float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
@@ -1139,13 +1142,14 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
                 score_products<T, D, R::kPitch>(dp, go[j], at + R::kTensor, g, c);
                 if (VALS && j == 0) next.values(x_next, vals, c);
+                const unsigned on[2] = {mine[0] & live[j][0], mine[1] & live[j][1]};
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e >> 1;
                         s[blk][e] = weight<VALS>(relative<VALS>(s[blk][e], scale, x[blk][e], lse[j][i])) * (dp[blk][e] - delta[j][i]);
-                        s[blk][e] = mine[i] & pair_bit(blk, e) && !dead[j][i] ? s[blk][e] : 0.0f;
+                        s[blk][e] = on[i] & pair_bit(blk, e) ? s[blk][e] : 0.0f;
                     }
                 if (VALS && ds_out) {
 #pragma unroll
@@ -1251,7 +1255,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, true>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
-    const TileRows rows(4, g);
+    const TileRows<false> rows(4, g);
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
                    dst = (unsigned)a.ds[1] * 2;
@@ -1451,8 +1455,13 @@ sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
         SLA_CHECK_LAUNCH();
         return SLA_OK;
     };
-    if (what == kTileFwd) return go(tile_forward_kernel<T, D, KH, VALS>, Ring<D, KH, false>::kBytes);
-    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, KH, VALS>, Ring<D, KH, false>::kBytes);
+    constexpr int row_bytes = Ring<D, KH, false>::kBytes;
+    if constexpr (KH == 1) {
+        if (what == kTileFwd && a.rows_log < 4) return go(tile_forward_kernel<T, D, 1, VALS, true>, row_bytes);
+        if (what == kTileBwdRows && a.rows_log < 4) return go(tile_bwd_rows_kernel<T, D, 1, VALS, true>, row_bytes);
+    }
+    if (what == kTileFwd) return go(tile_forward_kernel<T, D, KH, VALS, false>, row_bytes);
+    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, KH, VALS, false>, row_bytes);
     constexpr int bytes = Ring<D, KH, true>::kBytes;
     if constexpr (D * KH <= 64) {
         return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS>, bytes);

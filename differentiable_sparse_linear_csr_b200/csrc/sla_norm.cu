@@ -24,9 +24,9 @@ namespace sla {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormLoads = 8;                                    // 16-byte loads of a thread in flight
+constexpr int kNormLoads = 4;                                    // 16-byte loads of a thread in flight
 constexpr int kChunkBytes = kNormThreads * kNormLoads * 16;      // what a block takes at a time
-constexpr int kMaxPartials = 1184;
+constexpr int kMaxPartials = 2048;
 
 enum { kNormL2 = 0, kNormMax = 1 };
 
@@ -77,8 +77,22 @@ __device__ __forceinline__ double chunk_norm(const T *p, int64_t count, int64_t 
         return s;
     }
     const int64_t end = e0 + E < count ? e0 + E : count;
+    int64_t from = e0;
+    if (vec) {                       // a tensor's last chunk: whole vectors, then what is left
+        from = e0 + (end - e0) / V * V;
+#pragma unroll
+        for (int i = 0; i < kNormLoads; ++i) {
+            const int64_t at = e0 + (int64_t)(i * kNormThreads + threadIdx.x) * V;
+            if (at < from) {
+                const uint4 r = *reinterpret_cast<const uint4 *>(p + at);
+                const T *x = reinterpret_cast<const T *>(&r);
+#pragma unroll
+                for (int e = 0; e < V; ++e) take<T, KIND>(s, x[e]);
+            }
+        }
+    }
 #pragma unroll 4
-    for (int64_t i = e0 + threadIdx.x; i < end; i += kNormThreads) take<T, KIND>(s, p[i]);
+    for (int64_t i = from + threadIdx.x; i < end; i += kNormThreads) take<T, KIND>(s, p[i]);
     return s;
 }
 
@@ -181,8 +195,23 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t count, int
         return;
     }
     const int64_t end = e0 + E < count ? e0 + E : count;
+    int64_t from = e0;
+    if (vec) {
+        from = e0 + (end - e0) / V * V;
+#pragma unroll
+        for (int i = 0; i < kNormLoads; ++i) {
+            const int64_t at = e0 + (int64_t)(i * kNormThreads + threadIdx.x) * V;
+            if (at < from) {
+                uint4 r = *reinterpret_cast<const uint4 *>(p + at);
+                T *x = reinterpret_cast<T *>(&r);
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[e] = scaled<T>(x[e], f, ff);
+                *reinterpret_cast<uint4 *>(q + at) = r;
+            }
+        }
+    }
 #pragma unroll 4
-    for (int64_t i = e0 + threadIdx.x; i < end; i += kNormThreads) q[i] = scaled<T>(p[i], f, ff);
+    for (int64_t i = from + threadIdx.x; i < end; i += kNormThreads) q[i] = scaled<T>(p[i], f, ff);
 }
 
 // The chunks in the reverse of pass 1's order: the last ones read are the ones
@@ -258,7 +287,7 @@ int num_sms() {
 }
 
 // Chunks that one block takes faster than two launches would.
-constexpr int kSmallChunks = 4;
+constexpr int kSmallChunks = 8;
 
 // Pass 1 over the list, tables of N tensors at a time; then the norm alone, or
 // pass 2.  Partial results: at most kMaxPartials a table.
@@ -271,7 +300,7 @@ sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, v
         SLA_CHECK_LAUNCH();
         return SLA_OK;
     }
-    const unsigned most = std::min(kMaxPartials, num_sms() * 4);
+    const unsigned most = std::min(kMaxPartials, num_sms() * 8);
     int n_part = 0;
     for (int i = 0; i < n;) {
         i = fill(t, list, i, n);
