@@ -362,6 +362,7 @@ class _AttentionCall:
         self.lse = A.batch * A.n_rows * H * (8 if q.dtype == torch.float64 else 4)
         self.ready = [False, False]
         self.opts = self.options(q, k, v)
+        self.back = {}                           # options of the gradients, by the strides they depend on
 
     def options(self, q, k, v, do=None):
         def strides(x):
@@ -416,9 +417,12 @@ class _Attention(torch.autograd.Function):
         new = lambda need, t: torch.empty_like(t, memory_format=torch.contiguous_format) if need else None  # noqa: E731
         dq, dk, dv, dvals = (new(need, t) for need, t in zip(ctx.needs_input_grad[2:6], (q, k, v, values)))
         with _on_device(A.device):
+            key = (q.stride(), k.stride(), v.stride(), go.stride())
+            opts = call.back.get(key)
+            if opts is None:
+                opts = call.back[key] = call.options(q, k, v, go)
             ws = _workspace(call.workspace[1], A.device)
-            L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals,
-                                 call.options(q, k, v, go), ws)
+            L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals, opts, ws)
         return None, None, dq, dk, dv, dvals
 
 

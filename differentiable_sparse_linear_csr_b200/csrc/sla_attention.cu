@@ -146,7 +146,7 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 // heads as the one before, so it splits 8 times less.
 int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 8 >> (3 * level)); }
 
-constexpr int kRowKind = -1;             // plans of rows; tiles of 16 >> kind rows
+constexpr int kRowKind = -1;             // plans of rows, not tiles
 
 AttnPlan &plan_at(Csr *h, int kind, bool transposed, int level) {
     return kind == kRowKind ? h->attn->row[transposed][level] : h->attn->tile[transposed][kind][level];
@@ -161,7 +161,7 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
     AttnTiles *tiles = tiled ? &h->attn->tiles[transposed][kind] : nullptr;
     const int n = transposed ? h->n_cols : h->n_rows;
     const int32_t *rowptr = transposed ? h->rowptrT : h->rowptr, *colind = transposed ? h->colindT : h->colind;
-    p->rows = tiled ? kTileRows >> kind : 1;
+    p->rows = tiled ? kTileRows >> (transposed ? 0 : kind) : 1;
     p->n_units = (n + p->rows - 1) / p->rows;
     const int U = p->n_units;
     constexpr int kLeast = 64;           // entries of a row, columns of a tile
@@ -198,7 +198,7 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
             AttnPlan parts;
             parts.n_units = U;
             st = build_items(&parts, len, 256, 0, 0, nullptr, s);
-            if (st == SLA_OK) st = build_tiles(tiles, parts, p->rows, n, rowptr, colind, s);
+            if (st == SLA_OK) st = build_tiles(tiles, parts, p->rows, transposed ? 1 << kind : 1, n, rowptr, colind, s);
             free_plan(&parts);
             if (st != SLA_OK) return st;
         }
@@ -485,11 +485,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const __gri
             if (a.wide) acc.store(static_cast<A *>(a.wide) + at * a.dim, a.dim, lane);
             if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
         } else {
-            A *p = static_cast<A *>(a.part) + part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h) * (a.dim + 2);
-            acc.store_odd(p, a.dim, lane);
+            const int64_t at = part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h);
+            acc.store_odd(static_cast<A *>(a.part) + at * a.dim, a.dim, lane);
             if (lane == 0) {
-                p[a.dim] = m;
-                p[a.dim + 1] = l;
+                static_cast<A *>(a.part_ml)[at * 2] = m;
+                static_cast<A *>(a.part_ml)[at * 2 + 1] = l;
             }
         }
     }
@@ -540,21 +540,22 @@ attn_join_kernel(const AttnArgs a, int rows, int n_multi, const int32_t *__restr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     JoinAt j;
     if (!join_at(j, blockIdx.x, a.n_rows, rows, a.heads, n_multi, multi_unit, multi_slot)) return;
-    const int64_t step = (int64_t)rows * a.heads * (a.dim + 2);
-    const A *p = static_cast<const A *>(a.part) + part_index(j.s0, a.n_slots, j.b, rows, j.r, a.heads, j.h) * (a.dim + 2);
+    const int64_t from = part_index(j.s0, a.n_slots, j.b, rows, j.r, a.heads, j.h), seg = (int64_t)rows * a.heads;
+    const int64_t step = seg * a.dim;
+    const A *p = static_cast<const A *>(a.part) + from * a.dim, *ml = static_cast<const A *>(a.part_ml) + from * 2;
     const A none = neg_inf<A>();
     A m = none, l = (A)0;
-    for (int s = threadIdx.x; s < j.n; s += 32 * W) m = fmax(m, p[s * step + a.dim]);
+    for (int s = threadIdx.x; s < j.n; s += 32 * W) m = fmax(m, ml[s * seg * 2]);
     m = join_block<A, W>(m, red, true);
     const A ref = m == none ? (A)0 : m;
-    for (int s = threadIdx.x; s < j.n; s += 32 * W) l += p[s * step + a.dim + 1] * exp_acc(p[s * step + a.dim] - ref);
+    for (int s = threadIdx.x; s < j.n; s += 32 * W) l += ml[s * seg * 2 + 1] * exp_acc(ml[s * seg * 2] - ref);
     l = join_block<A, W>(l, red, false);
     const A inv = l > (A)0 || l != l ? (A)1 / l : (A)0;
     A x[8] = {};
     for (int s = warp; s < j.n; s += 4 * W) {
         A w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) w[u] = s + u * W < j.n ? exp_acc(p[(s + u * W) * step + a.dim] - ref) : (A)0;
+        for (int u = 0; u < 4; ++u) w[u] = s + u * W < j.n ? exp_acc(ml[(s + u * W) * seg * 2] - ref) : (A)0;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i * 32 + lane < a.dim)
@@ -935,7 +936,7 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
     }
     if (!a.dk && !a.dv) return SLA_OK;
     use_plan(a, pt);
-    use_tiles(a, h, true, 0);
+    use_tiles(a, h, true, kind);
     a.rowptr = h->rowptrT;
     a.colind = h->colindT;
     a.perm = h->permT;
@@ -948,14 +949,16 @@ sla_status attn_backward(const Csr *h, const AttnPlan &p, const AttnPlan &pt, At
 // Workspace pieces: what the backward keeps for every entry (row kernels) or
 // row (tile kernels), then the partial sums of split rows.
 struct AttnWs {
-    size_t pds = 0, stat = 0, ds = 0, vals_w = 0, part = 0;
-    size_t total() const { return align_up(pds) + align_up(stat) + align_up(ds) + align_up(vals_w) + align_up(part); }
+    size_t pds = 0, stat = 0, ds = 0, vals_w = 0, part = 0, part_ml = 0;
+    size_t total() const {
+        return align_up(pds) + align_up(stat) + align_up(ds) + align_up(vals_w) + align_up(part) + align_up(part_ml);
+    }
 };
 
 const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
     const int l = attn_level(h, o);
     if (!attn_tiled(o)) return h->attn->row[transposed][l];
-    return h->attn->tile[transposed][transposed ? 0 : attn_tile_kind(o)][l];
+    return h->attn->tile[transposed][attn_tile_kind(o)][l];
 }
 
 AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
@@ -964,7 +967,8 @@ AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
     AttnWs w;
     if (!backward) {
         if (attn_tiled(o) && h->dtype == SLA_F64) w.vals_w = B * (size_t)h->nnz * sizeof(float);
-        w.part = B * p.n_slots * p.rows * H * (D + 2) * acc;
+        w.part = B * p.n_slots * p.rows * H * D * acc;
+        w.part_ml = B * p.n_slots * p.rows * H * 2 * acc;
         return w;
     }
     if (attn_tiled(o)) {
@@ -1023,7 +1027,7 @@ sla_status prepare(Csr *h, const sla_attn_opts *o, bool backward, cudaStream_t s
             if (o && (bool)tiled != attn_tiled(o)) continue;
             const int kind = tiled ? (o ? attn_tile_kind(o) : 0) : kRowKind;
             st = ensure_plan(h, kind, false, l, s);
-            if (st == SLA_OK && backward) st = ensure_plan(h, tiled ? 0 : kRowKind, true, l, s);
+            if (st == SLA_OK && backward) st = ensure_plan(h, kind, true, l, s);
             if (st != SLA_OK) return st;
         }
     return SLA_OK;
@@ -1120,6 +1124,7 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     Carver c(ws);
     a.vals_w = reinterpret_cast<float *>(c.take<char>(ww.vals_w));
     a.part = c.take<char>(ww.part);
+    a.part_ml = c.take<char>(ww.part_ml);
     const AttnPlan &p = plan_of(h, o, false);
     const bool tiled = attn_tiled(o);
     const int kind = attn_tile_kind(o);

@@ -35,7 +35,8 @@ struct AttnPlan {
 // The tiles of one direction: the columns that any row of a tile stores, in
 // increasing order, 16 to a chunk.  A tile is the left side of a 16-row matrix
 // product: 16 rows, or fewer rows with several of the query heads that share a key
-// head (16 / 2^k rows with 2^k heads).
+// head (A: 16 / 2^k rows with 2^k heads).  A^T's tiles have 16 rows always, and every
+// column 2^k times in a row, once for each of those heads.
 struct AttnTiles {
     bool built = false;
     int32_t *chunk0 = nullptr;         // [n_units + 1]: first chunk of each tile
@@ -52,7 +53,7 @@ constexpr int kTileRows = 16;
 // the GPU: a plan for few, some and many of them.
 constexpr int kAttnLevels = 3;
 
-constexpr int kTileKinds = 5;          // tiles of 16, 8, 4, 2, 1 rows (A^T's have 16)
+constexpr int kTileKinds = 5;          // k = 0 to 4
 
 struct AttnPlans {
     AttnPlan row[2][kAttnLevels];      // one row a unit: A, A^T
@@ -60,8 +61,8 @@ struct AttnPlans {
     AttnTiles tiles[2][kTileKinds];
 };
 
-// Tiles of a forward pass: k with 2^k query heads in a tile, the largest power of
-// two that divides the heads sharing a key head.
+// The kind k of tiles with 2^k query heads together: the largest power of two that
+// divides the heads sharing a key head.
 inline int attn_tile_kind(const sla_attn_opts *o) {
     const int share = o->heads / o->kv_heads;
     int k = 0;
@@ -87,7 +88,7 @@ struct AttnArgs {
     const int32_t *rowptr, *colind, *perm;
     int32_t n_items, n_slots, seg_len;
     const int32_t *item_unit, *item_seg, *item_slot;
-    int32_t rows_log;                      // tiles: rows of one, as a power of two
+    int32_t rows_log;                      // tiles: rows of one of A's, as a power of two (4 - kind)
     const int32_t *chunk0;                 // chunks of each unit, and of each item of a split plan
     const int2 *item_chunks;
     const TileChunk *chunks;
@@ -102,7 +103,8 @@ struct AttnArgs {
     float *ds_out;                         // tile kernels: [B][heads][nnz] ds, or null
     float *vals_w;                         // tile kernels: room for [B][nnz] 32-bit values
     const float *vals_f, *vals_t;          // and the values as they read them, in A's and A^T's order
-    void *part;                            // partial sums of split rows
+    void *part;                            // partial sums of split rows (part_index)
+    void *part_ml;                         // forward: their maximum and sum, pairs in the same order
 };
 
 // Accumulator type of a storage type: 32 bits for 16- and 32-bit types.
@@ -177,8 +179,8 @@ __device__ __forceinline__ A load_value(const void *vals, int f64, int64_t t) {
     }
 }
 
-// Partial result of one segment: `dim` sums, then the running maximum and sum.
-// Rows of a unit and heads are the fastest indices.
+// Place of one segment's partial result: `dim` sums (forward; `dim` or twice as many
+// backward).  Rows of a unit and heads are the fastest indices.
 __host__ __device__ __forceinline__ int64_t part_index(int64_t slot, int32_t n_slots, int b, int rows, int r,
                                                        int heads, int h) {
     return (((int64_t)b * n_slots + slot) * rows + r) * heads + h;
@@ -195,7 +197,7 @@ sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int 
                           cudaStream_t s);
 
 // Tile kernels (sla_attention_tile.cu): plan arrays of a tile plan, and the calls.
-sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows, const int32_t *rowptr, const int32_t *colind,
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int times, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s);
 template <typename T> sla_status attn_tile_forward(AttnArgs a, cudaStream_t s);
 template <typename T> sla_status attn_tile_bwd_rows(AttnArgs a, cudaStream_t s);

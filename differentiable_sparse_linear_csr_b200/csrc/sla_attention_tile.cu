@@ -50,10 +50,11 @@ constexpr unsigned kAll = 0xffffffffu;
 // One warp a part of a tile: the columns from one entry of the tile's longest
 // row to the entry seg_len further on.  Lane r < rows walks row r's entries
 // there, and the smallest column any row is at is the next one.  FILL == false
-// counts the columns; FILL writes them, at[part] columns after the first part's.
+// counts the columns, each `times` times (a power of two); FILL writes them, at[part]
+// places after the first part's.
 template <bool FILL>
 __global__ void __launch_bounds__(128)
-tile_columns_kernel(int rows, int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_parts,
+tile_columns_kernel(int rows, int times, int n_rows, const int32_t *__restrict__ rowptr, const int32_t *__restrict__ colind, int n_parts,
                     int seg_len, const int32_t *__restrict__ part_unit, const int32_t *__restrict__ part_seg,
                     unsigned *count, const unsigned *__restrict__ at, const int32_t *__restrict__ chunk0,
                     TileChunk *chunks) {
@@ -111,14 +112,14 @@ tile_columns_kernel(int rows, int n_rows, const int32_t *__restrict__ rowptr, co
         const int place = (int)(n & 15);
         if (FILL && place == 0 && lane < kTileRows) ck->start[lane] = t;
         if (cur == c) {
-            row_bits |= 1u << place;
+            row_bits |= ((1u << times) - 1u) << place;
             cur = next;
             ++t;
             next = t + 1 < t1 ? colind[t + 1] : INT_MAX;
         }
         if (lane >= place) mine = c;            // later places hold the last column until they get theirs
-        ++n;
-        if (FILL && place == 15) flush(16);
+        n += times;
+        if (FILL && (n & 15) == 0) flush(16);
     }
     if (FILL && (n & 15) && n > n0) flush(last ? 16 : (int)(n & 15));
     if (!FILL && lane == 0) count[part] = n;
@@ -431,17 +432,6 @@ struct Sums {
             *reinterpret_cast<uint2 *>(p) = make_uint2(narrow2<T>(x[0], x[1]), narrow2<T>(x[2], x[3]));
         }
     }
-    // The same for numbers that need not lie on 16 bytes.
-    __device__ __forceinline__ void store_odd(float *p, int i, int c) const {
-#pragma unroll
-        for (int nb = 0; nb < D / 8; ++nb) {
-            const int n = nb < D / 64 * 8 ? 8 : (nb < D / 32 * 4 ? 4 : 2);              // blocks of the group
-            const int d0 = nb < D / 64 * 8 ? nb / 8 * 64 : (nb < D / 32 * 4 ? D / 64 * 64 : D / 32 * 32);
-            const int d = d0 + 2 * n * c + (nb * 8 - d0) / 8;
-            p[d] = o[nb][2 * i];
-            p[d + n] = o[nb][2 * i + 1];
-        }
-    }
 };
 
 // A piece of work: chunks [ch0, ch1) of a tile, heads h (and following) of one
@@ -500,13 +490,13 @@ __device__ __forceinline__ int2 item_range(const AttnArgs &a, unsigned it) {
     return make_int2(__ldg(a.chunk0 + it), __ldg(a.chunk0 + it + 1));
 }
 
-__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c, unsigned groups, int share) {
+__device__ __forceinline__ TileWork tile_work(const AttnArgs &a, const Cursor &c, unsigned groups, int share, int rows_log) {
     TileWork w;
     const unsigned it = c.item(groups);
     w.b = c.b;
     w.kh = c.kh;
     w.h = c.head(groups, share);
-    w.row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) << a.rows_log;
+    w.row0 = (a.item_unit ? __ldg(a.item_unit + it) : (int)it) << rows_log;
     w.slot = a.item_unit ? __ldg(a.item_slot + it) : -1;
     const int2 r = item_range(a, it);
     w.ch0 = r.x;
@@ -544,19 +534,20 @@ struct Chunk {
     }
     // Entries of rows g and g + 8 at columns 8 blk + 2c (the next column's entry
     // follows if the row stores both).
-    __device__ __forceinline__ int entry(int i, int blk, int c) const {
-        return at[i] + __popc(bits[i] & ((1u << (8 * blk + 2 * c)) - 1u));
+    // times: the log of how often the chunk repeats a column.
+    __device__ __forceinline__ int entry(int i, int blk, int c, int times = 0) const {
+        return at[i] + (__popc(bits[i] & ((1u << (8 * blk + 2 * c)) - 1u)) >> times);
     }
     // The stored values of this thread's 8 pairs, 0 where nothing is stored.
-    __device__ __forceinline__ void values(float (&x)[2][4], const float *vals, int c) const {
+    __device__ __forceinline__ void values(float (&x)[2][4], const float *vals, int c, int times = 0) const {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const unsigned mine = bits[i] >> (2 * c);
 #pragma unroll
             for (int blk = 0; blk < 2; ++blk) {
-                const float *p = vals + entry(i, blk, c);
+                const float *p = vals + entry(i, blk, c, times);
                 x[blk][2 * i] = mine & pair_bit(blk, 0) ? __ldg(p) : 0.0f;
-                x[blk][2 * i + 1] = mine & pair_bit(blk, 1) ? __ldg(p + (mine >> (8 * blk) & 1)) : 0.0f;
+                x[blk][2 * i + 1] = mine & pair_bit(blk, 1) ? __ldg(p + (times ? 0 : mine >> (8 * blk) & 1)) : 0.0f;
             }
         }
     }
@@ -590,17 +581,25 @@ struct Ring {
         const int x = lane % kPieces;
         return p + x / (D / 8) * head_bytes + x % (D / 8) * 16;
     }
-    // Copies of both tensors' rows of the columns in `col` (lane r: column r).
+    // Copies of both tensors' rows of the columns in `col` (lane r: column r).  times:
+    // the log of how often a column is repeated, for the next heads (head0, head1
+    // bytes apart).
     static __device__ __forceinline__ void gather(unsigned stage, const char *p0, unsigned stride0, const char *p1,
-                                                  unsigned stride1, unsigned col, int lane) {
+                                                  unsigned stride1, unsigned col, int lane, int times = 0,
+                                                  int64_t head0 = 0, int64_t head1 = 0) {
 #pragma unroll
         for (int i = 0; i < kPieces / 2; ++i) {
             const int x = i * 32 + lane, r = kEven ? lane / kPieces + i * (32 / kPieces) : x / kPieces;
             const int p = kEven ? lane % kPieces : x - r * kPieces;
             const unsigned cl = __shfl_sync(kAll, col, r), dst = stage + r * kPitch + p * 16;
             const int more = kEven ? 0 : p * 16;       // several heads are even (whole powers of two)
-            cp_async16(dst, p0 + (uint64_t)cl * stride0 + more);
-            cp_async16(dst + kTensor, p1 + (uint64_t)cl * stride1 + more);
+            const char *s0 = p0 + (uint64_t)cl * stride0 + more, *s1 = p1 + (uint64_t)cl * stride1 + more;
+            if (times) {
+                s0 += (r & ((1 << times) - 1)) * head0;
+                s1 += (r & ((1 << times) - 1)) * head1;
+            }
+            cp_async16(dst, s0);
+            cp_async16(dst + kTensor, s1);
         }
     }
 };
@@ -614,12 +613,13 @@ __device__ __forceinline__ unsigned chunk_column(const TileChunk *chunks, int ch
 #endif
 }
 
-// Entry range of row r of the tile in the item (every lane r < 16 its own row).
-__device__ __forceinline__ void row_range(const TileChunk *chunks, const TileWork &w, int lane, int &t0, int &t1) {
+// Entry range of row r of the tile in the item (every lane r < 16 its own row); times:
+// the log of how often a column is repeated.
+__device__ __forceinline__ void row_range(const TileChunk *chunks, const TileWork &w, int lane, int times, int &t0, int &t1) {
     t0 = t1 = 0;
     if (lane < kTileRows && w.ch0 < w.ch1) {
         t0 = t1 = __ldg(chunks[w.ch0].start + lane);
-        for (int ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(chunks[ch].bits + lane));
+        for (int ch = w.ch0; ch < w.ch1; ++ch) t1 += __popc((unsigned)__ldg(chunks[ch].bits + lane)) >> times;
     }
 }
 
@@ -650,7 +650,7 @@ template <typename T>
 __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(a.chunks, w, lane, s0, s1);
+    row_range(a.chunks, w, lane, 0, s0, s1);
     const T *qb = static_cast<const T *>(a.q) + w.b * a.qs[0] + w.h * a.qs[2];
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
@@ -684,15 +684,12 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
                 }
             if (lane == 0) static_cast<float *>(a.lse)[at] = l == 0.0f ? none : m + logf(l);
         } else {
-            float *p = static_cast<float *>(a.part) +
-                       part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h) * (a.dim + 2);
+            const int64_t at = part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h);
+            float *p = static_cast<float *>(a.part) + at * a.dim;
 #pragma unroll
             for (int i = 0; i < kSlowVec; ++i)
                 if (i * 32 + lane < a.dim) p[i * 32 + lane] = acc[i];
-            if (lane == 0) {
-                p[a.dim] = m;
-                p[a.dim + 1] = l;
-            }
+            if (lane == 0) static_cast<float2 *>(a.part_ml)[at] = make_float2(m, l);
         }
     }
 }
@@ -795,7 +792,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share);
+        const TileWork w = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH];
 #pragma unroll
@@ -951,13 +948,9 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                     if (a.wide) acc[j].store(static_cast<float *>(a.wide) + o * D, i, c);
                     if (c == 0) static_cast<float *>(a.lse)[o] = top + __log2f(l[j][i] == 0.0f ? 1.0f : l[j][i]) * kLn2;
                 } else {
-                    float *p = static_cast<float *>(a.part) +
-                               part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h + h) * (D + 2);
-                    acc[j].store_odd(p, i, c);          // D + 2 numbers a partial
-                    if (c == 0) {
-                        p[D] = top;
-                        p[D + 1] = l[j][i];
-                    }
+                    const int64_t at = part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h + h);
+                    acc[j].store(static_cast<float *>(a.part) + at * D, i, c);
+                    if (c == 0) static_cast<float2 *>(a.part_ml)[at] = make_float2(top, l[j][i]);
                 }
             }
         }
@@ -970,7 +963,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w) {
     const int lane = threadIdx.x & 31;
     int s0, s1;
-    row_range(a.chunks, w, lane, s0, s1);
+    row_range(a.chunks, w, lane, 0, s0, s1);
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.kh * a.ks[2];
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.kh * a.vs[2];
     const float scale = (float)a.scale, none = neg_inf<float>();
@@ -1074,7 +1067,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share);
+        const TileWork w = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH], go[KH];
         float lse[KH][2], delta[KH][2];
@@ -1200,7 +1193,7 @@ template <typename T>
 __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w, bool want_dk, bool want_dv) {
     const int lane = threadIdx.x & 31, share = a.heads / a.kv_heads;
     int s0, s1;
-    row_range(a.chunks, w, lane, s0, s1);
+    row_range(a.chunks, w, lane, 4 - a.rows_log, s0, s1);
     const float scale = (float)a.scale, none = neg_inf<float>();
     for (int r = 0; r < kTileRows && w.row0 + r < a.n_cols; ++r) {
         const int t0 = __shfl_sync(kAll, s0, r), t1 = __shfl_sync(kAll, s1, r);
@@ -1249,13 +1242,15 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 // query heads that share one following each other.  Wide heads take two launches:
 // both sums and both own operands would not fit the registers.  The values come in
 // A^T's order (tile_values_kernel).
-template <typename T, int D, int KH, bool DK, bool DV, bool VALS>
+template <typename T, int D, int KH, bool DK, bool DV, bool VALS, bool PACK>
 __global__ void __launch_bounds__(kTileThreads, 2)
 tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, true>;
     extern __shared__ __align__(128) char smem[];
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, share = a.heads / a.kv_heads;
     const TileRows<false> rows(4, g);
+    // PACK: a chunk holds every column (a query row) once for each of 2^times heads
+    const int times = PACK ? 4 - a.rows_log : 0, groups = share >> times;
     const unsigned ring = (unsigned)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * R::kBytes;
     const unsigned qst = (unsigned)a.qs[1] * 2, kst = (unsigned)a.ks[1] * 2, vst = (unsigned)a.vs[1] * 2,
                    dst = (unsigned)a.ds[1] * 2;
@@ -1263,8 +1258,8 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     unsigned first, by;
     const unsigned count = my_share(total, first, by);
     if (count == 0) return;
-    // A piece is a tile with one of the query heads of its key heads; the shared heads
-    // of a tile follow each other and its sums are written after the last one.
+    // A piece is a tile; the shared heads (or groups of them) follow each other and its
+    // sums are written after the last one.
     const Stride stride(by, (unsigned)a.n_items, 1, KH, a.kv_heads);
     Cursor now = stride.at(first);
     Feed<R> feed = {};
@@ -1289,16 +1284,18 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             prefetch_rows<T, D * KH>(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[1], 0, 4, row0, a.n_cols, lane);
     };
     auto copy = [&](unsigned st, unsigned col) {
-        R::gather(st, qb, qst, gb, dst, col, lane);
+        if constexpr (PACK) R::gather(st, qb, qst, gb, dst, col, lane, times, a.qs[2] * 2, a.ds[2] * 2);
+        else R::gather(st, qb, qst, gb, dst, col, lane);
 #pragma unroll
         for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
             const int jj = KH == 1 ? 0 : j + (lane >> 4);
             if (KH > 1 || lane < 16)
-                cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8, stat + (int64_t)jj * a.n_rows + col);
+                cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8,
+                          stat + (int64_t)(PACK ? lane & ((1 << times) - 1) : jj) * a.n_rows + col);
         }
-        if (KH == 1 && feed.at + 1 == feed.end && fh + 1 < share) {     // the tile again, with its next head
+        if (KH == 1 && feed.at + 1 == feed.end && fh + 1 < groups) {    // the tile again, with its next heads
             ++fh;
-            open_head(fb, fkh * share + fh);
+            open_head(fb, fkh * share + (fh << times));
             feed.at = begin - 1;
         }
     };
@@ -1307,7 +1304,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
     int st_read = 0;
     for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, 1, share);
+        const TileWork w = tile_work(a, now, 1, share, 4);
         Own<D> k[KH], v[DK ? KH : 1];
         Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
@@ -1319,14 +1316,14 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             }
             if constexpr (DV) dv[j].zero();
         }
-        const int n = w.ch1 - w.ch0, steps = n * (KH == 1 ? share : 1);
+        const int n = w.ch1 - w.ch0, steps = n * (KH == 1 ? groups : 1);
         int ci = 0;                                      // chunk of the step
         Chunk<VALS> next;
         float x_next[2][4] = {};
         const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
         if (n > 0) next.load(a.chunks, w.ch0, rows);
         if constexpr (VALS)
-            if (n > 0) next.values(x_next, vals, c);
+            if (n > 0) next.values(x_next, vals, c, times);
         for (int x = 0; x < steps; ++x) {
             unsigned mine[2] = {next.bits[0] >> (2 * c), next.bits[1] >> (2 * c)}, used = 0;
             float val[2][4];
@@ -1347,7 +1344,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, k[j], at, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], at + R::kTensor, g, c);
-                if (VALS && j == 0) next.values(x_next, vals, c);
+                if (VALS && j == 0) next.values(x_next, vals, c, times);
                 const unsigned sp = stage + 2 * R::kTensor + j * 128 + c * 16;
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
@@ -1463,13 +1460,19 @@ sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
     if (what == kTileFwd) return go(tile_forward_kernel<T, D, KH, VALS, false>, row_bytes);
     if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, KH, VALS, false>, row_bytes);
     constexpr int bytes = Ring<D, KH, true>::kBytes;
-    if constexpr (D * KH <= 64) {
-        return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS>, bytes);
-    } else {
-        sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS>, bytes) : SLA_OK;
-        if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS>, bytes);
-        return st;
-    }
+    auto cols_of = [&](auto pack) -> sla_status {
+        constexpr bool PACK = decltype(pack)::value;
+        if constexpr (D * KH <= 64) {
+            return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS, PACK>, bytes);
+        } else {
+            sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS, PACK>, bytes) : SLA_OK;
+            if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS, PACK>, bytes);
+            return st;
+        }
+    };
+    if constexpr (KH == 1)
+        if (a.rows_log < 4) return cols_of(std::true_type{});
+    return cols_of(std::false_type{});
 }
 
 template <typename T>
@@ -1520,7 +1523,7 @@ sla_status launch_tile_of(int what, const AttnArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows, const int32_t *rowptr, const int32_t *colind,
+sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int times, int n_rows, const int32_t *rowptr, const int32_t *colind,
                        cudaStream_t s) {
     const int n = parts.n_items, U = parts.n_units;
     DeviceScratch tmp(s);
@@ -1531,7 +1534,7 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows
         return SLA_ERR_OOM;
     }
     const unsigned grid = blocks_of(((int64_t)n + 1) * 32, 128);
-    tile_columns_kernel<false><<<grid, 128, 0, s>>>(rows, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+    tile_columns_kernel<false><<<grid, 128, 0, s>>>(rows, times, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
                                                     parts.item_seg, count, nullptr, nullptr, nullptr);
     SLA_CHECK_LAUNCH();
     sla_status st = exclusive_scan(count, count, (int64_t)n + 1, ws, s);
@@ -1548,7 +1551,7 @@ sla_status build_tiles(AttnTiles *t, const AttnPlan &parts, int rows, int n_rows
         return SLA_ERR_OOM;
     }
     SLA_CHECK_CUDA(cudaMemsetAsync(t->chunks, 0, (size_t)(total > 0 ? total : 1) * sizeof(TileChunk), s));
-    tile_columns_kernel<true><<<grid, 128, 0, s>>>(rows, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
+    tile_columns_kernel<true><<<grid, 128, 0, s>>>(rows, times, n_rows, rowptr, colind, n, parts.seg_len, parts.item_unit,
                                                    parts.item_seg, nullptr, count, t->chunk0, t->chunks);
     SLA_CHECK_LAUNCH();
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
