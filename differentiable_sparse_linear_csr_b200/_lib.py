@@ -392,10 +392,10 @@ def tensor_list(src, codes, dst=None):
     sla_dtypes `codes`."""
     n = len(src)
     words = [0] * (4 * n)
-    words[0::4] = [t.data_ptr() for t in src]
+    words[0::4] = map(torch.Tensor.data_ptr, src)
     if dst is not None:
-        words[1::4] = [t.data_ptr() for t in dst]
-    words[2::4] = [t.numel() for t in src]
+        words[1::4] = words[0::4] if dst is src else map(torch.Tensor.data_ptr, dst)
+    words[2::4] = map(torch.Tensor.numel, src)
     words[3::4] = codes
     return (ctypes.c_int64 * max(4 * n, 1))(*words)
 

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import math
+import operator
 from dataclasses import dataclass
 
 import torch
@@ -192,6 +193,7 @@ class CSR:
         whose rows do not start on 16 bytes; other strides are used as they are.  Returns o shaped like q.  Sums have a fixed order: equal
         calls give equal bits.
         """
+        scale = None if scale is None else float(scale)
         # what depends on shapes, strides and types alone is checked and laid out once
         key = (q.shape, k.shape, v.shape, q.stride(), k.stride(), v.stride(), q.dtype, k.dtype, v.dtype,
                q.device, k.device, v.device, scale, values is None)
@@ -662,7 +664,8 @@ def _norm_kind(norm_type) -> int:
 
 def _codes(tensors):
     """The tensors' types as the library's, all on one CUDA device."""
-    if any(not t.is_cuda for t in tensors) or len({t.get_device() for t in tensors}) > 1:
+    devices = {t.device for t in tensors}
+    if len(devices) > 1 or devices.pop().type != "cuda":
         raise ValueError("the tensors must be on one CUDA device")
     try:
         return [L.TENSOR_DTYPES[t.dtype] for t in tensors]
@@ -673,6 +676,12 @@ def _codes(tensors):
 def _dense(t: torch.Tensor) -> bool:
     """The elements fill one range of memory, in whatever order."""
     return t.is_contiguous() or torch.ops.aten.is_non_overlapping_and_dense(t)
+
+
+def _dense_list(tensors):
+    if all(map(torch.Tensor.is_contiguous, tensors)):
+        return tensors
+    return [t if _dense(t) else t.detach().contiguous() for t in tensors]
 
 
 def _norm_buffers(codes, device):
@@ -691,7 +700,7 @@ def global_norm(tensors, norm_type: float = 2.0) -> torch.Tensor:
     if not tensors:
         return torch.zeros(())
     codes = _codes(tensors)
-    src = [t if _dense(t) else t.detach().contiguous() for t in tensors]
+    src = _dense_list(tensors)
     with _on_device(tensors[0].device):
         norm, ws = _norm_buffers(codes, tensors[0].device)
         L.sla_global_norm(len(src), L.tensor_list(src, codes), kind, norm, ws)
@@ -719,9 +728,11 @@ def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out
     if not tensors:
         return [], torch.zeros(())
     codes = _codes(tensors)
-    src = [t if _dense(t) else t.detach().contiguous() for t in tensors]
+    src = _dense_list(tensors)
     if outs is None:
-        outs = dst = [torch.empty_like(t) for t in src]
+        outs = dst = list(map(torch.empty_like, src))
+    elif src is tensors and all(map(operator.is_, outs, src)):
+        dst = src
     else:
         # an output laid out otherwise than its input is written by way of a copy
         dst = [o if o is s or (o.stride() == s.stride() and _dense(o)) else torch.empty_like(s)
@@ -729,9 +740,10 @@ def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out
     with _on_device(tensors[0].device):
         norm, ws = _norm_buffers(codes, tensors[0].device)
         L.sla_clip_norm(len(src), L.tensor_list(src, codes, dst), kind, max_norm, norm, ws)
-    for o, d in zip(outs, dst):
-        if o is not d:
-            o.detach().copy_(d)
+    if outs is not dst:
+        for o, d in zip(outs, dst):
+            if o is not d:
+                o.detach().copy_(d)
     return outs, norm
 
 

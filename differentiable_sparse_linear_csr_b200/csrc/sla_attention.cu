@@ -997,6 +997,7 @@ sla_status check_device(const char *fn, const Csr *h) {
     int dev = -1;
     SLA_CHECK_CUDA(cudaGetDevice(&dev));
     SLA_REQUIRE(dev == h->device, "%s: the handle lives on device %d, the current device is %d", fn, h->device, dev);
+    SLA_REQUIRE(h->nnz <= INT_MAX - 64, "%s: nnz=%lld, at most 2^31 - 65", fn, (long long)h->nnz);   // steps beyond a row's end
     return SLA_OK;
 }
 

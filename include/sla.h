@@ -468,7 +468,8 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * not matter), or with NULL what calls of any type with heads == kv_heads need.  Workspaces are 256-byte
  * aligned; calls in flight at the same time need distinct ones.  With 16-bit
  * types and dim a multiple of 16 up to 128, addresses and strides of the head
- * tensors must be multiples of 16 bytes (SLA_ERR_INVALID otherwise).
+ * tensors must be multiples of 16 bytes and row strides below 2^31 elements
+ * (SLA_ERR_INVALID otherwise).  At most 2^31 - 65 entries.
  */
 typedef struct {
     int32_t dtype;            /* sla_dtype of q, k, v, out and their gradients */

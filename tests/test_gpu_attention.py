@@ -265,6 +265,41 @@ def test_gradient_against_differences():
         assert abs(fd - an) < 1e-7 * max(1.0, abs(an)), (x, fd, an)
 
 
+@pytest.mark.parametrize("code", ["f32", "bf16"])
+@pytest.mark.parametrize("n,m", [(0, 5), (3, 0), (0, 0)])
+def test_no_rows_or_no_columns(n, m, code):
+    rp = np.zeros(n + 1, np.int32)
+    A = sla.CSR(T(rp), torch.zeros(0, dtype=torch.int32, device=DEV), n_cols=m, dtype=torch.float32)
+    q = torch.randn(n, 2, 32, device=DEV).to(DT[code]).requires_grad_()
+    k, v = (torch.randn(m, 2, 32, device=DEV).to(DT[code]).requires_grad_() for _ in range(2))
+    vals = torch.zeros(0, device=DEV, requires_grad=True)
+    o = A.attention(q, k, v, vals)
+    assert o.shape == q.shape and not o.any()
+    for g, t in zip(torch.autograd.grad(o, [q, k, v, vals], torch.ones_like(o)), (q, k, v, vals)):
+        assert g.shape == t.shape and not g.any()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements in k and v: the last columns are read where they are."""
+    m, H_, D = 1 << 21, 8, 136                       # 2^31 + 2^27 elements
+    cols = [[0, m - 1], [m - 3], [m - 2, m - 1]]
+    rp, ci, _ = from_rows(cols, m)
+    A = sla.CSR(T(rp), T(ci), n_cols=m, dtype=torch.float32)
+    for width, code in ((D, "bf16"), (128, "bf16")):         # a row kernel, and a tile kernel through the strides
+        store = torch.zeros(m, H_, D, dtype=DT[code], device=DEV)
+        k = store[:, :, :width]
+        near = torch.tensor([0, m - 3, m - 2, m - 1], device=DEV)
+        k[near] = torch.randn(4, H_, width, device=DEV).to(DT[code])
+        q = torch.randn(3, H_, width, device=DEV).to(DT[code])
+        got = H(A.attention(q, k, k))
+        where = {0: 0, m - 3: 1, m - 2: 2, m - 1: 3}
+        rp2, ci2, _ = from_rows([[where[c] for c in r] for r in cols], 4)
+        small = H(k[near])
+        res, err = attention(rp2, ci2, H(q), small, small, None, width ** -0.5, None, code)
+        assert within(got, res["o"], err["o"]) <= 1.0
+        del store, k
+
+
 def test_only_the_asked_gradients():
     A, rp, ci, q, k, v, vals, do = inputs("hub", 1, 2, 1, 64, "bf16", True)
     want = run(A, q, k, v, vals, do)
