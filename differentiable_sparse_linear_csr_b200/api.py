@@ -394,7 +394,8 @@ class _AttentionCall:
             if train:
                 lse = torch.empty(A.batch, A.n_rows, q.shape[-2], dtype=self.wide, device=A.device)
                 wide = torch.empty(out.shape, dtype=self.wide, device=A.device) if q.element_size() == 2 else None
-                L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts, _workspace(room, A.device))
+                L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts,
+                                _workspace(room, A.device) if room else None)
                 return out, wide, lse, q, k, v
             ws = _workspace(room + self.lse, A.device)      # lse behind the workspace proper
             L.sla_attention(A.handle, q, k, v, vals, out, None, None, opts, ws, lse_ptr=ws.data_ptr() + room)

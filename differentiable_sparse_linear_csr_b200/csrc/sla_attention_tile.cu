@@ -35,6 +35,7 @@
 // read as zeros.  If a sum ends as a NaN all the same, the warp redoes its rows
 // entry by entry: a bad number of a column that some rows use would otherwise
 // reach the tile's other rows.
+#include <atomic>
 #include <climits>
 
 #include "sla_attention.cuh"
@@ -752,6 +753,55 @@ struct Feed {
     }
 };
 
+// What the consuming loop needs of the chunks to come, loaded as the feed passes
+// them and so across the pieces of work too: bits and first entries, and with VALS
+// the stored values one chunk ahead.  base: the values of system 0; times: see Chunk.
+template <bool VALS, typename R>
+struct Ahead {
+    static constexpr bool kTwo = R::kStages == 3;        // the feed is two chunks ahead, or one
+    Chunk<VALS> now, c0, c1;                             // the chunk at hand and the next ones
+    float x[2][4], x_next[2][4];
+    int b0, b1;
+
+    template <bool PACK>
+    __device__ __forceinline__ void first(const TileChunk *chunks, int at, int b, const TileRows<PACK> &rows) {
+        c0.load(chunks, at, rows);
+        b0 = b;
+    }
+    template <bool PACK>
+    __device__ __forceinline__ void second(const TileChunk *chunks, int at, int b, const TileRows<PACK> &rows) {
+        c1.load(chunks, at, rows);
+        b1 = b;
+    }
+    __device__ __forceinline__ void start(const float *base, int64_t nnz, int c, int times = 0) {
+        if constexpr (VALS) c0.values(x_next, base + b0 * nnz, c, times);
+    }
+    // Takes the next chunk; then `passed` with the chunk the feed is about to copy.
+    __device__ __forceinline__ void take(const float *base, int64_t nnz, int c, int times = 0) {
+        now = c0;
+        if constexpr (VALS) {
+#pragma unroll
+            for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
+            if constexpr (kTwo) c1.values(x_next, base + b1 * nnz, c, times);
+        }
+        if constexpr (kTwo) {
+            c0 = c1;
+            b0 = b1;
+        }
+    }
+    template <bool PACK>
+    __device__ __forceinline__ void passed(const TileChunk *chunks, int at, int b, const TileRows<PACK> &rows) {
+        if constexpr (kTwo) second(chunks, at, b, rows);
+        else first(chunks, at, b, rows);
+    }
+    // With the feed one chunk ahead the next values are loaded when its bits are there.
+    __device__ __forceinline__ void late(const float *base, int64_t nnz, int c, int times = 0) {
+        if constexpr (VALS && !kTwo) c0.values(x_next, base + b0 * nnz, c, times);
+    }
+};
+
 // Pieces of work of this warp out of `total`.
 __device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, unsigned &stride) {
     first = blockIdx.x * kTileWarps + (threadIdx.x >> 5);
@@ -777,8 +827,10 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     const Stride stride(by, (unsigned)a.n_items, groups, KH, a.kv_heads);
     Cursor now = stride.at(first);
     Feed<R> feed;
-    const char *kb = nullptr, *vb = nullptr;             // of the piece the feed is at
+    const char *kb = nullptr, *vb = nullptr;             // of the piece the feed is at, and its system
+    int fb = 0;
     auto open = [&](const Cursor &f) {
+        fb = f.b;
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
@@ -788,11 +840,20 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     };
     auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    Ahead<VALS, R> meta;
+    meta.first(a.chunks, feed.at, fb, rows);
+    feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    if constexpr (meta.kTwo) {
+        meta.second(a.chunks, feed.at, fb, rows);
+        feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    }
+    meta.start(a.vals_f, a.nnz, c);
     int st_read = 0;
-    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
+    TileWork w_next = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
+    for (unsigned piece = 0; piece < count; ++piece) {
+        const TileWork w = w_next;
+        if (piece + 1 < count) stride.move(now);
+        w_next = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH];
 #pragma unroll
@@ -805,40 +866,16 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             acc[j].zero();
             m[j][0] = m[j][1] = l[j][0] = l[j][1] = 0.0f;
         }
-        Chunk<VALS> next, cur;
-        float x_next[2][4] = {};
-        const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, rows);
-        if constexpr (VALS) {
-            cur = next;
-            if (n > 0) cur.values(x_next, vals, c);
-            if (n > 0) next.load(a.chunks, w.ch0 + min(1, n - 1), rows);
-        }
         for (int ch = 0; ch < n; ++ch) {
-            // bookkeeping of this chunk, and loads of the next one's
-            float x[2][4];
-            unsigned bits[2];
-            if constexpr (VALS) {
-                bits[0] = cur.bits[0];
-                bits[1] = cur.bits[1];
-#pragma unroll
-                for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
-                cur = next;
-                cur.values(x_next, vals, c);
-                next.load(a.chunks, w.ch0 + min(ch + 2, n - 1), rows);
-            } else {
-                bits[0] = next.bits[0];
-                bits[1] = next.bits[1];
-                next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), rows);
-            }
+            meta.take(a.vals_f, a.nnz, c);
             cp_wait<R::kStages - 2>();
             __syncwarp();
+            meta.passed(a.chunks, feed.at, fb, rows);
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
             const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
-            unsigned mine[2] = {bits[0] >> (2 * c), bits[1] >> (2 * c)}, used = 0;
+            const auto &x = meta.x;
+            unsigned mine[2] = {meta.now.bits[0] >> (2 * c), meta.now.bits[1] >> (2 * c)}, used = 0;
             bool drop = false;
             if constexpr (VALS) {
                 bool out = false;                       // a stored pair that a value of -inf leaves out
@@ -852,7 +889,10 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                         }
                 drop = __any_sync(kAll, out);
                 if (drop) {
-                    if (!__any_sync(kAll, (mine[0] | mine[1]) & 0x303u)) continue;      // nothing left
+                    if (!__any_sync(kAll, (mine[0] | mine[1]) & 0x303u)) {              // nothing left
+                        meta.late(a.vals_f, a.nnz, c);
+                        continue;
+                    }
                     used = (mine[0] | mine[1]) & 0x303u;
                     used = (used | used >> 6) & 15u;
                 }
@@ -862,6 +902,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 const unsigned at = stage + (KH == 1 ? 0 : j * (D * 2));
                 float s[2][4], t[2][4], far[2] = {none, none};
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
+                if (j == 0) meta.late(a.vals_f, a.nnz, c);
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
@@ -1050,7 +1091,9 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     Cursor now = stride.at(first);
     Feed<R> feed;
     const char *kb = nullptr, *vb = nullptr;
+    int fb = 0;
     auto open = [&](const Cursor &f) {
+        fb = f.b;
         kb = R::source(static_cast<const T *>(a.k) + f.b * a.ks[0] + f.kh * a.ks[2], a.ks[2] * 2, lane);
         vb = R::source(static_cast<const T *>(a.v) + f.b * a.vs[0] + f.kh * a.vs[2], a.vs[2] * 2, lane);
         const unsigned it = f.item(groups);
@@ -1063,11 +1106,20 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     };
     auto copy = [&](unsigned st, unsigned col) { R::gather(st, kb, kst, vb, vst, col, lane); };
     feed.start(a, now, count, stride, groups, lane, a.n_cols, open);
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    Ahead<VALS, R> meta;
+    meta.first(a.chunks, feed.at, fb, rows);
+    feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    if constexpr (meta.kTwo) {
+        meta.second(a.chunks, feed.at, fb, rows);
+        feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
+    }
+    meta.start(a.vals_f, a.nnz, c);
     int st_read = 0;
-    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
+    TileWork w_next = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
+    for (unsigned piece = 0; piece < count; ++piece) {
+        const TileWork w = w_next;
+        if (piece + 1 < count) stride.move(now);
+        w_next = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH], go[KH];
         float lse[KH][2], delta[KH][2];
@@ -1090,25 +1142,16 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             }
         }
         float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
-        Chunk<VALS> next, cur;
-        float x_next[2][4] = {};
-        const float *vals = VALS ? a.vals_f + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, rows);
-        if constexpr (VALS)
-            if (n > 0) next.values(x_next, vals, c);
         for (int ch = 0; ch < n; ++ch) {
-            cur = next;
-            float x[2][4];
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[blk][e] = x_next[blk][e];
-            next.load(a.chunks, w.ch0 + min(ch + 1, n - 1), rows);
+            meta.take(a.vals_f, a.nnz, c);
             cp_wait<R::kStages - 2>();
             __syncwarp();
+            meta.passed(a.chunks, feed.at, fb, rows);
             feed.advance(a, stride, groups, lane, a.n_cols, ring, open, copy);
             const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
+            const auto &x = meta.x;
+            const Chunk<VALS> &cur = meta.now;
             const unsigned there[2] = {cur.bits[0] >> (2 * c), cur.bits[1] >> (2 * c)};
             unsigned mine[2] = {there[0], there[1]}, used = 0;
             bool drop = false;
@@ -1134,7 +1177,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
                 score_products<T, D, R::kPitch>(dp, go[j], at + R::kTensor, g, c);
-                if (VALS && j == 0) next.values(x_next, vals, c);
+                if (j == 0) meta.late(a.vals_f, a.nnz, c);
                 const unsigned on[2] = {mine[0] & live[j][0], mine[1] & live[j][1]};
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
@@ -1300,11 +1343,20 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         }
     };
     feed.start(a, now, count, stride, 1, lane, a.n_rows, open);
-#pragma unroll
-    for (int i = 0; i < R::kStages - 1; ++i) feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
+    Ahead<VALS, R> meta;
+    meta.first(a.chunks, feed.at, fb, rows);
+    feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
+    if constexpr (meta.kTwo) {
+        meta.second(a.chunks, feed.at, fb, rows);
+        feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
+    }
+    meta.start(a.vals_t, a.nnz, c, times);
     int st_read = 0;
-    for (unsigned piece = 0; piece < count; ++piece, stride.move(now)) {
-        const TileWork w = tile_work(a, now, 1, share, 4);
+    TileWork w_next = tile_work(a, now, 1, share, 4);
+    for (unsigned piece = 0; piece < count; ++piece) {
+        const TileWork w = w_next;
+        if (piece + 1 < count) stride.move(now);
+        w_next = tile_work(a, now, 1, share, 4);
         Own<D> k[KH], v[DK ? KH : 1];
         Sums<T, D> dk[DK ? KH : 1], dv[DV ? KH : 1];
 #pragma unroll
@@ -1317,34 +1369,23 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
             if constexpr (DV) dv[j].zero();
         }
         const int n = w.ch1 - w.ch0, steps = n * (KH == 1 ? groups : 1);
-        int ci = 0;                                      // chunk of the step
-        Chunk<VALS> next;
-        float x_next[2][4] = {};
-        const float *vals = VALS ? a.vals_t + w.b * a.nnz : nullptr;
-        if (n > 0) next.load(a.chunks, w.ch0, rows);
-        if constexpr (VALS)
-            if (n > 0) next.values(x_next, vals, c, times);
         for (int x = 0; x < steps; ++x) {
-            unsigned mine[2] = {next.bits[0] >> (2 * c), next.bits[1] >> (2 * c)}, used = 0;
-            float val[2][4];
-#pragma unroll
-            for (int blk = 0; blk < 2; ++blk)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) val[blk][e] = x_next[blk][e];
-            ci = ci + 1 == n ? 0 : ci + 1;
-            next.load(a.chunks, w.ch0 + ci, rows);
+            meta.take(a.vals_t, a.nnz, c, times);
             cp_wait<R::kStages - 2>();
             __syncwarp();
+            meta.passed(a.chunks, feed.at, fb, rows);
             feed.advance(a, stride, 1, lane, a.n_rows, ring, open, copy);
             const unsigned stage = ring + st_read;
             st_read = st_read == (R::kStages - 1) * R::kStage ? 0 : st_read + R::kStage;
+            unsigned mine[2] = {meta.now.bits[0] >> (2 * c), meta.now.bits[1] >> (2 * c)}, used = 0;
+            const auto &val = meta.x;
 #pragma unroll
             for (int j = 0; j < KH; ++j) {
                 const unsigned at = stage + j * (D * 2);
                 float s[2][4], dp[2][4];
                 score_products<T, D, R::kPitch>(s, k[j], at, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], at + R::kTensor, g, c);
-                if (VALS && j == 0) next.values(x_next, vals, c, times);
+                if (j == 0) meta.late(a.vals_t, a.nnz, c, times);
                 const unsigned sp = stage + 2 * R::kTensor + j * 128 + c * 16;
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
@@ -1430,6 +1471,31 @@ sla_status tile_values(const AttnArgs &a, const int32_t *perm, float *out, cudaS
 // -------------------------------------------------------------- launches ----
 enum { kTileFwd, kTileBwdRows, kTileBwdCols };
 
+// As many blocks as run at once, each warp going through the work in strides.  How
+// many that is, is asked once a kernel and device.
+template <auto KERNEL>
+sla_status launch_stream(const AttnArgs &a, int64_t total, int ring, cudaStream_t s) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> resident[kDevices];
+    const int bytes = ring * kTileWarps;
+    int dev = 0;
+    SLA_CHECK_CUDA(cudaGetDevice(&dev));
+    if (bytes > 48 * 1024)
+        SLA_CHECK_CUDA(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    int most = dev < kDevices ? resident[dev].load(std::memory_order_acquire) : 0;
+    if (most == 0) {
+        int per_sm = 0, sms = 0;
+        SLA_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, KERNEL, kTileThreads, bytes));
+        SLA_CHECK_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+        most = (per_sm > 0 ? per_sm : 1) * sms;
+        if (dev < kDevices) resident[dev].store(most, std::memory_order_release);
+    }
+    const int64_t blocks = (total + kTileWarps - 1) / kTileWarps;
+    KERNEL<<<(unsigned)(blocks < most ? blocks : most), kTileThreads, bytes, s>>>(a, (unsigned)total);
+    SLA_CHECK_LAUNCH();
+    return SLA_OK;
+}
+
 // KH key heads a warp.
 template <typename T, int D, int KH, bool VALS>
 sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
@@ -1438,35 +1504,21 @@ sla_status launch_tile(int what, const AttnArgs &a, cudaStream_t s) {
                           (a.kv_heads / KH);
     SLA_REQUIRE(total < INT_MAX, "sla_attention: too many rows, systems and heads");
     if (total == 0) return SLA_OK;
-    // as many blocks as run at once, each warp going through the work in strides
-    auto go = [&](auto *kernel, int ring) -> sla_status {
-        const int bytes = ring * kTileWarps;
-        if (bytes > 48 * 1024)
-            SLA_CHECK_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-        int per_sm = 0, dev = 0, sms = 0;
-        SLA_CHECK_CUDA(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kTileThreads, bytes));
-        SLA_CHECK_CUDA(cudaGetDevice(&dev));
-        SLA_CHECK_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-        const int64_t blocks = (total + kTileWarps - 1) / kTileWarps, most = (int64_t)(per_sm > 0 ? per_sm : 1) * sms;
-        kernel<<<(unsigned)(blocks < most ? blocks : most), kTileThreads, bytes, s>>>(a, (unsigned)total);
-        SLA_CHECK_LAUNCH();
-        return SLA_OK;
-    };
     constexpr int row_bytes = Ring<D, KH, false>::kBytes;
     if constexpr (KH == 1) {
-        if (what == kTileFwd && a.rows_log < 4) return go(tile_forward_kernel<T, D, 1, VALS, true>, row_bytes);
-        if (what == kTileBwdRows && a.rows_log < 4) return go(tile_bwd_rows_kernel<T, D, 1, VALS, true>, row_bytes);
+        if (what == kTileFwd && a.rows_log < 4) return launch_stream<tile_forward_kernel<T, D, 1, VALS, true>>(a, total, row_bytes, s);
+        if (what == kTileBwdRows && a.rows_log < 4) return launch_stream<tile_bwd_rows_kernel<T, D, 1, VALS, true>>(a, total, row_bytes, s);
     }
-    if (what == kTileFwd) return go(tile_forward_kernel<T, D, KH, VALS, false>, row_bytes);
-    if (what == kTileBwdRows) return go(tile_bwd_rows_kernel<T, D, KH, VALS, false>, row_bytes);
+    if (what == kTileFwd) return launch_stream<tile_forward_kernel<T, D, KH, VALS, false>>(a, total, row_bytes, s);
+    if (what == kTileBwdRows) return launch_stream<tile_bwd_rows_kernel<T, D, KH, VALS, false>>(a, total, row_bytes, s);
     constexpr int bytes = Ring<D, KH, true>::kBytes;
     auto cols_of = [&](auto pack) -> sla_status {
         constexpr bool PACK = decltype(pack)::value;
         if constexpr (D * KH <= 64) {
-            return go(tile_bwd_cols_kernel<T, D, KH, true, true, VALS, PACK>, bytes);
+            return launch_stream<tile_bwd_cols_kernel<T, D, KH, true, true, VALS, PACK>>(a, total, bytes, s);
         } else {
-            sla_status st = a.dv ? go(tile_bwd_cols_kernel<T, D, KH, false, true, VALS, PACK>, bytes) : SLA_OK;
-            if (st == SLA_OK && a.dk) st = go(tile_bwd_cols_kernel<T, D, KH, true, false, VALS, PACK>, bytes);
+            sla_status st = a.dv ? launch_stream<tile_bwd_cols_kernel<T, D, KH, false, true, VALS, PACK>>(a, total, bytes, s) : SLA_OK;
+            if (st == SLA_OK && a.dk) st = launch_stream<tile_bwd_cols_kernel<T, D, KH, true, false, VALS, PACK>>(a, total, bytes, s);
             return st;
         }
     };
