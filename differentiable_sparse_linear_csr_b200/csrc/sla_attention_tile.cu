@@ -312,14 +312,17 @@ struct Own {
 // the columns 8 blk + (2c, 2c + 1) of rows g and g + 8 in this thread.
 template <typename T, int D, int PITCH>
 __device__ __forceinline__ void score_products(float (&s)[2][4], const Own<D> &own, unsigned stage, int g, int c) {
+    // the halves alternate, so that a product does not wait for the one before it
+    uint32_t k[2][D / 8];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-        uint32_t k[D / 8];
-        read_score<D>(k, stage + g * PITCH + 8 * blk * PITCH, c);
+        read_score<D>(k[blk], stage + g * PITCH + 8 * blk * PITCH, c);
         s[blk][0] = s[blk][1] = s[blk][2] = s[blk][3] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) mma16<T>(s[blk], own.a[i], k[2 * i], k[2 * i + 1]);
     }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) mma16<T>(s[blk], own.a[i], k[blk][2 * i], k[blk][2 * i + 1]);
 }
 
 // Zeros for the gathered rows of the columns that no row of the tile uses; used:
@@ -365,16 +368,24 @@ struct Sums {
             else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(v[i]));
             lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i]));
         }
+        // four blocks at a time, the second parts after the first ones
+        constexpr int W = D / 16, G = W % 2 == 0 ? 2 : 1;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            uint32_t a0, a1, b0, b1;
-            widen<T>(x0[i], a0, a1);
-            widen<T>(x1[i], b0, b1);
-            mma_tf32(o[2 * i], hi, a0, b0);
-            mma_tf32(o[2 * i + 1], hi, a1, b1);
+        for (int j = 0; j < W; j += G) {
+            uint32_t y[G][4];
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                widen<T>(x0[j + i], y[i][0], y[i][1]);
+                widen<T>(x1[j + i], y[i][2], y[i][3]);
+                mma_tf32(o[2 * (j + i)], hi, y[i][0], y[i][2]);
+                mma_tf32(o[2 * (j + i) + 1], hi, y[i][1], y[i][3]);
+            }
             if (two) {
-                mma_tf32(o[2 * i], lo, a0, b0);
-                mma_tf32(o[2 * i + 1], lo, a1, b1);
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    mma_tf32(o[2 * (j + i)], lo, y[i][0], y[i][2]);
+                    mma_tf32(o[2 * (j + i) + 1], lo, y[i][1], y[i][3]);
+                }
             }
         }
     }
