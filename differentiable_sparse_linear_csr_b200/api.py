@@ -167,7 +167,9 @@ class CSR:
         """Build the work plan of ``attention`` (and, with ``backward``, A^T's
         pattern and plan) now instead of at the first call: needed before the
         calls are captured into a CUDA graph.  heads_per_key: H // K of the calls.
-        Synchronises the host."""
+        Synchronises the host.  A captured backward pass also needs that no graph of
+        the same leaves made outside the capture is still alive (drop the warm-up's
+        outputs): autograd would tie the capture to that graph's stream."""
         if heads_per_key < 1:
             raise ValueError("heads_per_key must be positive")
         with _on_device(self.device):
@@ -190,8 +192,9 @@ class CSR:
         an entry whose value is -inf is left out, whatever its k and v hold.  A
         row with no entry left gives zeros.  scale defaults to D ** -0.5.  A tensor's
         last dimension is copied if it is not contiguous, and in 16 bits a tensor
-        whose rows do not start on 16 bytes; other strides are used as they are.  Returns o shaped like q.  Sums have a fixed order: equal
-        calls give equal bits.
+        whose rows do not start on 16 bytes; other strides are used as they are.
+        Returns o shaped like q.  Sums have a fixed order: equal calls give equal
+        bits.
         """
         scale = None if scale is None else float(scale)
         # what depends on shapes, strides and types alone is checked and laid out once
@@ -741,6 +744,8 @@ def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out
     with _on_device(tensors[0].device):
         norm, ws = _norm_buffers(codes, tensors[0].device)
         L.sla_clip_norm(len(src), L.tensor_list(src, codes, dst), kind, max_norm, norm, ws)
+    if out is not None:                          # for autograd graphs that saved them
+        torch.autograd.graph.increment_version(outs)
     if outs is not dst:
         for o, d in zip(outs, dst):
             if o is not d:

@@ -170,3 +170,15 @@ def test_refusals():
     # the same input twice is two gradients, with an output each
     outs, norm = sla.clip_by_global_norm([ts[0], ts[0]], 1.0)
     check([ts[0], ts[0]], outs, norm, 1.0)
+
+
+def test_writing_counts_as_a_change():
+    """A tensor that autograd saved and clipping overwrote is refused by the backward pass."""
+    x = torch.ones(5, device=DEV)
+    w = torch.ones(5, device=DEV, requires_grad=True)
+    y = (x * w).sum()
+    sla.clip_by_global_norm([x], 1.0)                  # new outputs: x is as it was
+    torch.autograd.grad(y, w, retain_graph=True)
+    sla.clip_by_global_norm([x], 1.0, out=[x])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(y, w)
