@@ -6,6 +6,9 @@
 // arguments, so a call needs no copy and can be captured.  Pass 1 leaves one
 // partial result a block in the workspace; every block of pass 2 adds them up
 // in the same fixed order, so equal calls give equal bits without atomics.
+// 200 M float32 elements: norm 117 us (6.8 TB/s), scaling 264 us (6.1 TB/s); 62
+// tensors of odd sizes, 12 M elements: 10 and 13 us.  Pass 2 walks the chunks
+// backwards: what pass 1 read last is still in L2.
 // Squares are summed in 64 bits whatever the type: the square of a 32-bit or
 // bfloat16 number need not be one.
 #include <cuda_bf16.h>
@@ -30,14 +33,16 @@ constexpr int kMaxPartials = 2048;
 
 enum { kNormL2 = 0, kNormMax = 1 };
 
-template <int N>
+// What one launch takes (its arguments: a call with two tensors pays nothing for the
+// unused ones).
+constexpr int kTable = 256;
 struct Table {
     int n;
-    unsigned chunk0[N + 1];    // first chunk of each tensor
-    const void *src[N];
-    void *dst[N];
-    int64_t count[N];
-    uint8_t dtype[N];
+    unsigned chunk0[kTable + 1];    // first chunk of each tensor
+    const void *src[kTable];
+    void *dst[kTable];
+    int64_t count[kTable];
+    uint8_t dtype[kTable];
 };
 
 template <typename T> __device__ __forceinline__ double wide(T x) {
@@ -110,8 +115,7 @@ __device__ __forceinline__ double block_join(double v, double *red) {
     return s;
 }
 
-template <int N>
-__device__ __forceinline__ int tensor_of(const Table<N> &t, unsigned chunk) {
+__device__ __forceinline__ int tensor_of(const Table &t, unsigned chunk) {
     int lo = 0, hi = t.n - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -121,8 +125,8 @@ __device__ __forceinline__ int tensor_of(const Table<N> &t, unsigned chunk) {
     return lo;
 }
 
-template <int KIND, int N>
-__device__ __forceinline__ double table_norm(const Table<N> &t, unsigned first, unsigned stride) {
+template <int KIND>
+__device__ __forceinline__ double table_norm(const Table &t, unsigned first, unsigned stride) {
     double s = 0.0;
     for (unsigned c = first; c < t.chunk0[t.n]; c += stride) {
         const int k = tensor_of(t, c);
@@ -140,8 +144,8 @@ __device__ __forceinline__ double table_norm(const Table<N> &t, unsigned first, 
     return s;
 }
 
-template <int KIND, int N>
-__global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const __grid_constant__ Table<N> t, double *part) {
+template <int KIND>
+__global__ void __launch_bounds__(kNormThreads) norm_partial_kernel(const __grid_constant__ Table t, double *part) {
     __shared__ double red[kNormThreads / 32];
     const double s = block_join<KIND>(table_norm<KIND>(t, blockIdx.x, gridDim.x), red);
     if (threadIdx.x == 0) part[blockIdx.x] = s;
@@ -216,8 +220,7 @@ __device__ __forceinline__ void chunk_scale(const T *p, T *q, int64_t count, int
 
 // The chunks in the reverse of pass 1's order: the last ones read are the ones
 // still in L2.
-template <int N>
-__device__ __forceinline__ void table_scale(const Table<N> &t, unsigned first, unsigned stride, double f) {
+__device__ __forceinline__ void table_scale(const Table &t, unsigned first, unsigned stride, double f) {
     const unsigned n = t.chunk0[t.n];
     for (unsigned i = first; i < n; i += stride) {
         const unsigned c = n - 1 - i;
@@ -239,9 +242,9 @@ __device__ __forceinline__ double clip_factor(double norm, double max_norm) {
     return f > 1.0 ? 1.0 : f;                       // a NaN norm gives a NaN factor
 }
 
-template <int KIND, int N>
+template <int KIND>
 __global__ void __launch_bounds__(kNormThreads)
-clip_scale_kernel(const __grid_constant__ Table<N> t, const double *part, int n_part, double max_norm, void *norm,
+clip_scale_kernel(const __grid_constant__ Table t, const double *part, int n_part, double max_norm, void *norm,
                   int f64) {
     __shared__ double red[kNormThreads / 32];
     const double v = total_norm<KIND>(part, n_part, red);
@@ -250,9 +253,9 @@ clip_scale_kernel(const __grid_constant__ Table<N> t, const double *part, int n_
 }
 
 // Both passes of a short list in one block: one launch, nothing to join.
-template <int KIND, int N>
+template <int KIND>
 __global__ void __launch_bounds__(kNormThreads)
-clip_small_kernel(const __grid_constant__ Table<N> t, double max_norm, void *norm, int f64) {
+clip_small_kernel(const __grid_constant__ Table t, double max_norm, void *norm, int f64) {
     __shared__ double red[kNormThreads / 32];
     double v = block_join<KIND>(table_norm<KIND>(t, 0, 1), red);
     if (KIND == kNormL2) v = sqrt(v);
@@ -260,12 +263,11 @@ clip_small_kernel(const __grid_constant__ Table<N> t, double max_norm, void *nor
     if (max_norm >= 0.0) table_scale(t, 0, 1, clip_factor(v, max_norm));
 }
 
-template <int N>
-int fill(Table<N> &t, const sla_tensor *list, int from, int n) {
+int fill(Table &t, const sla_tensor *list, int from, int n) {
     t.n = 0;
     t.chunk0[0] = 0;
     int i = from;
-    for (; i < n && t.n < N; ++i) {
+    for (; i < n && t.n < kTable; ++i) {
         if (list[i].count == 0) continue;
         const int64_t size = list[i].dtype == SLA_F64 ? 8 : (list[i].dtype == SLA_F32 ? 4 : 2);
         const int64_t chunks = (list[i].count * size + kChunkBytes - 1) / kChunkBytes;
@@ -286,17 +288,19 @@ int num_sms() {
     return n;
 }
 
-// Chunks that one block takes faster than two launches would.
-constexpr int kSmallChunks = 8;
+// Chunks that one block takes as fast as two launches would, or faster (clipping 1, 2,
+// 4 and 8 chunks of float32: 2.2, 2.9, 4.6 and 7.3 us against 4.0 to 4.4; a call's
+// launch on the host 4 us less).
+constexpr int kSmallChunks = 4;
 
 // Pass 1 over the list, tables of N tensors at a time; then the norm alone, or
 // pass 2.  Partial results: at most kMaxPartials a table.
-template <int KIND, int N>
+template <int KIND>
 sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, void *norm, int f64, double *part,
                     cudaStream_t s) {
-    Table<N> t;
+    Table t;
     if (fill(t, list, 0, n) == n && t.chunk0[t.n] <= (unsigned)kSmallChunks) {
-        clip_small_kernel<KIND, N><<<1, kNormThreads, 0, s>>>(t, clip ? max_norm : -1.0, norm, f64);
+        clip_small_kernel<KIND><<<1, kNormThreads, 0, s>>>(t, clip ? max_norm : -1.0, norm, f64);
         SLA_CHECK_LAUNCH();
         return SLA_OK;
     }
@@ -306,7 +310,7 @@ sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, v
         i = fill(t, list, i, n);
         if (t.n == 0) break;
         const unsigned grid = std::min(t.chunk0[t.n], most);
-        norm_partial_kernel<KIND, N><<<grid, kNormThreads, 0, s>>>(t, part + n_part);
+        norm_partial_kernel<KIND><<<grid, kNormThreads, 0, s>>>(t, part + n_part);
         SLA_CHECK_LAUNCH();
         n_part += (int)grid;
     }
@@ -320,24 +324,14 @@ sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, v
         i = fill(t, list, i, n);
         if (t.n == 0) break;
         const unsigned grid = std::min(t.chunk0[t.n], most);
-        clip_scale_kernel<KIND, N><<<grid, kNormThreads, 0, s>>>(t, part, n_part, max_norm, first ? norm : nullptr, f64);
+        clip_scale_kernel<KIND><<<grid, kNormThreads, 0, s>>>(t, part, n_part, max_norm, first ? norm : nullptr, f64);
         SLA_CHECK_LAUNCH();
         first = false;
     }
     return SLA_OK;
 }
 
-constexpr int kSmallTable = 16, kLargeTable = 256;
-
-template <int KIND>
-sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, void *norm, int f64, double *part,
-                    cudaStream_t s) {
-    // the kernel's arguments are copied at every launch: few tensors, few bytes
-    if (n <= kSmallTable) return run_norm<KIND, kSmallTable>(list, n, clip, max_norm, norm, f64, part, s);
-    return run_norm<KIND, kLargeTable>(list, n, clip, max_norm, norm, f64, part, s);
-}
-
-size_t norm_ws(int64_t n) { return align_up((size_t)(n / kLargeTable + 1) * kMaxPartials * sizeof(double)); }
+size_t norm_ws(int64_t n) { return align_up((size_t)(n / kTable + 1) * kMaxPartials * sizeof(double)); }
 
 int64_t bytes_of(const sla_tensor &t) {
     return t.count * (t.dtype == SLA_F64 ? 8 : (t.dtype == SLA_F32 ? 4 : 2));
