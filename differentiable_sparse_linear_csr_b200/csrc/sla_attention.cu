@@ -8,6 +8,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <initializer_list>
 #include <new>
 #include <utility>
@@ -28,13 +29,14 @@ __global__ void unit_len_kernel(int n_rows, int rows, int n_units, const int32_t
     len[u] = (unsigned)m;
 }
 
-// Segments, slots (segments of split units) and split units of every unit.
-__global__ void unit_split_kernel(int n_units, int seg_len, const unsigned *__restrict__ len, unsigned *nseg,
+// Segments, slots (segments of split units) and split units of every unit; units up
+// to `whole` are not split.
+__global__ void unit_split_kernel(int n_units, int seg_len, int whole, const unsigned *__restrict__ len, unsigned *nseg,
                                   unsigned *slots, unsigned *multi, unsigned *most) {
     const int u = blockIdx.x * blockDim.x + threadIdx.x;
     if (u > n_units) return;
     unsigned n = 0;
-    if (u < n_units) n = max(1u, (len[u] + seg_len - 1) / seg_len);
+    if (u < n_units) n = len[u] <= (unsigned)whole ? 1u : (len[u] + seg_len - 1) / seg_len;
     nseg[u] = n;
     slots[u] = n > 1 ? n : 0;
     multi[u] = n > 1 ? 1 : 0;
@@ -85,9 +87,13 @@ __global__ void tile_len_kernel(int n_units, const int32_t *__restrict__ chunk0,
 
 // Items of units with the lengths len (device, [n_units + 1]).  seg_len > 0: a
 // given segment length; else one that makes about `fill` items when the units
-// are few, and at least `least`.
-sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, const int32_t *chunk0,
-                       cudaStream_t s) {
+// are few, at least `least`, and at least the root of a 16th of the longest unit:
+// a segment is walked alone, then the unit's segments are joined by one block, 16
+// warps taking 4 at a time.  (One row of 65536 entries, a head of 64 elements: 31 us,
+// 41 with the root of a 64th, 33 of an 8th; 67 without, and for tiles 47 -> 21.)
+// Units up to `whole`, or `share` items' share of the work, are not split.
+sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, int least, int whole, int share,
+                       const int32_t *chunk0, cudaStream_t s) {
     const int U = p->n_units;
     DeviceScratch tmp(s);
     unsigned *nseg = tmp.get<unsigned>((size_t)U + 1), *slots = tmp.get<unsigned>((size_t)U + 1),
@@ -99,26 +105,35 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
         return SLA_ERR_OOM;
     }
     sla_status st;
-    if (seg_len <= 0) {
+    const bool chosen = seg_len <= 0;
+    if (chosen) {
         unsigned total = 0;
         st = exclusive_scan(len, nseg, (int64_t)U + 1, ws, s);
         if (st != SLA_OK) return st;
         SLA_CHECK_CUDA(cudaMemcpyAsync(&total, nseg + U, sizeof total, cudaMemcpyDeviceToHost, s));
         SLA_CHECK_CUDA(cudaStreamSynchronize(s));
-        seg_len = (int)std::max<int64_t>(least, ((int64_t)total + fill - 1) / fill);
+        const int64_t mean = ((int64_t)total + fill - 1) / fill;
+        seg_len = (int)std::max<int64_t>(least, mean);
+        whole = (int)std::min<int64_t>(INT_MAX, std::max<int64_t>(whole, mean * share));
     }
-    p->seg_len = seg_len;
-    SLA_CHECK_CUDA(cudaMemsetAsync(most, 0, sizeof(unsigned), s));
-    unit_split_kernel<<<blocks_of((int64_t)U + 1), 256, 0, s>>>(U, seg_len, len, nseg, slots, multi, most);
-    SLA_CHECK_LAUNCH();
     unsigned *vec[3] = {nseg, slots, multi};
     unsigned tot[4] = {0, 0, 0, 1};
+    for (int pass = 0;; ++pass) {
+        SLA_CHECK_CUDA(cudaMemsetAsync(most, 0, sizeof(unsigned), s));
+        unit_split_kernel<<<blocks_of((int64_t)U + 1), 256, 0, s>>>(U, seg_len, whole, len, nseg, slots, multi, most);
+        SLA_CHECK_LAUNCH();
+        SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[3], most, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
+        SLA_CHECK_CUDA(cudaStreamSynchronize(s));
+        const int root = (int)std::sqrt((double)tot[3] * seg_len / 16.0);
+        if (!chosen || pass > 0 || root <= seg_len) break;
+        seg_len = root;
+    }
+    p->seg_len = seg_len;
     for (int i = 0; i < 3; ++i) {
         st = exclusive_scan(vec[i], vec[i], (int64_t)U + 1, ws, s);
         if (st != SLA_OK) return st;
         SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[i], vec[i] + U, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
     }
-    SLA_CHECK_CUDA(cudaMemcpyAsync(&tot[3], most, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
     SLA_CHECK_CUDA(cudaStreamSynchronize(s));
     p->n_items = (int32_t)tot[0];
     p->n_slots = (int32_t)tot[1];
@@ -140,11 +155,22 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
     return SLA_OK;
 }
 
-// Enough items to fill the GPU when there are few units (8 an SM), but none
-// shorter than 64 entries or columns: a shorter one spends more on its partial
-// result than on its entries.  A level counts on 8 times as many systems and
-// heads as the one before, so it splits 8 times less.
-int64_t fill_of(const Csr *h, int level) { return std::max<int64_t>(1, (int64_t)h->num_sms * 8 >> (3 * level)); }
+// Enough items to fill the GPU when there are few units: 8 tiles an SM, a warp each,
+// or 128 rows, a few lanes each.  A level counts on 8 times as many systems and heads
+// as the one before, so it splits 8 times less.  Rows up to kWhole entries, or 5 items'
+// share of the work, are not split, nor tiles up to kWhole columns: a short part
+// spends more on its partial result than on its entries.  Measured, forward pass:
+//   tiles, 24 an SM against 8: 300 rows over 1500 columns, 64 systems and heads,
+//   107 -> 116 us and a join of 26; 513 rows of 256 entries, 2 key heads of 128
+//   elements, 26 -> 30 us;
+//   rows, float32, 8, 64 and 128 an SM: 30000 rows of 20 entries and one of 20000, 8
+//   heads of 32, 1150, 205 and 137 us; 64 full rows over 4096 columns, 292, 60 and 45 us;
+//   rows whole up to 8 shares against 5: 513 rows of 256 entries, 8 heads of 32, 67
+//   against 46 us; up to 64 entries alone: 4000 rows of 100, a head of 64, 29 against 22.
+int64_t fill_of(const Csr *h, int level, bool tiled) {
+    return std::max<int64_t>(1, (int64_t)h->num_sms * (tiled ? 8 : 128) >> (3 * level));
+}
+constexpr int kWhole = 64;
 
 constexpr int kRowKind = -1;             // plans of rows, not tiles
 
@@ -164,9 +190,8 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
     p->rows = tiled ? kTileRows >> (transposed ? 0 : kind) : 1;
     p->n_units = (n + p->rows - 1) / p->rows;
     const int U = p->n_units;
-    constexpr int kLeast = 64;           // entries of a row, columns of a tile
     // no row that any level would split (the lengths of A's rows are known)
-    if (U == 0 || (!tiled && !transposed && h->row_max <= kLeast)) {
+    if (U == 0 || (!tiled && !transposed && h->row_max <= kWhole)) {
         p->n_items = U;
         p->built = true;
         return SLA_OK;
@@ -197,7 +222,7 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
             // columns are gathered by parts of 256 entries of a tile's longest row
             AttnPlan parts;
             parts.n_units = U;
-            st = build_items(&parts, len, 256, 0, 0, nullptr, s);
+            st = build_items(&parts, len, 256, 0, 0, 0, 0, nullptr, s);
             if (st == SLA_OK) st = build_tiles(tiles, parts, p->rows, transposed ? 1 << kind : 1, n, rowptr, colind, s);
             free_plan(&parts);
             if (st != SLA_OK) return st;
@@ -205,7 +230,8 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
         tile_len_kernel<<<grid, 256, 0, s>>>(U, tiles->chunk0, len);
         SLA_CHECK_LAUNCH();
     }
-    st = build_items(p, len, 0, fill_of(h, level), tiled ? kLeast / 16 : kLeast, tiled ? tiles->chunk0 : nullptr, s);
+    if (tiled) st = build_items(p, len, 0, fill_of(h, level, true), kWhole / 16, kWhole / 16, 1, tiles->chunk0, s);
+    else st = build_items(p, len, 0, fill_of(h, level, false), kWhole / 4, kWhole, 5, nullptr, s);
     if (st == SLA_OK) p->built = true;
     return st;
 }
@@ -270,8 +296,11 @@ void free_attn_plans(Csr *h) {
 // (i * L + l) * VEC + e of the head.  Neighbouring groups take neighbouring
 // heads, so a warp reads consecutive memory of a gathered row.  The entries of
 // the item are walked STEP at a time with their loads issued together.
-// Bound by the gathers (2 * dim elements an entry and head) and, for short rows,
-// by the instructions around them.
+// Bound by the gathers (2 * dim elements an entry and head, mostly from L1 and L2)
+// and, for short rows, by the instructions around them.  128 systems of a 32 x 32
+// grid, 4 heads of 32 float32 elements (67 MB a tensor): forward 97 us, dq and the
+// stored (p, ds) 140 us, dk and dv 96 us, 2.8 to 3.0 TB/s of the bytes that cannot
+// be left out.
 namespace {
 
 constexpr int kAttnThreads = 128;
@@ -310,7 +339,7 @@ __device__ __forceinline__ bool load_item(Item &r, const AttnArgs &a, unsigned y
         const int64_t end = begin + a.seg_len;
         r.slot = __ldg(a.item_slot + it);
         r.t0 = (int)begin;
-        r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);
+        if (r.slot >= 0) r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);    // whole rows may be longer
     }
     return true;
 }
@@ -781,18 +810,25 @@ attn_dvals_kernel(int64_t count, int heads, const A *__restrict__ pds, V *__rest
 
 }  // namespace
 
-// One warp a joined row while segments are few (one batch of loads each), else 8.
-constexpr int kJoinFew = 16;
+// Warps a joined row: one while segments are few (one batch of loads each) and the
+// rows many (513 rows of 256 entries, 8 query heads of 128: forward 37 us, 58 with
+// 8), else 8 (one row of 1024 entries: 9.8 us, 11.6 with 1), and 16 where a few rows
+// have many segments (one row of 4096 entries, 8 heads of 64: 11.7 us, 13.9 with 8; the
+// 125 tiles of 2000 rows 20.2, 32.8 with 16).  Sums without a softmax take 8: 16 were
+// no faster.
+int join_warps(int64_t blocks, int most_segs) {
+    if (blocks > 1024) return most_segs <= 16 ? 1 : 8;
+    return most_segs <= 64 ? 8 : 16;
+}
 
 template <typename T>
 sla_status attn_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t s) {
     const int64_t blocks = (int64_t)a.batch * p.n_multi * p.rows * a.heads;
     SLA_REQUIRE(blocks < INT_MAX, "sla_attention: too many split rows, systems and heads");
     if (blocks == 0) return SLA_OK;
-    if (p.most_segs <= kJoinFew)
-        attn_join_kernel<T, 1><<<(unsigned)blocks, 32, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit, p.multi_slot);
-    else
-        attn_join_kernel<T, 8><<<(unsigned)blocks, 256, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit, p.multi_slot);
+    const int warps = join_warps(blocks, p.most_segs);
+    auto *kernel = warps == 1 ? attn_join_kernel<T, 1> : (warps == 8 ? attn_join_kernel<T, 8> : attn_join_kernel<T, 16>);
+    kernel<<<(unsigned)blocks, 32 * warps, 0, s>>>(a, p.rows, p.n_multi, p.multi_unit, p.multi_slot);
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }
@@ -805,12 +841,10 @@ sla_status attn_join_sums(const AttnArgs &a, const AttnPlan &p, int n_rows, int 
     if (blocks == 0) return SLA_OK;
     const auto *part = static_cast<const typename AccOf<T>::type *>(a.part);
     T *o0 = static_cast<T *>(out0), *o1 = static_cast<T *>(out1);
-    if (p.most_segs <= kJoinFew)
-        attn_join_sums_kernel<T, 1><<<(unsigned)blocks, 32, 0, s>>>(part, n_rows, p.n_slots, p.rows, heads, a.dim, width,
-                                                                    p.n_multi, p.multi_unit, p.multi_slot, o0, o1);
-    else
-        attn_join_sums_kernel<T, 8><<<(unsigned)blocks, 256, 0, s>>>(part, n_rows, p.n_slots, p.rows, heads, a.dim, width,
-                                                                     p.n_multi, p.multi_unit, p.multi_slot, o0, o1);
+    const int warps = join_warps(blocks, p.most_segs);
+    auto *kernel = warps == 1 ? attn_join_sums_kernel<T, 1> : attn_join_sums_kernel<T, 8>;
+    kernel<<<(unsigned)blocks, warps == 1 ? 32 : 256, 0, s>>>(part, n_rows, p.n_slots, p.rows, heads, a.dim, width, p.n_multi,
+                                                              p.multi_unit, p.multi_slot, o0, o1);
     SLA_CHECK_LAUNCH();
     return SLA_OK;
 }
@@ -838,8 +872,9 @@ sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
 }
 
 // Entries in flight: 4 or 5, whichever leaves fewer places empty on a row of mean
-// length (a 5-point row in one step instead of two); 2 where the registers hold
-// no more.
+// length (a 5-point row in one step instead of two: the 128 systems above take 97,
+// 140 and 96 us with 5, 112, 153 and 103 with 4); 2 where the registers hold no
+// more.
 template <typename T, int VEC, int L, int NV>
 sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
     constexpr int bytes = NV * VEC * (int)sizeof(typename AccOf<T>::type);
@@ -852,8 +887,9 @@ sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
     }
 }
 
-// Lanes and vectors a lane by the head's width: a group's load covers 128
-// consecutive bytes where the head has them.
+// Lanes and vectors a lane by the head's width.  Two 16-byte vectors a lane share
+// the loop's instructions (32 float32 elements: 97 us with 4 lanes, 123 with 8); a
+// group's load still covers 64 bytes or more where the head has them.
 template <typename T>
 sla_status launch_rows_of(int what, const AttnArgs &a, bool vec, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
@@ -998,6 +1034,7 @@ sla_status check_device(const char *fn, const Csr *h) {
     SLA_CHECK_CUDA(cudaGetDevice(&dev));
     SLA_REQUIRE(dev == h->device, "%s: the handle lives on device %d, the current device is %d", fn, h->device, dev);
     SLA_REQUIRE(h->nnz <= INT_MAX - 64, "%s: nnz=%lld, at most 2^31 - 65", fn, (long long)h->nnz);   // steps beyond a row's end
+    SLA_REQUIRE(h->n_rows <= INT_MAX - 512 && h->n_cols <= INT_MAX - 512, "%s: more than 2^31 - 513 rows or columns", fn);
     return SLA_OK;
 }
 
@@ -1022,6 +1059,11 @@ sla_status prepare(Csr *h, const sla_attn_opts *o, bool backward, cudaStream_t s
         }
     }
     sla_status st = SLA_OK;
+    // A^T's tiles count their columns, one for each of the sharing heads, in 32 bits
+    if (backward && o && attn_tiled(o))
+        SLA_REQUIRE((h->nnz << attn_tile_kind(o)) <= (int64_t)UINT_MAX - 64,
+                    "sla_attention: nnz=%lld with %d heads sharing a key head, 16-bit gradients take 2^32 / %d entries",
+                    (long long)h->nnz, 1 << attn_tile_kind(o), 1 << attn_tile_kind(o));
     if (backward && (st = ensure_transpose(h, s)) != SLA_OK) return st;
     for (int l = 0; l < kAttnLevels; ++l)
         for (int tiled = 0; tiled < 2; ++tiled) {

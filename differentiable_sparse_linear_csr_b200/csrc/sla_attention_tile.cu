@@ -30,6 +30,14 @@
 // backward subtracts D = dout . o from numbers of its size, and the values' gradient
 // shows the difference in 32 bits.
 //
+// What bounds it is neither the memory nor the tensor pipe (15 to 20 % active) but
+// the instructions of the masked softmax, the reads of shared memory and the waits
+// between them, with 12 warps an SM.  Measured: 1024 x 1024 grid, 4 heads of 32
+// bfloat16 elements, forward 500 us (2.1 TB/s of the bytes that cannot be left out;
+// the row kernels take 733); graph of 100 k rows and 1.2 M entries, 8 heads of 64:
+// forward 185 us, dq and ds 193, dk and dv 219, 2.7 to 3.3 TB/s (row kernels 528,
+// 696, 495).
+//
 // Masked pairs have weight 0, but 0 times an infinity or a NaN is a NaN.  A column
 // that every row leaves out (values of -inf: padding, which may hold anything) is
 // read as zeros.  If a sum ends as a NaN all the same, the warp redoes its rows
@@ -575,7 +583,9 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // A warp's ring of stages: two gathered tensors of HEADS heads, 16 rows each,
-// and with STAT a pair of numbers a column and head.
+// and with STAT a pair of numbers a column and head.  The padded pitch beats pieces
+// permuted in an unpadded row (508 against 546 us on the 1024 x 1024 grid): no
+// address arithmetic at a read.  Three stages where 12 warps' rings fit an SM.
 template <int D, int HEADS, bool STAT>
 struct Ring {
     static constexpr int kPieces = D / 8 * HEADS;                       // of a row
@@ -821,6 +831,9 @@ __device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, un
 }
 
 // KH key heads a warp; with one, the query heads of the tile share it.
+// Blocks an SM, here and below: 3 while the sums and the own rows leave room in 168
+// registers, else 2.  (1024 x 1024 grid, 2 heads of 32 a warp: 526 us cold with 3,
+// 612 with 2, 528 with 4 and spills, and dq of the graph 232 -> 380 us with 4.)
 template <typename T, int D, int KH, bool VALS, bool PACK>
 __global__ void __launch_bounds__(kTileThreads, D * KH <= 64 && !(PACK && VALS) ? 3 : 2)
 tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
@@ -1052,7 +1065,8 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
 }
 
 // (lse, D = dout . o) of every row and head, for both kernels below; lse in the unit
-// of relative().  G lanes a row and head, 8 elements each.
+// of relative().  G lanes a row and head, 8 elements each.  Bound by memory: 100 k
+// rows, 8 heads of 64, 307 MB in 50 us (6.1 TB/s).
 template <typename T, int G>
 __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__ AttnArgs a, int64_t count, float unit) {
     const int64_t x = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
@@ -1294,7 +1308,8 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 
 // By A^T's rows: dk (DK) and dv (DV) of 16 columns of A for KH key heads, the
 // query heads that share one following each other.  Wide heads take two launches:
-// both sums and both own operands would not fit the registers.  The values come in
+// both sums and both own operands would not fit the registers, and 3 blocks an SM
+// would spill (219 us with 2 on the graph above).  The values come in
 // A^T's order (tile_values_kernel).
 template <typename T, int D, int KH, bool DK, bool DV, bool VALS, bool PACK>
 __global__ void __launch_bounds__(kTileThreads, 2)
@@ -1555,7 +1570,8 @@ sla_status launch_delta(const AttnArgs &a, cudaStream_t s) {
 }
 
 // Key heads a warp: as many as fill 128 bytes of a gathered row, if every query
-// head has its own and their number allows.
+// head has its own and their number allows (1024 x 1024 grid, heads of 32: 526 us
+// with two, 654 with one, cold).
 template <typename T, int D, bool VALS>
 sla_status launch_tile_heads(int what, const AttnArgs &a, cudaStream_t s) {
     if constexpr (D <= 32) {

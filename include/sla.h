@@ -465,11 +465,13 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * and which a stream capture cannot hold (SLA_ERR_UNSUPPORTED): call
  * sla_attention_prepare before capturing, and before asking for the workspace
  * size (0 until then).  It prepares what calls with `opts` need (its strides do
- * not matter), or with NULL what calls of any type with heads == kv_heads need.  Workspaces are 256-byte
- * aligned; calls in flight at the same time need distinct ones.  With 16-bit
+ * not matter), or with NULL what calls of any type with heads == kv_heads need.
+ * Workspaces are 256-byte aligned; calls in flight at the same time need distinct ones.  With 16-bit
  * types and dim a multiple of 16 up to 128, addresses and strides of the head
  * tensors must be multiples of 16 bytes and row strides below 2^31 elements
- * (SLA_ERR_INVALID otherwise).  At most 2^31 - 65 entries.
+ * (SLA_ERR_INVALID otherwise).  At most 2^31 - 65 entries, and for their gradients
+ * fewer than 2^32 / s where s heads share a key head (the largest power of two that
+ * divides heads / kv_heads, at most 16).
  */
 typedef struct {
     int32_t dtype;            /* sla_dtype of q, k, v, out and their gradients */

@@ -94,6 +94,32 @@ def compare(A, rp, ci, q, k, v, vals, do, code, scale=None):
     return got
 
 
+LENGTHS = {
+    "long_among_middle": [60, 17, 64, 65, 5000, 0, 63, 1, 129, 16],    # one row in hundreds of parts, others whole
+    "many_of_few_parts": [100] * 140,
+    "many_of_many_parts": [700] * 140,
+}
+
+
+@pytest.mark.parametrize("name", LENGTHS)
+@pytest.mark.parametrize("code", ["f64", "f32", "bf16", "f16"])
+def test_split_rows(name, code):
+    """Rows of every number of parts: joined by one warp, or by several."""
+    rng = np.random.default_rng(11)
+    m = max(LENGTHS[name]) + 13
+    rp, ci, m = from_rows([rng.choice(m, size=c, replace=False) for c in LENGTHS[name]], m)
+    for heads, kv, dim in ((8, 8, 16), (4, 1, 32)):
+        gen = torch.Generator().manual_seed(3)
+        new = lambda *s: torch.randn(1, *s, generator=gen, dtype=torch.float64).to(DT[code])  # noqa: E731
+        n = rp.shape[0] - 1
+        q, do, k, v = new(n, heads, dim), new(n, heads, dim), new(m, kv, dim), new(m, kv, dim)
+        vt = torch.float64 if code == "f64" else torch.float32
+        vals = torch.randn(1, ci.shape[0], generator=gen, dtype=torch.float64).to(vt)
+        vals[0, ::7] = -np.inf
+        A = sla.CSR(T(rp), T(ci), n_cols=m, batch=1, dtype=vt)
+        compare(A, rp, ci, q, k, v, vals, do, code)
+
+
 @pytest.mark.parametrize("name", ["one", "one_row_long", "one_column", "full", "empty_rows", "no_entries", "hub", "grid"])
 @pytest.mark.parametrize("code", ["f64", "f32", "bf16", "f16"])
 def test_patterns(name, code):
@@ -453,3 +479,12 @@ def test_a_training_step_with_the_other_operators():
     assert abs(float(norm) - total) < 1e-7 * total
     after = float(torch.sqrt(sum((p.grad * p.grad).sum() for p in params)))
     assert abs(after - 0.25 * total) < 1e-5 * total
+
+
+def test_counts_beyond_32_bits_are_refused():
+    """16 heads on a key head repeat A^T's columns 16 times: 2^28 entries would wrap."""
+    n, m = 1 << 12, 1 << 16
+    rp = torch.arange(n + 1, dtype=torch.int32, device=DEV) * m
+    A = sla.CSR(rp, torch.arange(m, dtype=torch.int32, device=DEV).repeat(n), n_cols=m, dtype=torch.float32)
+    with pytest.raises((RuntimeError, ValueError), match="sharing a key head"):
+        A.prepare_attention(backward=True, heads_per_key=16)
