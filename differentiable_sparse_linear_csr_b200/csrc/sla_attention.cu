@@ -157,7 +157,7 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 
 // Enough items to fill the GPU when there are few units: 8 tiles an SM, a warp each,
 // or 128 rows, a few lanes each.  A level counts on 8 times as many systems and heads
-// as the one before, so it splits 8 times less.  Rows up to kWhole entries, or 5 items'
+// as the one before, so it splits 8 times less.  Rows up to kWhole entries, or 4 items'
 // share of the work, are not split, nor tiles up to kWhole columns: a short part
 // spends more on its partial result than on its entries.  Measured, forward pass:
 //   tiles, 24 an SM against 8: 300 rows over 1500 columns, 64 systems and heads,
@@ -165,8 +165,9 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 //   elements, 26 -> 30 us;
 //   rows, float32, 8, 64 and 128 an SM: 30000 rows of 20 entries and one of 20000, 8
 //   heads of 32, 1150, 205 and 137 us; 64 full rows over 4096 columns, 292, 60 and 45 us;
-//   rows whole up to 8 shares against 5: 513 rows of 256 entries, 8 heads of 32, 67
-//   against 46 us; up to 64 entries alone: 4000 rows of 100, a head of 64, 29 against 22.
+//   rows whole up to 5 shares against 4: 513 rows of 256 entries, 8 heads of 32, 66
+//   against 46 us (training 256, 184); 4000 rows of 100, a head of 64, 22 against 29
+//   (training 128, 134).
 int64_t fill_of(const Csr *h, int level, bool tiled) {
     return std::max<int64_t>(1, (int64_t)h->num_sms * (tiled ? 8 : 128) >> (3 * level));
 }
@@ -231,7 +232,7 @@ sla_status build_plans(Csr *h, int kind, bool transposed, int level, cudaStream_
         SLA_CHECK_LAUNCH();
     }
     if (tiled) st = build_items(p, len, 0, fill_of(h, level, true), kWhole / 16, kWhole / 16, 1, tiles->chunk0, s);
-    else st = build_items(p, len, 0, fill_of(h, level, false), kWhole / 4, kWhole, 5, nullptr, s);
+    else st = build_items(p, len, 0, fill_of(h, level, false), kWhole / 4, kWhole, 4, nullptr, s);
     if (st == SLA_OK) p->built = true;
     return st;
 }
@@ -335,11 +336,11 @@ __device__ __forceinline__ bool load_item(Item &r, const AttnArgs &a, unsigned y
     r.t1 = __ldg(a.rowptr + r.row + 1);
     r.slot = -1;
     if (a.item_unit) {
-        const int64_t begin = (int64_t)r.t0 + (int64_t)__ldg(a.item_seg + it) * a.seg_len;
-        const int64_t end = begin + a.seg_len;
         r.slot = __ldg(a.item_slot + it);
+        const int64_t begin = (int64_t)r.t0 + (int64_t)__ldg(a.item_seg + it) * a.seg_len;
+        const int64_t end = begin + (r.slot < 0 ? INT_MAX : a.seg_len);     // whole rows may be longer
         r.t0 = (int)begin;
-        if (r.slot >= 0) r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);    // whole rows may be longer
+        r.t1 = (int)(end < r.t1 ? end : (int64_t)r.t1);
     }
     return true;
 }
