@@ -223,6 +223,13 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same onto zeros.
+__device__ __forceinline__ void mma_tf32_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // The two 16-bit elements of a word as 32-bit numbers.
 template <typename T>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
@@ -365,35 +372,58 @@ struct Sums {
             o[nb][3] *= hi;
         }
     }
-    // The weights in two parts, or one.
-    __device__ __forceinline__ void add(const float (&w)[4], const uint32_t (&x0)[D / 16], const uint32_t (&x1)[D / 16],
-                                        bool two) {
+    // The weights of one half of a chunk in two parts, or one.
+    static __device__ __forceinline__ void split(const float (&w)[4], uint32_t (&hi)[4], uint32_t (&lo)[4], bool two) {
         const float v[4] = {w[0], w[2], w[1], w[3]};
-        uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (two) hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
             else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(v[i]));
             lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i]));
         }
-        // four blocks at a time, the second parts after the first ones
+    }
+    // The tensor core drops the bits that its 32-bit sums cannot hold, always towards
+    // zero, so a sum that stayed in it over a long row would drift (1500 entries: by
+    // 3.6e-6, a row of products in rounded sums 5e-7).  A chunk is summed from zero
+    // there and added to the running sums with rounding to nearest.
+    __device__ __forceinline__ void add(const float (&w)[2][4], const uint32_t (&x)[4][D / 16], bool two) {
+        uint32_t hi[2][4], lo[2][4];
+        split(w[0], hi[0], lo[0], two);
+        split(w[1], hi[1], lo[1], two);
+        // four blocks at a time, so that a product does not wait for the one before it
         constexpr int W = D / 16, G = W % 2 == 0 ? 2 : 1;
 #pragma unroll
         for (int j = 0; j < W; j += G) {
+            float t[2 * G][4];
             uint32_t y[G][4];
 #pragma unroll
-            for (int i = 0; i < G; ++i) {
-                widen<T>(x0[j + i], y[i][0], y[i][1]);
-                widen<T>(x1[j + i], y[i][2], y[i][3]);
-                mma_tf32(o[2 * (j + i)], hi, y[i][0], y[i][2]);
-                mma_tf32(o[2 * (j + i) + 1], hi, y[i][1], y[i][3]);
-            }
-            if (two) {
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int i = 0; i < G; ++i) {
-                    mma_tf32(o[2 * (j + i)], lo, y[i][0], y[i][2]);
-                    mma_tf32(o[2 * (j + i) + 1], lo, y[i][1], y[i][3]);
+                    widen<T>(x[2 * h][j + i], y[i][0], y[i][1]);
+                    widen<T>(x[2 * h + 1][j + i], y[i][2], y[i][3]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        if (h == 0) mma_tf32_first(t[2 * i + e], hi[0], y[i][e], y[i][2 + e]);
+                        else mma_tf32(t[2 * i + e], hi[1], y[i][e], y[i][2 + e]);
+                    }
                 }
+                if (two) {
+#pragma unroll
+                    for (int i = 0; i < G; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) mma_tf32(t[2 * i + e], lo[h], y[i][e], y[i][2 + e]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i) {
+                float (&to)[4] = o[2 * j + i];
+                const float2 a = add2(make_float2(to[0], to[1]), make_float2(t[i][0], t[i][1])),
+                             b = add2(make_float2(to[2], to[3]), make_float2(t[i][2], t[i][3]));
+                to[0] = a.x;
+                to[1] = a.y;
+                to[2] = b.x;
+                to[3] = b.y;
             }
         }
     }
@@ -418,8 +448,7 @@ struct Sums {
 #pragma unroll
         for (int j = 0; j < 4; ++j) read_sum<D>(x[j], stage + 2 * c * PITCH + (8 * (j >> 1) + (j & 1)) * PITCH, g);
         if (drop) drop_unused(x, used);
-        add(w[0], x[0], x[1], two);
-        add(w[1], x[2], x[3], two);
+        add(w, x, two);
     }
     // Row g (i = 0) or g + 8 (i = 1) to its D elements at p.  Of every group of
     // blocks this thread holds consecutive elements, first those of column 2c.
