@@ -972,18 +972,26 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 const bool down = (far[0] < -20.0f * kUnit && l[j][0] == 0.0f && far[0] != none) ||
                                   (far[1] < -20.0f * kUnit && l[j][1] == 0.0f && far[1] != none);
                 if (__any_sync(kAll, up || down)) {
-                    float sum[2] = {l[j][0], l[j][1]}, f[2];
+                    // Taken from the scores themselves: a difference to a reference of -1e10,
+                    // say, would hold none of their digits.
+                    float sum[2] = {l[j][0], l[j][1]}, top[2] = {none, none}, f[2];
+#pragma unroll
+                    for (int blk = 0; blk < 2; ++blk)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (mine[e >> 1] & pair_bit(blk, e))
+                                top[e >> 1] = fmaxf(top[e >> 1], relative<VALS>(s[blk][e], scale, x[blk][e], 0.0f));
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
 #pragma unroll
                         for (int o = 1; o < 4; o += o) {
-                            far[i] = fmaxf(far[i], __shfl_xor_sync(kAll, far[i], o));
+                            top[i] = fmaxf(top[i], __shfl_xor_sync(kAll, top[i], o));
                             sum[i] += __shfl_xor_sync(kAll, sum[i], o);
                         }
-                        const float by = far[i] == none ? 0.0f : (sum[i] == 0.0f ? far[i] : fmaxf(far[i], 0.0f));
-                        f[i] = by == 0.0f || sum[i] == 0.0f ? 1.0f : weight<VALS>(-by);
+                        const float to = top[i] == none ? m[j][i] : (sum[i] == 0.0f ? top[i] : fmaxf(m[j][i], top[i]));
+                        f[i] = to == m[j][i] || sum[i] == 0.0f ? 1.0f : weight<VALS>(m[j][i] - to);
                         l[j][i] *= f[i];
-                        m[j][i] += by;
+                        m[j][i] = to;
                     }
                     acc[j].scale(f[0], f[1]);
 #pragma unroll

@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import differentiable_sparse_linear_csr_b200 as sla
+from tests.attention_oracle import attention, within
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -70,3 +71,51 @@ def test_sums_of_long_columns_do_not_drift():
         want[:, h] = torch.softmax(q[:, h].double() @ k[:, h].double().T * D ** -0.5, 1).T @ do[:, h].double()
     drift = float((dv.double() / want - 1).mean())
     assert abs(drift) <= 2 * 2.0 ** -20 + 4 * 2.0 ** -23 + 2.0 ** -21 + 4 * 2.0 ** -12 / np.sqrt(3 * want.numel()), drift
+
+
+def left_padded(code, vt, low, level, heads=(2, 2), dim=64, m=70):
+    """A full pattern whose first 10 to 64 columns hold the value `low` (rows differ),
+    and what is left values around `level`: (A, q, k, v, vals, out) with out the
+    same values and -inf in place of `low`."""
+    n = 37
+    A = full_pattern(n, m, dtype=vt)
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    q, k, v = (torch.randn(s, h, dim, generator=gen, device=DEV).to(DT[code])
+               for s, h in ((n, heads[0]), (m, heads[1]), (m, heads[1])))
+    vals = level + torch.randn(n, m, generator=gen, device=DEV, dtype=vt)
+    pad = torch.arange(m, device=DEV) < (10 + torch.arange(n, device=DEV) * 3 % 55)[:, None]
+    return (A, q, k, v, torch.where(pad, torch.full_like(vals, low), vals).reshape(1, -1),
+            torch.where(pad, torch.full_like(vals, -float("inf")), vals).reshape(1, -1))
+
+
+LOWS = [-1e9, -1e10, -1e30, float(torch.finfo(torch.bfloat16).min), float(torch.finfo(torch.float32).min)]
+
+
+def oracle_of(A, q, k, v, vals, do, code):
+    num = lambda t: None if t is None else t.detach().double().cpu().numpy()  # noqa: E731
+    return attention(A.rowptr.cpu().numpy(), A.colind.cpu().numpy(), num(q), num(k), num(v), num(vals)[0],
+                     q.shape[2] ** -0.5, num(do), code)
+
+
+@pytest.mark.parametrize("level", [-300.0, -100.0, 0.0, 86.0, 120.0])
+@pytest.mark.parametrize("low", LOWS)
+@pytest.mark.parametrize("code,heads", [("f32", (2, 2)), ("bf16", (2, 2)), ("f16", (8, 2))])
+def test_low_finite_values_before_scores_of_any_size(code, heads, low, level):
+    """Entries of a very low finite value have weight 0 beside others (exp of -1e9 is 0
+    in 64 bits too), so the result is that of leaving them out, to its own bounds."""
+    A, q, k, v, vals, out = left_padded(code, torch.float32, low, level, heads)
+    o, wide, lse = forward_parts(A, q, k, v, vals)
+    res, err = oracle_of(A, q, k, v, out, None, code)
+    got = {"o": o, "lse": lse}
+    assert all(within(t.double().cpu().numpy(), res[x], err[x]) <= 1.0 for x, t in got.items())
+
+
+def test_low_finite_values_of_64_bits():
+    """The same with a float64 handle, whose lowest number is beyond 32 bits."""
+    low = float(torch.finfo(torch.float64).min)
+    for code in ("f64", "bf16"):
+        A, q, k, v, vals, out = left_padded(code, torch.float64, low, -100.0)
+        o, _, lse = forward_parts(A, q, k, v, vals)
+        res, err = oracle_of(A, q, k, v, out, None, code)
+        assert within(o.double().cpu().numpy(), res["o"], err["o"]) <= 1.0
+        assert within(lse.double().cpu().numpy(), res["lse"], err["lse"]) <= 1.0
