@@ -68,7 +68,8 @@ class sla_attn_opts(ctypes.Structure):
     _fields_ = [("dtype", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("dim", ctypes.c_int32), ("scale", ctypes.c_double),
                 ("q_stride", ctypes.c_int64 * 3), ("k_stride", ctypes.c_int64 * 3),
-                ("v_stride", ctypes.c_int64 * 3), ("do_stride", ctypes.c_int64 * 3)]
+                ("v_stride", ctypes.c_int64 * 3), ("do_stride", ctypes.c_int64 * 3),
+                ("lse_pairs", ctypes.c_int32)]
 
 
 class sla_tensor(ctypes.Structure):
@@ -356,10 +357,10 @@ def sla_attention_prepare(h, opts=None, backward=0, stream=None) -> None:
 
 
 def make_attn_opts(dtype, heads, kv_heads, dim, scale, q_stride, k_stride, v_stride,
-                   do_stride=(0, 0, 0)) -> sla_attn_opts:
+                   do_stride=(0, 0, 0), lse_pairs=False) -> sla_attn_opts:
     st = ctypes.c_int64 * 3
     return sla_attn_opts(TENSOR_DTYPES[dtype], int(heads), int(kv_heads), int(dim), float(scale),
-                         st(*q_stride), st(*k_stride), st(*v_stride), st(*do_stride))
+                         st(*q_stride), st(*k_stride), st(*v_stride), st(*do_stride), int(lse_pairs))
 
 
 def sla_attention_workspace_bytes(h, opts, backward=0) -> int:

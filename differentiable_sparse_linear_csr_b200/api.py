@@ -366,16 +366,16 @@ class _AttentionCall:
         self.wide = torch.float64 if q.dtype == torch.float64 else torch.float32
         self.lse = A.batch * A.n_rows * H * (8 if q.dtype == torch.float64 else 4)
         self.ready = [False, False]
-        self.opts = self.options(q, k, v)
+        self.opts = [self.options(q, k, v, pairs=train) for train in (False, True)]
         self.back = {}                           # options of the gradients, by the strides they depend on
 
-    def options(self, q, k, v, do=None):
+    def options(self, q, k, v, do=None, pairs=True):
         def strides(x):
             st = x.stride()
             return st[:3] if len(st) == 4 else (0, *st[:2])
 
         return L.make_attn_opts(*self.size, self.scale, strides(q), strides(k), strides(v),
-                                (0, 0, 0) if do is None else strides(do))
+                                (0, 0, 0) if do is None else strides(do), pairs)
 
     def prepare(self, A, opts, backward):
         if not self.ready[backward]:
@@ -384,18 +384,18 @@ class _AttentionCall:
             self.ready[0] = self.ready[backward] = True
 
     def forward(self, A, q, k, v, values, train):
-        """(o, its 32-bit form or None, lse or None, q, k, v as the kernels read them)"""
+        """(o, its 32-bit form or None, the rows' (m, l) or None, q, k, v as the kernels read them)"""
         vals = None if values is None else A._values(values)
-        opts, given = self.opts, (q, k, v)
+        opts, given = self.opts[train], (q, k, v)
         q, k, v = _head_layout(q, self.whole), _head_layout(k, self.whole), _head_layout(v, self.whole)
         if q is not given[0] or k is not given[1] or v is not given[2]:
-            opts = self.options(q, k, v)
+            opts = self.options(q, k, v, pairs=train)
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         with _on_device(A.device):
             self.prepare(A, opts, train)
             room = self.workspace[0]
             if train:
-                lse = torch.empty(A.batch, A.n_rows, q.shape[-2], dtype=self.wide, device=A.device)
+                lse = torch.empty(A.batch, A.n_rows, q.shape[-2], 2, dtype=self.wide, device=A.device)
                 wide = torch.empty(out.shape, dtype=self.wide, device=A.device) if q.element_size() == 2 else None
                 L.sla_attention(A.handle, q, k, v, vals, out, wide, lse, opts,
                                 _workspace(room, A.device) if room else None)

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fwd_rows_kernel(const __gri
             acc.scale(l > (A)0 || l != l ? (A)1 / l : (A)0);   // no entry left: zeros
             acc.store(static_cast<T *>(a.out) + at * a.dim, a.dim, lane);
             if (a.wide) acc.store(static_cast<A *>(a.wide) + at * a.dim, a.dim, lane);
-            if (lane == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+            if (lane == 0) store_lse<A>(a, at, m, l);
         } else {
             const int64_t at = part_index(it.slot, a.n_slots, (int)it.b, 1, 0, a.heads, h);
             acc.store_odd(static_cast<A *>(a.part) + at * a.dim, a.dim, lane);
@@ -612,7 +612,7 @@ attn_join_kernel(const AttnArgs a, int rows, int n_multi, const int32_t *__restr
         static_cast<T *>(a.out)[at * a.dim + d] = from_acc<T>(y * inv);
         if (a.wide) static_cast<A *>(a.wide)[at * a.dim + d] = y * inv;
     }
-    if (threadIdx.x == 0) static_cast<A *>(a.lse)[at] = l == (A)0 ? none : m + log_acc(l);
+    if (threadIdx.x == 0) store_lse<A>(a, at, m, l);
 }
 
 // Gradients by A's rows: p and ds of every entry and head, and dq.
@@ -632,7 +632,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_bwd_rows_kernel(const __gri
         go.load(static_cast<const T *>(a.dout) + it.b * a.ds[0] + it.row * a.ds[1] + h * a.ds[2], a.dim, lane);
         acc.load(static_cast<const A *>(a.o) + at * a.dim, a.dim, lane);
         const A delta = group_sum<L>(go.dot(acc), mask);
-        const A lse = static_cast<const A *>(a.lse)[at];
+        const A m = static_cast<const A *>(a.lse)[2 * at], l = static_cast<const A *>(a.lse)[2 * at + 1];
+        const A inv = (A)1 / l;
         acc.zero();
         const T *kb = static_cast<const T *>(a.k) + it.b * a.ks[0] + kh * a.ks[2];
         const T *vb = static_cast<const T *>(a.v) + it.b * a.vs[0] + kh * a.vs[2];
@@ -655,10 +656,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_bwd_rows_kernel(const __gri
             }
 #pragma unroll
             for (int u = 0; u < STEP; ++u) {
-                const bool on = w[u] != none && lse != none;
+                const bool on = w[u] != none && l != (A)0;
                 p[u] = group_sum<L>(p[u], mask);
                 ds[u] = group_sum<L>(ds[u], mask);
-                p[u] = on ? exp_acc(fma(p[u], scale, w[u]) - lse) : (A)0;
+                p[u] = on ? exp_acc(fma(p[u], scale, w[u]) - m) * inv : (A)0;
                 ds[u] = on ? p[u] * (ds[u] - delta) : (A)0;
                 if (on) acc.axpy(ds[u], kf[u]);
             }
@@ -1009,7 +1010,7 @@ AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
         return w;
     }
     if (attn_tiled(o)) {
-        w.stat = B * H * (size_t)h->n_rows * sizeof(float2);
+        w.stat = B * H * (size_t)h->n_rows * sizeof(float4);
         w.ds = B * H * (size_t)h->nnz * sizeof(float);
         w.vals_w = B * (size_t)h->nnz * sizeof(float);
     } else {
@@ -1026,6 +1027,7 @@ sla_status check_opts(const char *fn, const sla_attn_opts *o) {
                 "%s: heads must be a positive multiple of kv_heads (%d, %d)", fn, o->heads, o->kv_heads);
     SLA_REQUIRE(o->dim >= 1 && o->dim <= 256, "%s: dim must be in [1, 256] (got %d)", fn, o->dim);
     SLA_REQUIRE(o->scale == o->scale && o->scale <= DBL_MAX && o->scale >= -DBL_MAX, "%s: scale is not finite", fn);
+    SLA_REQUIRE(o->lse_pairs == 0 || o->lse_pairs == 1, "%s: lse_pairs must be 0 or 1 (got %d)", fn, o->lse_pairs);
     return SLA_OK;
 }
 
@@ -1110,6 +1112,7 @@ AttnArgs make_args(const Csr *h, const sla_attn_opts *o, const void *q, const vo
     a.v = v;
     a.vals = vals;
     a.vals_f64 = h->dtype == SLA_F64;
+    a.lse_pairs = o->lse_pairs;
     for (int i = 0; i < 3; ++i) {
         a.qs[i] = o->q_stride[i];
         a.ks[i] = o->k_stride[i];
@@ -1152,6 +1155,7 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     if (st != SLA_OK) return st;
     if (h->n_rows == 0) return SLA_OK;
     SLA_REQUIRE(q && out && lse && (h->n_cols == 0 || (k && v)), "sla_attention: NULL pointer");
+    SLA_REQUIRE((uintptr_t)lse % (acc_size(o->dtype) << o->lse_pairs) == 0, "sla_attention: lse is not aligned");
     if (o->dtype == SLA_F64 || o->dtype == SLA_F32) out_wide = nullptr;
     st = check_tiled("sla_attention", o, {out, out_wide}, {{q, o->q_stride}, {k, o->k_stride}, {v, o->v_stride}});
     if (st != SLA_OK) return st;
@@ -1190,6 +1194,8 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     sla_status st = check_device("sla_attention_grad", h);
     if (st == SLA_OK) st = check_opts("sla_attention_grad", o);
     if (st != SLA_OK) return st;
+    SLA_REQUIRE(o->lse_pairs, "sla_attention_grad: needs the statistics of a forward call with lse_pairs");
+    SLA_REQUIRE((uintptr_t)lse % (2 * acc_size(o->dtype)) == 0, "sla_attention_grad: lse is not aligned to its pairs");
     SLA_REQUIRE(!dvals || vals, "sla_attention_grad: dvals without vals");
     SLA_REQUIRE(h->n_rows == 0 || (q && out && lse && dout), "sla_attention_grad: NULL pointer");
     SLA_REQUIRE(h->n_cols == 0 || (k && v), "sla_attention_grad: NULL pointer");
@@ -1213,7 +1219,7 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     a.dvals = dvals;
     Carver c(ws);
     a.pds = c.take<char>(w.pds);
-    a.stat = reinterpret_cast<float2 *>(c.take<char>(w.stat));
+    a.stat = reinterpret_cast<float4 *>(c.take<char>(w.stat));
     a.ds_out = dvals ? reinterpret_cast<float *>(c.take<char>(w.ds)) : (c.take<char>(w.ds), nullptr);
     a.vals_w = reinterpret_cast<float *>(c.take<char>(w.vals_w));
     a.part = c.take<char>(w.part);

@@ -3,8 +3,10 @@
 // split rows.
 //
 //   s_t = scale * q_i . k_j + vals_t      for entry t = (i, j) of row i
-//   p_t = exp(s_t - lse_i),  lse_i = log sum_t exp(s_t),  o_i = sum_t p_t v_j
-// and backwards, with D_i = do_i . o_i:
+//   p_t = exp(s_t - m_i) / l_i,  l_i = sum_t exp(s_t - m_i),  o_i = sum_t p_t v_j
+// with a reference m_i near the row's maximum (lse_i = m_i + log l_i).  The backward
+// needs m and l apart: beside a large m their sum holds little or nothing of log l.
+// Backwards, with D_i = do_i . o_i:
 //   ds_t = p_t (do_i . v_j - D_i),  dq_i = scale sum_t ds_t k_j,
 //   dk_j = scale sum_t ds_t q_i,    dv_j = sum_t p_t do_i,  dvals_t = sum_heads ds_t.
 #pragma once
@@ -97,9 +99,10 @@ struct AttnArgs {
     const void *vals;
     int32_t vals_f64;
     void *out, *wide, *lse;                // forward (wide: out before its rounding, or null)
+    int32_t lse_pairs;                     // lse holds pairs (m, l)
     void *dq, *dk, *dv, *dvals;            // backward
     void *pds;                             // row kernels: [B][nnz][heads] pairs (p, ds)
-    float2 *stat;                          // tile kernels: [B][heads][n_rows] pairs (lse, D), lse / log 2 without values
+    float4 *stat;                          // tile kernels: [B][heads][n_rows] m, 1 / l, D / l, 0 (m / log 2 without values)
     float *ds_out;                         // tile kernels: [B][heads][nnz] ds, or null
     float *vals_w;                         // tile kernels: room for [B][nnz] 32-bit values
     const float *vals_f, *vals_t;          // and the values as they read them, in A's and A^T's order
@@ -171,6 +174,19 @@ __device__ __forceinline__ double log_acc(double x) { return log(x); }
 template <typename A> __device__ __forceinline__ A neg_inf();
 template <> __device__ __forceinline__ float neg_inf<float>() { return __int_as_float(0xff800000); }
 template <> __device__ __forceinline__ double neg_inf<double>() { return __longlong_as_double(0xfff0000000000000ll); }
+
+// A row's statistics: l == 0 (no weight) is lse = -inf.
+template <typename A>
+__device__ __forceinline__ void store_lse(const AttnArgs &a, int64_t at, A m, A l) {
+    const A top = l == (A)0 ? neg_inf<A>() : m;
+    A *p = static_cast<A *>(a.lse);
+    if (a.lse_pairs) {
+        p[2 * at] = top;
+        p[2 * at + 1] = l;
+    } else {
+        p[at] = l == (A)0 ? top : m + log_acc(l);
+    }
+}
 
 // A stored value as a score term.  A finite 64-bit value beyond the 32-bit
 // range stays finite, so that only -inf removes an entry.

@@ -257,7 +257,7 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Scores less a reference (a number near the maximum, or lse), and their
+// Scores less a reference (a number near the maximum), and their
 // exponential.  Without values both are in units of log 2: the factor log2 e is
 // part of `scale`, so that the difference is one multiply-add.  Values come in
 // natural units, and the factor is applied to the difference, so that the lowest
@@ -605,23 +605,20 @@ struct Chunk {
 __device__ __forceinline__ void cp_async16(unsigned dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp_async8(unsigned dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // A warp's ring of stages: two gathered tensors of HEADS heads, 16 rows each,
-// and with STAT a pair of numbers a column and head.  The padded pitch beats pieces
+// and with STAT four numbers a column and head.  The padded pitch beats pieces
 // permuted in an unpadded row (508 against 546 us on the 1024 x 1024 grid): no
-// address arithmetic at a read.  Three stages where 12 warps' rings fit an SM.
+// address arithmetic at a read.  Three stages where 12 warps' rings (8 with STAT) fit an SM.
 template <int D, int HEADS, bool STAT>
 struct Ring {
     static constexpr int kPieces = D / 8 * HEADS;                       // of a row
     static constexpr int kPitch = (kPieces + 7) / 8 * 128 + 16;
     static constexpr int kTensor = 16 * kPitch;
-    static constexpr int kStage = 2 * kTensor + (STAT ? 16 * 8 * HEADS : 0);
-    static constexpr int kStages = kStage <= 5120 ? 3 : 2;
+    static constexpr int kStage = 2 * kTensor + (STAT ? 16 * 16 * HEADS : 0);
+    static constexpr int kStages = kStage <= (STAT ? 5632 : 5120) ? 3 : 2;
     static constexpr int kBytes = kStage * kStages;
     static constexpr bool kEven = 32 % kPieces == 0;                    // a lane has one piece of every row it copies
 
@@ -733,7 +730,7 @@ __device__ __noinline__ void slow_forward(const AttnArgs &a, const TileWork &w) 
                     static_cast<T *>(a.out)[at * a.dim + i * 32 + lane] = from_acc<T>(acc[i] * inv);
                     if (a.wide) static_cast<float *>(a.wide)[at * a.dim + i * 32 + lane] = acc[i] * inv;
                 }
-            if (lane == 0) static_cast<float *>(a.lse)[at] = l == 0.0f ? none : m + logf(l);
+            if (lane == 0) store_lse(a, at, m, l);
         } else {
             const int64_t at = part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h);
             float *p = static_cast<float *>(a.part) + at * a.dim;
@@ -1048,7 +1045,17 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                     const int64_t o = at0 + (uint64_t)(unsigned)r * step + h;
                     acc[j].store(static_cast<T *>(a.out) + o * D, i, c);
                     if (a.wide) acc[j].store(static_cast<float *>(a.wide) + o * D, i, c);
-                    if (c == 0) static_cast<float *>(a.lse)[o] = top + __log2f(l[j][i] == 0.0f ? 1.0f : l[j][i]) * kLn2;
+                    if (c == 0) {
+                        if (a.lse_pairs) {
+                            // The sum takes what m's return to natural units rounds away, so that the
+                            // two agree when the backward goes back to units of log 2.
+                            float sum = l[j][i];
+                            if (!VALS && sum > 0.0f) sum *= exp2_of(fminf(fmaxf(m[j][i] - top * kLog2e, -64.0f), 64.0f));
+                            static_cast<float2 *>(a.lse)[o] = make_float2(top, sum);
+                        } else {
+                            static_cast<float *>(a.lse)[o] = top + __log2f(l[j][i] == 0.0f ? 1.0f : l[j][i]) * kLn2;
+                        }
+                    }
                 } else {
                     const int64_t at = part_index(w.slot, a.n_slots, w.b, 1 << a.rows_log, r, a.heads, w.h + h);
                     acc[j].store(static_cast<float *>(a.part) + at * D, i, c);
@@ -1076,15 +1083,17 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
         slow_load(q, static_cast<const T *>(a.q) + w.b * a.qs[0] + row * a.qs[1] + w.h * a.qs[2], a.dim, lane);
         slow_load(go, static_cast<const T *>(a.dout) + w.b * a.ds[0] + row * a.ds[1] + w.h * a.ds[2], a.dim, lane);
         slow_load(o, static_cast<const float *>(a.o) + at * a.dim, a.dim, lane);
-        const float delta = slow_dot(go, o), lse = static_cast<const float *>(a.lse)[at];
-        for (int t = t0; t < t1 && lse != none; ++t) {
+        const float delta = slow_dot(go, o);
+        const float2 ml = static_cast<const float2 *>(a.lse)[at];
+        const float inv = 1.0f / ml.y;
+        for (int t = t0; t < t1 && ml.y != 0.0f; ++t) {
             const int64_t col = SLA_IDX((int64_t)__ldg(a.colind + t), a.n_cols, kBndColumn);
             const float x = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + t);
             if (x == none) continue;
             float k[kSlowVec], v[kSlowVec];
             slow_load(k, kb + col * a.ks[1], a.dim, lane);
             slow_load(v, vb + col * a.vs[1], a.dim, lane);
-            const float p = exp_acc(fmaf(slow_dot(q, k), scale, x) - lse);
+            const float p = exp_acc(fmaf(slow_dot(q, k), scale, x) - ml.x) * inv;
             const float ds = p * (slow_dot(go, v) - delta);
 #pragma unroll
             for (int i = 0; i < kSlowVec; ++i) acc[i] = fmaf(ds, k[i], acc[i]);
@@ -1101,9 +1110,11 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
     }
 }
 
-// (lse, D = dout . o) of every row and head, for both kernels below; lse in the unit
-// of relative().  G lanes a row and head, 8 elements each.  Bound by memory: 100 k
-// rows, 8 heads of 64, 307 MB in 50 us (6.1 TB/s).
+// (m, 1 / l, D / l) with D = dout . o of every row and head, for both kernels below; m
+// in the unit of relative(), -inf where the row has no weight.  A weight's derivative
+// p (dp - D) is then exp(s - m) (dp / l - D / l), one multiply-add as without l.
+// G lanes a row and head, 8 elements each.  Bound by memory: 100 k rows, 8 heads of
+// 64, 307 MB in 50 us (6.1 TB/s).
 template <typename T, int G>
 __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__ AttnArgs a, int64_t count, float unit) {
     const int64_t x = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
@@ -1128,9 +1139,13 @@ __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-    if (x < count && l == 0)
-        a.stat[(b * a.heads + h) * a.n_rows + (row - b * a.n_rows)] =
-            make_float2(__ldg(static_cast<const float *>(a.lse) + x) * unit, s);
+    if (x < count && l == 0) {
+        const float2 ml = __ldg(static_cast<const float2 *>(a.lse) + x);
+        const float inv = 1.0f / ml.y;
+        // a sum that is a NaN may come with m = -inf, which would say that there is none
+        const float m = ml.y == 0.0f ? neg_inf<float>() : (ml.y != ml.y ? ml.y : ml.x * unit);
+        a.stat[(b * a.heads + h) * a.n_rows + (row - b * a.n_rows)] = make_float4(m, inv, s * inv, 0.0f);
+    }
 }
 
 // By A's rows: dq, and ds of every entry if asked for.
@@ -1184,8 +1199,7 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         w_next = tile_work(a, now, groups, share, PACK ? a.rows_log : 4);
         const int n = w.ch1 - w.ch0;
         Own<D> q[KH], go[KH];
-        float lse[KH][2], delta[KH][2];
-        unsigned live[KH][2];                            // all ones, or 0: the row has no weights
+        float m[KH][2], inv[KH][2], delta[KH][2];        // delta: D / l
         Sums<T, D> acc[KH];
 #pragma unroll
         for (int j = 0; j < KH; ++j) {
@@ -1196,11 +1210,11 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int64_t row = w.row0 + rows.r[i];
-                float2 st = make_float2(none, 0.0f);
+                float4 st = make_float4(none, 0.0f, 0.0f, 0.0f);
                 if (row < a.n_rows) st = __ldg(a.stat + ((int64_t)w.b * a.heads + h + rows.h[i]) * a.n_rows + row);
-                lse[j][i] = st.x;
-                delta[j][i] = st.y;
-                live[j][i] = st.x == none ? 0u : ~0u;
+                m[j][i] = st.x;
+                inv[j][i] = st.y;
+                delta[j][i] = st.z;
             }
         }
         float *ds_out = VALS && a.ds_out ? a.ds_out + ((int64_t)w.b * a.heads + w.h) * a.nnz : nullptr;
@@ -1240,13 +1254,14 @@ tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 score_products<T, D, R::kPitch>(s, q[j], at, g, c);
                 score_products<T, D, R::kPitch>(dp, go[j], at + R::kTensor, g, c);
                 if (j == 0) meta.late(a.vals_f, a.nnz, c);
-                const unsigned on[2] = {mine[0] & live[j][0], mine[1] & live[j][1]};
+                const unsigned on[2] = {m[j][0] == none ? 0u : mine[0], m[j][1] == none ? 0u : mine[1]};    // rows with weights
 #pragma unroll
                 for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = e >> 1;
-                        s[blk][e] = weight<VALS>(relative<VALS>(s[blk][e], scale, x[blk][e], lse[j][i])) * (dp[blk][e] - delta[j][i]);
+                        s[blk][e] = weight<VALS>(relative<VALS>(s[blk][e], scale, x[blk][e], m[j][i])) *
+                                    fmaf(dp[blk][e], inv[j][i], -delta[j][i]);
                         s[blk][e] = on[i] & pair_bit(blk, e) ? s[blk][e] : 0.0f;
                     }
                 if (VALS && ds_out) {
@@ -1311,14 +1326,14 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
                 const int64_t i = SLA_IDX((int64_t)__ldg(a.colind + t), a.n_rows, kBndColumn);
                 const int64_t e = SLA_IDX((int64_t)__ldg(a.perm + t), a.nnz, kBndEntry);
                 const float x = load_value<float>(a.vals, a.vals_f64, w.b * a.nnz + e);
-                const float2 st = a.stat[((int64_t)w.b * a.heads + h) * a.n_rows + i];
+                const float4 st = a.stat[((int64_t)w.b * a.heads + h) * a.n_rows + i];
                 if (x == none || st.x == none) continue;
                 float q[kSlowVec], go[kSlowVec];
                 slow_load(q, static_cast<const T *>(a.q) + w.b * a.qs[0] + i * a.qs[1] + h * a.qs[2], a.dim, lane);
                 slow_load(go, static_cast<const T *>(a.dout) + w.b * a.ds[0] + i * a.ds[1] + h * a.ds[2], a.dim, lane);
-                const float p = exp2f(a.vals ? (fmaf(slow_dot(q, k), scale, x) - st.x) * kLog2e
-                                            : fmaf(slow_dot(q, k), scale * kLog2e, -st.x));
-                const float ds = p * (slow_dot(go, v) - st.y);
+                const float e2 = exp2f(a.vals ? (fmaf(slow_dot(q, k), scale, x) - st.x) * kLog2e
+                                             : fmaf(slow_dot(q, k), scale * kLog2e, -st.x));
+                const float p = e2 * st.y, ds = e2 * fmaf(slow_dot(go, v), st.y, -st.z);
 #pragma unroll
                 for (int j = 0; j < kSlowVec; ++j) {
                     dk[j] = fmaf(ds, q[j], dk[j]);
@@ -1370,7 +1385,7 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     Cursor now = stride.at(first);
     Feed<R> feed = {};
     const char *qb = nullptr, *gb = nullptr;
-    const float2 *stat = nullptr;
+    const float4 *stat = nullptr;
     int begin = 0, fh = 0;                               // first chunk of the feed's tile, its shared head
     auto open_head = [&](int b, int h) {
         qb = R::source(static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2], a.qs[2] * 2, lane);
@@ -1396,8 +1411,8 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
         for (int j = 0; j < KH; j += 2) {               // lanes 16 to 31: the next head
             const int jj = KH == 1 ? 0 : j + (lane >> 4);
             if (KH > 1 || lane < 16)
-                cp_async8(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 8,
-                          stat + (int64_t)(PACK ? lane & ((1 << times) - 1) : jj) * a.n_rows + col);
+                cp_async16(st + 2 * R::kTensor + (jj * 16 + (lane & 15)) * 16,
+                           stat + (int64_t)(PACK ? lane & ((1 << times) - 1) : jj) * a.n_rows + col);
         }
         if (KH == 1 && feed.at + 1 == feed.end && fh + 1 < groups) {    // the tile again, with its next heads
             ++fh;
@@ -1449,26 +1464,28 @@ tile_bwd_cols_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                 score_products<T, D, R::kPitch>(s, k[j], at, g, c);
                 if constexpr (DK) score_products<T, D, R::kPitch>(dp, v[j], at + R::kTensor, g, c);
                 if (j == 0) meta.late(a.vals_t, a.nnz, c, times);
-                const unsigned sp = stage + 2 * R::kTensor + j * 128 + c * 16;
+                const unsigned sp = stage + 2 * R::kTensor + j * 256 + c * 32;
                 unsigned live[2] = {mine[0], mine[1]};
                 bool out = false;                       // a stored pair without a part: its row or value is left out
 #pragma unroll
-                for (int blk = 0; blk < 2; ++blk) {
-                    const uint4 su = lds16(sp + blk * 64);          // (lse, D) of the columns 2c and 2c + 1
-                    const float4 st = make_float4(__uint_as_float(su.x), __uint_as_float(su.y), __uint_as_float(su.z),
-                                                  __uint_as_float(su.w));
+                for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float lse = e & 1 ? st.z : st.x, delta = e & 1 ? st.w : st.y;
-                        if (lse == none || (VALS && val[blk][e] == none)) {
-                            out = out || (live[e >> 1] & pair_bit(blk, e));
-                            live[e >> 1] &= ~pair_bit(blk, e);
+                    for (int col = 0; col < 2; ++col) {
+                        const uint4 st = lds16(sp + blk * 128 + col * 16);      // the statistics of column 2c + col
+                        const float m = __uint_as_float(st.x), inv = __uint_as_float(st.y), delta = __uint_as_float(st.z);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int e = 2 * i + col;
+                            if (m == none || (VALS && val[blk][e] == none)) {
+                                out = out || (live[i] & pair_bit(blk, e));
+                                live[i] &= ~pair_bit(blk, e);
+                            }
+                            const bool on = live[i] & pair_bit(blk, e);
+                            const float p = weight<VALS>(relative<VALS>(s[blk][e], scale, val[blk][e], m));
+                            if constexpr (DV) s[blk][e] = on ? p * inv : 0.0f;
+                            if constexpr (DK) dp[blk][e] = on ? p * fmaf(dp[blk][e], inv, -delta) : 0.0f;
                         }
-                        const bool on = live[e >> 1] & pair_bit(blk, e);
-                        s[blk][e] = on ? weight<VALS>(relative<VALS>(s[blk][e], scale, val[blk][e], lse)) : 0.0f;
-                        if constexpr (DK) dp[blk][e] = on ? s[blk][e] * (dp[blk][e] - delta) : 0.0f;
                     }
-                }
                 const bool drop = VALS && __any_sync(kAll, out);
                 used = (live[0] | live[1]) & 0x303u;
                 used = (used | used >> 6) & 15u;

@@ -445,13 +445,18 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * q: [B][n_rows][heads][dim], k and v: [B][n_cols][kv_heads][dim], of opts.dtype
  * (any sla_dtype, whatever the handle's), with the strides of opts; the last
  * dimension is contiguous.  out [B][n_rows][heads][dim] (opts.dtype) and lse
- * [B][n_rows][heads] (double for SLA_F64, else float) are contiguous.
+ * [B][n_rows][heads] (double for SLA_F64, else float) are contiguous.  With
+ * opts.lse_pairs, lse is [B][n_rows][heads][2], pairs (m, l) with lse_i = m + log l
+ * and m near the row's largest score (-inf and 0 where no entry is left): beside
+ * scores of a large size (a value of -1e9 on every entry of a row) the sum holds
+ * little or nothing of log l.
  * out_wide: NULL, or for 16-bit types a float array like out that receives o
  * before its rounding (ignored for the others).  Sums,
  * maxima and weights are held in 32 bits (64 for SLA_F64) and every sum has a
  * fixed order: equal calls give equal bits.
  *
- * sla_attention_grad needs lse and the unrounded o of the forward call (out, or
+ * sla_attention_grad needs lse in pairs (SLA_ERR_INVALID without opts.lse_pairs) and
+ * the unrounded o of the forward call (out, or
  * out_wide for 16-bit types: the difference below would keep only the rounded
  * o's digits) and dout = dL/dout:
  *   ds_t = p_t (dout_i . v_j - dout_i . o_i);   dq_i = scale sum_t ds_t k_j;
@@ -483,6 +488,7 @@ typedef struct {
     int64_t k_stride[3];
     int64_t v_stride[3];
     int64_t do_stride[3];     /* of dout (sla_attention_grad) */
+    int32_t lse_pairs;        /* 1: lse holds pairs (m, l); else 0 */
 } sla_attn_opts;
 sla_status sla_attention_prepare(sla_csr_t h, const sla_attn_opts *opts, int32_t backward,
                                  void *stream);

@@ -119,3 +119,82 @@ def test_low_finite_values_of_64_bits():
         res, err = oracle_of(A, q, k, v, out, None, code)
         assert within(o.double().cpu().numpy(), res["o"], err["o"]) <= 1.0
         assert within(lse.double().cpu().numpy(), res["lse"], err["lse"]) <= 1.0
+
+
+def training(A, q, k, v, vals, do):
+    ts = [t.clone().requires_grad_() for t in (q, k, v, vals)]
+    o = A.attention(*ts)
+    return [t.double().cpu().numpy() for t in (o.detach(), *torch.autograd.grad(o, ts, do))]
+
+
+@pytest.mark.parametrize("level", [-10000.0, -1e9, -1e30, "lowest"])
+@pytest.mark.parametrize("code,heads,dim", [("f64", (2, 2), 32), ("f32", (2, 2), 64), ("f32", (4, 1), 20), ("bf16", (2, 2), 64),
+                                            ("bf16", (8, 2), 32), ("f16", (4, 4), 32), ("f16", (1, 1), 100)])
+def test_gradients_of_rows_of_equal_low_values(code, heads, dim, level):
+    """Rows whose entries all hold one very low finite value are the rows without it:
+    softmax does not see what all scores share.  q = 0, so that no score is lost beside
+    the value: every weight is 1 / n, and the gradients have closed forms,
+        o = mean v,  ds_t = (do . v_t - do . mean v) / n,  dv = sum do / n,
+        dq = scale sum_t ds_t k_t,  dk = 0,  dvals = sum over heads of ds.
+    Every row also has a part beyond 64 entries that is split from it."""
+    vt = torch.float64 if code == "f64" else torch.float32
+    n, m = 37, 700
+    A = full_pattern(n, m, dtype=vt)
+    low = float(torch.finfo(vt).min) if level == "lowest" else level
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    k, v, do = (torch.randn(s, h, dim, generator=gen, device=DEV, dtype=torch.float64).to(DT[code])
+                for s, h in ((m, heads[1]), (m, heads[1]), (n, heads[0])))
+    q = torch.zeros(n, heads[0], dim, device=DEV, dtype=DT[code])
+    got = training(A, q, k, v, torch.full((1, m * n), low, dtype=vt, device=DEV), do)
+    res, err = oracle_of(A, q, k, v, torch.zeros(1, m * n, device=DEV), do, code)
+    assert np.array_equal(res["dk"], np.zeros_like(res["dk"]))
+    worst = {x: within(g, res[x], err[x]) for x, g in zip(("o", "dq", "dk", "dv", "dvals"),
+                                                          (got[0], got[1], got[2], got[3], got[4][0]))}
+    assert all(w <= 1.0 for w in worst.values()), worst
+
+
+@pytest.mark.parametrize("low", LOWS)
+@pytest.mark.parametrize("code,heads", [("f32", (2, 2)), ("bf16", (2, 2)), ("f16", (8, 2))])
+def test_gradients_with_low_finite_values_before_others(code, heads, low):
+    """As in the forward pass: the gradients of leaving those entries out."""
+    A, q, k, v, vals, out = left_padded(code, torch.float32, low, -100.0, heads)
+    do = torch.randn(q.shape, generator=torch.Generator(device=DEV).manual_seed(9), device=DEV).to(DT[code])
+    got = training(A, q, k, v, vals, do)
+    res, err = oracle_of(A, q, k, v, out, do, code)
+    worst = {x: within(g, res[x], err[x]) for x, g in zip(("o", "dq", "dk", "dv", "dvals"), (*got[:4], got[4][0]))}
+    assert all(w <= 1.0 for w in worst.values()), worst
+
+
+def test_pairs_of_maximum_and_sum():
+    """The C call's pairs (m, l) give lse, on whole and split rows, rows without an
+    entry left and in every kind of kernel; gradients without pairs are refused."""
+    from differentiable_sparse_linear_csr_b200 import _lib as L
+    for code, heads, dim, m in (("f64", (2, 1), 16, 70), ("f32", (2, 2), 32, 700), ("bf16", (2, 2), 64, 70),
+                                ("bf16", (2, 2), 64, 3000), ("f16", (8, 1), 16, 700)):
+        vt = torch.float64 if code == "f64" else torch.float32
+        for values in (True, False):
+            A = full_pattern(5, m, dtype=vt)
+            gen = torch.Generator(device=DEV).manual_seed(10)
+            q, k = (torch.randn(s, h, dim, generator=gen, device=DEV).to(DT[code]) for s, h in zip((5, m), heads))
+            vals = None
+            if values:
+                vals = 50 * torch.randn(5, m, generator=gen, device=DEV, dtype=vt)
+                vals[3] = -float("inf")
+                vals = vals.reshape(1, -1)
+            opts = L.make_attn_opts(q.dtype, *heads, dim, 0.3, *((0, *x.stride()[:2]) for x in (q, k, k)), lse_pairs=True)
+            o, ml = torch.empty_like(q), torch.empty(5, heads[0], 2, dtype=vt, device=DEV)
+            L.sla_attention_prepare(A.handle, opts, 1)
+            ws = torch.empty(max(1, L.sla_attention_workspace_bytes(A.handle, opts)), dtype=torch.uint8, device=DEV)
+            L.sla_attention(A.handle, q, k, k, vals, o, None, ml, opts, ws)
+            res, err = attention(A.rowptr.cpu().numpy(), A.colind.cpu().numpy(), *(x.double().cpu().numpy() for x in (q, k, k)),
+                                 None if vals is None else vals[0].double().cpu().numpy(), 0.3, None, code)
+            ml = ml.double().cpu().numpy()
+            dead = ~np.isfinite(res["lse"])
+            assert dead.any() == values and np.array_equal(ml[dead], np.tile([-np.inf, 0.0], (int(dead.sum()), 1)))
+            got = ml[..., 0][~dead] + np.log(ml[..., 1][~dead])
+            assert within(got, res["lse"][~dead], err["lse"][~dead]) <= 1.0
+            opts.lse_pairs = 0
+            room = torch.empty(1 << 20, dtype=torch.uint8, device=DEV)
+            with pytest.raises(L.SlaError, match="lse_pairs"):
+                L.sla_attention_grad(A.handle, q, k, k, vals, o, torch.empty(10, dtype=vt, device=DEV), q, q, None, None, None,
+                                     opts, room)
