@@ -20,6 +20,7 @@ import operator
 from dataclasses import dataclass
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 
@@ -194,7 +195,7 @@ class CSR:
         last dimension is copied if it is not contiguous, and in 16 bits a tensor
         whose rows do not start on 16 bytes; other strides are used as they are.
         Returns o shaped like q.  Sums have a fixed order: equal calls give equal
-        bits.
+        bits.  Forward-mode derivatives are refused.
         """
         scale = None if scale is None else float(scale)
         # what depends on shapes, strides and types alone is checked and laid out once
@@ -206,8 +207,9 @@ class CSR:
             if len(self._attn_calls) >= 64:
                 self._attn_calls.clear()
             self._attn_calls[key] = call
-        if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
-                                        (values is not None and values.requires_grad)):
+        # inside a forward-mode level the function refuses inputs that carry a tangent
+        if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
+                                         (values is not None and values.requires_grad))) or _forward_mode():
             if q.dim() == 3:
                 return _Attention.apply(self, call, q.unsqueeze(0), k.unsqueeze(0), v.unsqueeze(0), values).squeeze(0)
             return _Attention.apply(self, call, q, k, v, values)
@@ -313,6 +315,10 @@ class _Solve(torch.autograd.Function):
         gv = A.grad_values(lam, x).reshape(values.shape) if ctx.needs_input_grad[1] else None
         gb = lam.reshape(gx.shape) if ctx.needs_input_grad[2] else None
         return None, gv, gb, None
+
+
+def _forward_mode() -> bool:
+    return getattr(forward_ad, "_current_level", 0) >= 0
 
 
 def _on_device(device):

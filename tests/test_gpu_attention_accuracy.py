@@ -198,3 +198,33 @@ def test_pairs_of_maximum_and_sum():
             with pytest.raises(L.SlaError, match="lse_pairs"):
                 L.sla_attention_grad(A.handle, q, k, k, vals, o, torch.empty(10, dtype=vt, device=DEV), q, q, None, None, None,
                                      opts, room)
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("at", range(4))
+def test_forward_mode_is_refused(at, grad):
+    """A tangent of any input is refused, not dropped, as matvec does; other inputs
+    within a forward-mode level, and calls after it, are computed as before."""
+    A = full_pattern(3, 5, dtype=torch.float32)
+    ts = [torch.randn(s, 2, 16, device=DEV) for s in (3, 5, 5)] + [torch.randn(1, 15, device=DEV)]
+    want = A.attention(*ts)
+    with torch.set_grad_enabled(grad), torch.autograd.forward_ad.dual_level():
+        dual = list(ts)
+        dual[at] = torch.autograd.forward_ad.make_dual(ts[at], torch.ones_like(ts[at]))
+        with pytest.raises((NotImplementedError, RuntimeError), match="jvp|forward"):
+            A.attention(*dual)
+        with pytest.raises((NotImplementedError, RuntimeError), match="jvp|forward"):
+            A.attention(*(t[None] if t.dim() == 3 else t for t in dual))
+        assert torch.equal(A.attention(*ts), want)
+    assert torch.equal(A.attention(*ts), want)
+
+
+def test_function_transforms_are_refused():
+    A = full_pattern(3, 5, dtype=torch.float32)
+    q, k = torch.randn(3, 2, 16, device=DEV), torch.randn(5, 2, 16, device=DEV)
+    with pytest.raises(RuntimeError):
+        torch.func.jvp(lambda x: A.attention(x, k, k), (q,), (q,))
+    with pytest.raises(RuntimeError):
+        torch.func.vmap(lambda x: A.attention(x, k, k))(q.expand(4, -1, -1, -1))
+    with pytest.raises(RuntimeError):
+        torch.func.grad(lambda x: A.attention(x, k, k).sum())(q)
