@@ -24,11 +24,10 @@
 //
 // Scores: 16-bit products, exact, summed in 32 bits.  Weights are not rounded to
 // 16 bits: they multiply as tf32 (the 16-bit operand is exact in it), as a sum of
-// two 11-bit parts in the forward pass and for float16 gradients (11 bits), rounded
-// to 11 bits for bfloat16 gradients (8 bits), which keeps the outputs as good as
-// 32-bit products.  The forward pass needs both parts whatever its type: the
-// backward subtracts D = dout . o from numbers of its size, and the values' gradient
-// shows the difference in 32 bits.
+// two 11-bit parts, which hold a weight to 2^-20 of itself.  One part would show
+// where terms cancel: the gradients' weights ds sum to zero over a row, so what its
+// keys share must leave no trace in dq (keys with a common offset of 16: dq off by
+// 5e-3 with one part), and D = dout . o is subtracted from numbers of its size.
 //
 // What bounds it is neither the memory nor the tensor pipe (15 to 20 % active) but
 // the instructions of the masked softmax, the reads of shared memory and the waits
@@ -372,13 +371,12 @@ struct Sums {
             o[nb][3] *= hi;
         }
     }
-    // The weights of one half of a chunk in two parts, or one.
-    static __device__ __forceinline__ void split(const float (&w)[4], uint32_t (&hi)[4], uint32_t (&lo)[4], bool two) {
+    // The weights of one half of a chunk in two parts.
+    static __device__ __forceinline__ void split(const float (&w)[4], uint32_t (&hi)[4], uint32_t (&lo)[4]) {
         const float v[4] = {w[0], w[2], w[1], w[3]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (two) hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
-            else asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi[i]) : "f"(v[i]));
+            hi[i] = __float_as_uint(v[i]) & 0xffffe000u;
             lo[i] = __float_as_uint(v[i] - __uint_as_float(hi[i]));
         }
     }
@@ -386,10 +384,10 @@ struct Sums {
     // zero, so a sum that stayed in it over a long row would drift (1500 entries: by
     // 3.6e-6, a row of products in rounded sums 5e-7).  A chunk is summed from zero
     // there and added to the running sums with rounding to nearest.
-    __device__ __forceinline__ void add(const float (&w)[2][4], const uint32_t (&x)[4][D / 16], bool two) {
+    __device__ __forceinline__ void add(const float (&w)[2][4], const uint32_t (&x)[4][D / 16]) {
         uint32_t hi[2][4], lo[2][4];
-        split(w[0], hi[0], lo[0], two);
-        split(w[1], hi[1], lo[1], two);
+        split(w[0], hi[0], lo[0]);
+        split(w[1], hi[1], lo[1]);
         // four blocks at a time, so that a product does not wait for the one before it
         constexpr int W = D / 16, G = W % 2 == 0 ? 2 : 1;
 #pragma unroll
@@ -408,12 +406,10 @@ struct Sums {
                         else mma_tf32(t[2 * i + e], hi[1], y[i][e], y[i][2 + e]);
                     }
                 }
-                if (two) {
 #pragma unroll
-                    for (int i = 0; i < G; ++i)
+                for (int i = 0; i < G; ++i)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) mma_tf32(t[2 * i + e], lo[h], y[i][e], y[i][2 + e]);
-                }
+                    for (int e = 0; e < 2; ++e) mma_tf32(t[2 * i + e], lo[h], y[i][e], y[i][2 + e]);
             }
 #pragma unroll
             for (int i = 0; i < 2 * G; ++i) {
@@ -443,12 +439,12 @@ struct Sums {
     // drop_unused.
     template <int PITCH>
     __device__ __forceinline__ void add_chunk(const float (&w)[2][4], unsigned stage, int g, int c, bool drop,
-                                              unsigned used, bool two = std::is_same_v<T, __half>) {
+                                              unsigned used) {
         uint32_t x[4][D / 16];
 #pragma unroll
         for (int j = 0; j < 4; ++j) read_sum<D>(x[j], stage + 2 * c * PITCH + (8 * (j >> 1) + (j & 1)) * PITCH, g);
         if (drop) drop_unused(x, used);
-        add(w, x, two);
+        add(w, x);
     }
     // Row g (i = 0) or g + 8 (i = 1) to its D elements at p.  Of every group of
     // blocks this thread holds consecutive elements, first those of column 2c.
@@ -1006,7 +1002,7 @@ tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
                         s[blk][e] = weight<VALS>(t[blk][e]);
                         l[j][e >> 1] += s[blk][e];
                     }
-                acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used, true);
+                acc[j].template add_chunk<R::kPitch>(s, at + R::kTensor, g, c, VALS && drop, used);
             }
         }
         // A NaN among the sums, or a sum of weights that is none (which the outputs

@@ -452,8 +452,9 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * little or nothing of log l.
  * out_wide: NULL, or for 16-bit types a float array like out that receives o
  * before its rounding (ignored for the others).  Sums,
- * maxima and weights are held in 32 bits (64 for SLA_F64) and every sum has a
- * fixed order: equal calls give equal bits.
+ * maxima and weights are held in 32 bits (64 for SLA_F64; 16-bit heads of a multiple
+ * of 16 elements up to 128 multiply weights rounded to 2^-20 of themselves) and every
+ * sum has a fixed order: equal calls give equal bits.
  *
  * sla_attention_grad needs lse in pairs (SLA_ERR_INVALID without opts.lse_pairs) and
  * the unrounded o of the forward call (out, or

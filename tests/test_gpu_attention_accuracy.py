@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import differentiable_sparse_linear_csr_b200 as sla
+from tests import attention_oracle
 from tests.attention_oracle import attention, within
 
 pytestmark = pytest.mark.gpu
@@ -228,3 +229,90 @@ def test_function_transforms_are_refused():
         torch.func.vmap(lambda x: A.attention(x, k, k))(q.expand(4, -1, -1, -1))
     with pytest.raises(RuntimeError):
         torch.func.grad(lambda x: A.attention(x, k, k).sum())(q)
+
+
+TIGHT = (2.0 ** -24, 2.0 ** -20)           # sums in 32 bits, weights to 2^-20 of themselves: both 16-bit types
+
+
+def random_rows(lengths, heads, dim, code, seed=0, offset=0.0):
+    """A pattern of rows of the given lengths, with values (every 7th -inf); keys share
+    `offset` in every element."""
+    rng = np.random.default_rng(11)
+    m = max(lengths) + 13
+    ci = np.concatenate([np.sort(rng.choice(m, size=c, replace=False)) for c in lengths]).astype(np.int32)
+    rp = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    new = lambda *s: torch.randn(*s, generator=gen, device=DEV)  # noqa: E731
+    n = len(lengths)
+    q, k, v, do = new(n, heads[0], dim), new(m, heads[1], dim) + offset, new(m, heads[1], dim), new(n, heads[0], dim)
+    vt = torch.float64 if code == "f64" else torch.float32
+    vals = new(1, ci.shape[0]).to(vt)
+    vals[0, ::7] = -float("inf")
+    A = sla.CSR(torch.from_numpy(rp).to(DEV), torch.from_numpy(ci).to(DEV), n_cols=m, dtype=vt)
+    return A, *(x.to(DT[code]) for x in (q, k, v)), vals, do.to(DT[code])
+
+
+ROWS = {"split": [60, 17, 64, 65, 5000, 0, 63, 1, 129, 16], "whole": [5, 0, 33, 64, 1, 16, 17, 40, 3]}
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("heads,dim", [((2, 2), 64), ((4, 4), 32), ((8, 1), 16), ((6, 2), 128), ((1, 1), 20)])
+@pytest.mark.parametrize("code", ["f64", "f32", "bf16", "f16"])
+def test_outputs_before_their_rounding(code, heads, dim, rows, monkeypatch):
+    """o in 32 bits, lse, and the gradients to the bounds of weights in two parts, on
+    whole and on joined rows."""
+    A, q, k, v, vals, do = random_rows(ROWS[rows], heads, dim, code)
+    if code in ("bf16", "f16"):
+        ut = attention_oracle.CODES[code][1]
+        monkeypatch.setitem(attention_oracle.CODES, code, (TIGHT[0], 0.0, TIGHT[1]))
+    o, wide, lse = forward_parts(A, q, k, v, vals)
+    res, err = oracle_of(A, q, k, v, vals, None, code)
+    worst = {"wide": within(wide.double().cpu().numpy(), res["o"], err["o"]),
+             "lse": within(np.where(np.isfinite(res["lse"]), lse.double().cpu().numpy(), 0.0),
+                           np.where(np.isfinite(res["lse"]), res["lse"], 0.0), err["lse"])}
+    assert np.array_equal(np.isneginf(lse.double().cpu().numpy()), np.isneginf(res["lse"]))
+    assert torch.equal(o, wide.to(o.dtype))
+    if code in ("bf16", "f16"):
+        monkeypatch.setitem(attention_oracle.CODES, code, (TIGHT[0], ut, TIGHT[1]))
+    got = training(A, q, k, v, vals, do)
+    res, err = oracle_of(A, q, k, v, vals, do, code)
+    worst |= {x: within(g, res[x], err[x]) for x, g in zip(("o", "dq", "dk", "dv", "dvals"), (*got[:4], got[4][0]))}
+    assert all(w <= 1.0 for w in worst.values()), worst
+
+
+@pytest.mark.parametrize("code", ["f32", "bf16", "f16"])
+def test_what_keys_share_leaves_no_trace_in_dq(code):
+    """256 keys of a row share an offset of 512: ds sums to zero over a row, so the
+    offset cancels from dq = scale sum ds k if the weights ds keep their bits.  q = 0 and
+    small integers elsewhere: p = 2^-8, dp, D (multiples of 2^-8) and ds (20 bits) are
+    exact, so what is left is the rounding of the sums: 16 chunks to nearest, u each, and
+    4 products of a chunk truncated, 2 u each (32-bit heads: 64 steps of 4 entries, their
+    partial sums near zero like the total): 32 u sum |ds| |k| covers both; then the
+    output's own.  Weights of 11 bits would be off by 2^-12 of each term."""
+    n, m, H, D = 6, 256, 2, 64
+    A = full_pattern(n, m, dtype=torch.float32)
+    gen = torch.Generator(device=DEV).manual_seed(12)
+    ints = lambda lo, hi, *s: torch.randint(lo, hi + 1, s, generator=gen, device=DEV).double()  # noqa: E731
+    K = 512 * torch.sign(ints(0, 1, D) - 0.5) + 4 * ints(-2, 2, m, H, D)
+    V, G = ints(-8, 8, m, H, D), ints(-8, 8, n, H, D)
+    q = torch.zeros(n, H, D, device=DEV, dtype=DT[code], requires_grad=True)
+    k, v, do = (x.to(DT[code]) for x in (K, V, G))
+    assert torch.equal(k.double(), K)
+    (dq,) = torch.autograd.grad(A.attention(q, k, v), [q], do)
+    dp = torch.einsum("ihd,jhd->ihj", G, V)
+    ds = (dp - dp.mean(2, keepdim=True)) / m
+    want = torch.einsum("ihj,jhd->ihd", ds, K) * D ** -0.5
+    ut = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[code]
+    bound = 32 * 2.0 ** -24 * torch.einsum("ihj,jhd->ihd", ds.abs(), K.abs()) * D ** -0.5 + ut * want.abs()
+    assert bool(((dq.double() - want).abs() <= bound).all()), float(((dq.double() - want).abs() / bound).max())
+
+
+@pytest.mark.parametrize("heads", [(64, 64), (64, 1), (66, 11)])
+@pytest.mark.parametrize("code", ["f32", "bf16"])
+def test_split_rows_with_many_heads(code, heads):
+    """Plans for 64 and more systems and heads, with rows and columns that are split."""
+    A, q, k, v, vals, do = random_rows(ROWS["split"], heads, 16, code, seed=3)
+    got = training(A, q, k, v, vals, do)
+    res, err = oracle_of(A, q, k, v, vals, do, code)
+    worst = {x: within(g, res[x], err[x]) for x, g in zip(("o", "dq", "dk", "dv", "dvals"), (*got[:4], got[4][0]))}
+    assert all(w <= 1.0 for w in worst.values()), worst
