@@ -26,6 +26,7 @@ SLA_STRATEGY_AUTO, SLA_STRATEGY_GRID, SLA_STRATEGY_BLOCK, SLA_STRATEGY_CLUSTER =
 SLA_OP_SPMV, SLA_OP_CG, SLA_OP_ADJOINT, SLA_OP_GRAD = 0, 1, 2, 3
 SLA_GRAD_ACCUMULATE, SLA_GRAD_SHIFT_SHARED = 1, 2
 SLA_NORM_L2, SLA_NORM_MAX = 0, 1
+SLA_ATTN_NO_VALS, SLA_ATTN_NO_DVALS, SLA_ATTN_NO_DQ, SLA_ATTN_NO_DK_DV = 2, 4, 8, 16
 
 STATUS_NAMES = {0: "converged", 1: "not_converged", 2: "breakdown", 3: "nonfinite",
                 4: "fixed_done", 5: "timed_out"}

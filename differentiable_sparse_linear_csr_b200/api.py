@@ -372,6 +372,7 @@ class _AttentionCall:
         self.wide = torch.float64 if q.dtype == torch.float64 else torch.float32
         self.lse = A.batch * A.n_rows * H * (8 if q.dtype == torch.float64 else 4)
         self.ready = [False, False]
+        self.rooms = {}
         self.opts = [self.options(q, k, v, pairs=train) for train in (False, True)]
         self.back = {}                           # options of the gradients, by the strides they depend on
 
@@ -386,8 +387,14 @@ class _AttentionCall:
     def prepare(self, A, opts, backward):
         if not self.ready[backward]:
             L.sla_attention_prepare(A.handle, opts, backward)
-            self.workspace = [L.sla_attention_workspace_bytes(A.handle, opts, x) for x in range(backward + 1)]
             self.ready[0] = self.ready[backward] = True
+
+    def room(self, A, opts, what):
+        """Workspace bytes of a prepared call (what: see sla_attention_workspace_bytes)."""
+        n = self.rooms.get(what)
+        if n is None:
+            n = self.rooms[what] = L.sla_attention_workspace_bytes(A.handle, opts, what)
+        return n
 
     def forward(self, A, q, k, v, values, train):
         """(o, its 32-bit form or None, the rows' (m, l) or None, q, k, v as the kernels read them)"""
@@ -399,7 +406,7 @@ class _AttentionCall:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         with _on_device(A.device):
             self.prepare(A, opts, train)
-            room = self.workspace[0]
+            room = self.room(A, opts, 0 if vals is not None else L.SLA_ATTN_NO_VALS)
             if train:
                 lse = torch.empty(A.batch, A.n_rows, q.shape[-2], 2, dtype=self.wide, device=A.device)
                 wide = torch.empty(out.shape, dtype=self.wide, device=A.device) if q.element_size() == 2 else None
@@ -433,7 +440,10 @@ class _Attention(torch.autograd.Function):
             opts = call.back.get(key)
             if opts is None:
                 opts = call.back[key] = call.options(q, k, v, go)
-            ws = _workspace(call.workspace[1], A.device)
+            what = 1 | (0 if vals is not None else L.SLA_ATTN_NO_VALS) | \
+                (0 if dvals is not None else L.SLA_ATTN_NO_DVALS) | (0 if dq is not None else L.SLA_ATTN_NO_DQ) | \
+                (0 if dk is not None or dv is not None else L.SLA_ATTN_NO_DK_DV)
+            ws = _workspace(call.room(A, opts, what), A.device)
             L.sla_attention_grad(A.handle, q, k, v, vals, out, lse, go, dq, dk, dv, dvals, opts, ws)
         return None, None, dq, dk, dv, dvals
 

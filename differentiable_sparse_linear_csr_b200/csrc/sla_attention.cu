@@ -999,24 +999,28 @@ const AttnPlan &plan_of(const Csr *h, const sla_attn_opts *o, bool transposed) {
     return h->attn->tile[transposed][attn_tile_kind(o)][l];
 }
 
-AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, bool backward) {
+// `what`: as for sla_attention_workspace_bytes.
+AttnWs attn_ws(const Csr *h, const sla_attn_opts *o, int what) {
     const size_t acc = acc_size(o->dtype), B = (size_t)h->batch, H = (size_t)o->heads, D = (size_t)o->dim;
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
+    const bool tiled = attn_tiled(o), vals = !(what & SLA_ATTN_NO_VALS), dvals = vals && !(what & SLA_ATTN_NO_DVALS),
+               dq = !(what & SLA_ATTN_NO_DQ), cols = !(what & SLA_ATTN_NO_DK_DV);
     AttnWs w;
-    if (!backward) {
-        if (attn_tiled(o) && h->dtype == SLA_F64) w.vals_w = B * (size_t)h->nnz * sizeof(float);
+    // the values as the tiles read them: in 32 bits, and for dk and dv in A^T's order
+    if (tiled && vals && (h->dtype == SLA_F64 || ((what & 1) && cols))) w.vals_w = B * (size_t)h->nnz * sizeof(float);
+    if (!(what & 1)) {
         w.part = B * p.n_slots * p.rows * H * D * acc;
         w.part_ml = B * p.n_slots * p.rows * H * 2 * acc;
         return w;
     }
-    if (attn_tiled(o)) {
+    if (tiled) {
         w.stat = B * H * (size_t)h->n_rows * sizeof(float4);
-        w.ds = B * H * (size_t)h->nnz * sizeof(float);
-        w.vals_w = B * (size_t)h->nnz * sizeof(float);
-    } else {
+        if (dvals) w.ds = B * H * (size_t)h->nnz * sizeof(float);
+    } else if (cols || dvals) {
         w.pds = B * (size_t)h->nnz * H * 2 * acc;
     }
-    w.part = std::max(B * p.n_slots * p.rows * H * D * acc, B * pt.n_slots * pt.rows * (size_t)o->kv_heads * 2 * D * acc);
+    if (dq) w.part = B * p.n_slots * p.rows * H * D * acc;
+    if (cols) w.part = std::max(w.part, B * pt.n_slots * pt.rows * (size_t)o->kv_heads * 2 * D * acc);
     return w;
 }
 
@@ -1140,8 +1144,8 @@ extern "C" sla_status sla_attention_prepare(sla_csr_t hh, const sla_attn_opts *o
 extern "C" size_t sla_attention_workspace_bytes(sla_csr_t hh, const sla_attn_opts *o, int32_t backward) {
     const Csr *h = reinterpret_cast<const Csr *>(hh);
     clear_error();
-    if (!h || check_opts("sla_attention_workspace_bytes", o) != SLA_OK || !plans_ready(h, o, backward != 0)) return 0;
-    return attn_ws(h, o, backward != 0).total();
+    if (!h || check_opts("sla_attention_workspace_bytes", o) != SLA_OK || !plans_ready(h, o, backward & 1)) return 0;
+    return attn_ws(h, o, backward).total();
 }
 
 extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, const void *v, const void *vals,
@@ -1161,7 +1165,7 @@ extern "C" sla_status sla_attention(sla_csr_t hh, const void *q, const void *k, 
     if (st != SLA_OK) return st;
     cudaStream_t s = as_stream(stream);
     if (!plans_ready(h, o, false) && (st = prepare(h, o, false, s)) != SLA_OK) return st;
-    const AttnWs ww = attn_ws(h, o, false);
+    const AttnWs ww = attn_ws(h, o, vals ? 0 : SLA_ATTN_NO_VALS);
     const size_t need = ww.total();
     SLA_REQUIRE(need == 0 || (ws && ws_bytes >= need), "sla_attention: workspace too small (%zu < %zu)", ws_bytes, need);
     SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention: workspace must be 256-byte aligned");
@@ -1205,7 +1209,8 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     cudaStream_t s = as_stream(stream);
     if (!dq && !dk && !dv && !dvals) return SLA_OK;
     if (!plans_ready(h, o, true) && (st = prepare(h, o, true, s)) != SLA_OK) return st;
-    const AttnWs w = attn_ws(h, o, true);
+    const AttnWs w = attn_ws(h, o, 1 | (vals ? 0 : SLA_ATTN_NO_VALS) | (dvals ? 0 : SLA_ATTN_NO_DVALS) |
+                                       (dq ? 0 : SLA_ATTN_NO_DQ) | (dk || dv ? 0 : SLA_ATTN_NO_DK_DV));
     SLA_REQUIRE(w.total() == 0 || (ws && ws_bytes >= w.total()), "sla_attention_grad: workspace too small (%zu < %zu)",
                 ws_bytes, w.total());
     SLA_REQUIRE(((uintptr_t)ws & 255) == 0, "sla_attention_grad: workspace must be 256-byte aligned");
@@ -1218,12 +1223,11 @@ extern "C" sla_status sla_attention_grad(sla_csr_t hh, const void *q, const void
     a.dv = dv;
     a.dvals = dvals;
     Carver c(ws);
-    a.pds = c.take<char>(w.pds);
+    a.pds = w.pds ? c.take<char>(w.pds) : nullptr;
     a.stat = reinterpret_cast<float4 *>(c.take<char>(w.stat));
-    a.ds_out = dvals ? reinterpret_cast<float *>(c.take<char>(w.ds)) : (c.take<char>(w.ds), nullptr);
+    a.ds_out = w.ds ? reinterpret_cast<float *>(c.take<char>(w.ds)) : nullptr;
     a.vals_w = reinterpret_cast<float *>(c.take<char>(w.vals_w));
     a.part = c.take<char>(w.part);
-    if (!dk && !dv && !dvals) a.pds = nullptr;
     const AttnPlan &p = plan_of(h, o, false), &pt = plan_of(h, o, true);
     const bool tiled = attn_tiled(o);
     const int kind = attn_tile_kind(o);

@@ -472,6 +472,9 @@ sla_status sla_laplacian_grad(sla_edges_t e, const void *lambda, const void *x, 
  * sla_attention_prepare before capturing, and before asking for the workspace
  * size (0 until then).  It prepares what calls with `opts` need (its strides do
  * not matter), or with NULL what calls of any type with heads == kv_heads need.
+ * sla_attention_workspace_bytes: `backward` is 0 for the forward call and 1 for the
+ * gradients, plus the SLA_ATTN_NO_* flags of what the call does not have; a call asks
+ * for no more than its own pointers need.
  * Workspaces are 256-byte aligned; calls in flight at the same time need distinct ones.  With 16-bit
  * types and dim a multiple of 16 up to 128, addresses and strides of the head
  * tensors must be multiples of 16 bytes and row strides below 2^31 elements
@@ -491,6 +494,9 @@ typedef struct {
     int64_t do_stride[3];     /* of dout (sla_attention_grad) */
     int32_t lse_pairs;        /* 1: lse holds pairs (m, l); else 0 */
 } sla_attn_opts;
+/* Added to `backward` of sla_attention_workspace_bytes: the call has no vals, no dvals,
+ * no dq, or neither dk nor dv. */
+enum { SLA_ATTN_NO_VALS = 2, SLA_ATTN_NO_DVALS = 4, SLA_ATTN_NO_DQ = 8, SLA_ATTN_NO_DK_DV = 16 };
 sla_status sla_attention_prepare(sla_csr_t h, const sla_attn_opts *opts, int32_t backward,
                                  void *stream);
 size_t sla_attention_workspace_bytes(sla_csr_t h, const sla_attn_opts *opts, int32_t backward);

@@ -316,3 +316,65 @@ def test_split_rows_with_many_heads(code, heads):
     res, err = oracle_of(A, q, k, v, vals, do, code)
     worst = {x: within(g, res[x], err[x]) for x, g in zip(("o", "dq", "dk", "dv", "dvals"), (*got[:4], got[4][0]))}
     assert all(w <= 1.0 for w in worst.values()), worst
+
+
+@pytest.mark.parametrize("vt", [torch.float32, torch.float64])
+@pytest.mark.parametrize("code,heads,dim", [("f32", (2, 1), 32), ("f64", (2, 2), 16), ("bf16", (4, 2), 64), ("bf16", (2, 2), 128),
+                                            ("f16", (4, 4), 16), ("bf16", (2, 2), 24)])
+def test_workspaces_of_what_a_call_needs(code, heads, dim, vt):
+    """Every set of gradients, with and without values, in a workspace of exactly the
+    bytes asked for: the bits of the whole call, and nothing written behind it."""
+    from differentiable_sparse_linear_csr_b200 import _lib as L
+    A, q, k, v, vals, do = random_rows(ROWS["split"], heads, dim, code)
+    A = sla.CSR(A.rowptr, A.colind, n_cols=A.n_cols, dtype=vt)
+    vals = vals.to(vt)
+    wide = torch.float64 if code == "f64" else torch.float32
+    opts = L.make_attn_opts(q.dtype, *heads, dim, 0.25, *((0, *x.stride()[:2]) for x in (q, k, v, do)), lse_pairs=True)
+    L.sla_attention_prepare(A.handle, opts, 1)
+
+    def room(what):
+        need = L.sla_attention_workspace_bytes(A.handle, opts, what)
+        return need, torch.full((need + 4096,), 171, dtype=torch.uint8, device=DEV)
+
+    for has_values in (True, False):
+        x = vals if has_values else None
+        no = 0 if has_values else L.SLA_ATTN_NO_VALS
+        o, o_wide = torch.empty_like(q), torch.empty(q.shape, dtype=wide, device=DEV)
+        ml = torch.empty(*q.shape[:2], 2, dtype=wide, device=DEV)
+        need, ws = room(no)
+        L.sla_attention(A.handle, q, k, v, x, o, o_wide, ml, opts, ws[:need])
+        assert bool((ws[need:] == 171).all())
+        whole = None
+        for wanted in range(15 if has_values else 7, 0, -1):
+            dq, dk, dv = (torch.empty_like(t) if wanted >> i & 1 else None for i, t in enumerate((q, k, v)))
+            dvals = torch.empty_like(vals) if wanted & 8 else None
+            need, ws = room(1 | no | (0 if dvals is not None else L.SLA_ATTN_NO_DVALS) | (0 if dq is not None else L.SLA_ATTN_NO_DQ) |
+                            (0 if dk is not None or dv is not None else L.SLA_ATTN_NO_DK_DV))
+            assert need <= L.sla_attention_workspace_bytes(A.handle, opts, 1)
+            L.sla_attention_grad(A.handle, q, k, v, x, o_wide if q.element_size() == 2 else o, ml, do, dq, dk, dv, dvals, opts,
+                                 ws[:need])
+            assert bool((ws[need:] == 171).all())
+            whole = whole or (dq, dk, dv, dvals)
+            assert all(t is None or torch.equal(t, u) for t, u in zip((dq, dk, dv, dvals), whole)), wanted
+            if need > 0:
+                with pytest.raises(L.SlaError, match="workspace"):
+                    L.sla_attention_grad(A.handle, q, k, v, x, o_wide if q.element_size() == 2 else o, ml, do, dq, dk, dv, dvals,
+                                         opts, ws[:need - 1])
+
+
+def test_training_asks_for_no_memory_that_it_leaves_alone():
+    """A million entries and 16 heads: 67 MB for 32-bit ds of every entry and head, which
+    only the values' gradient reads, and 134 MB for pairs (p, ds), which dq does not."""
+    A = full_pattern(512, 2048, dtype=torch.float32)
+    for code, only_q in (("bf16", False), ("f32", True)):
+        q, k, v = (torch.randn(s, 16, 16, device=DEV).to(DT[code]) for s in (512, 2048, 2048))
+        ts = [q.requires_grad_()] if only_q else [t.requires_grad_() for t in (q, k, v)]
+        do = torch.randn_like(q)
+        torch.autograd.grad(A.attention(q, k, v), ts, do)
+        o = A.attention(q, k, v)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        torch.autograd.grad(o, ts, do)
+        torch.cuda.synchronize()
+        assert torch.cuda.max_memory_allocated() - before < 32 << 20
