@@ -208,7 +208,7 @@ def prepare(case, seed):
         # the pattern's handle, which a program makes once and keeps
         state["A"] = sla.CSR(state["rowptr"], state["colind"], n_cols=_sizes(case)[1], batch=case["batch"],
                              dtype=torch.float64 if case["dtype"] == "f64" else torch.float32)
-        state["A"].prepare_attention(backward=case["train"])
+        state["A"].prepare_attention(backward=case["train"], heads_per_key=case["heads"] // case["kv_heads"])
         if case["train"]:
             state["wrt"] = [state[x].requires_grad_() for x in ("q", "k", "v", "values") if state[x] is not None]
     return state
