@@ -704,6 +704,14 @@ def _dense_list(tensors):
     return [t if _dense(t) else t.detach().contiguous() for t in tensors]
 
 
+def _check_copied(outs):
+    """Outputs that the library does not see: refused before anything is written."""
+    if any(n > 1 and st == 0 for o in outs for n, st in zip(o.shape, o.stride())):
+        raise ValueError("an output has several elements in one place (an expanded tensor)")
+    if len({(o.data_ptr(), o.shape, o.stride()) for o in outs if o.numel()}) < sum(1 for o in outs if o.numel()):
+        raise ValueError("one output is given twice")
+
+
 def _norm_buffers(codes, device):
     return (torch.empty((), dtype=torch.float64 if L.SLA_F64 in codes else torch.float32, device=device),
             _workspace(L.sla_norm_workspace_bytes(len(codes)), device))
@@ -757,6 +765,7 @@ def clip_by_global_norm(tensors, max_norm: float, *, norm_type: float = 2.0, out
         # an output laid out otherwise than its input is written by way of a copy
         dst = [o if o is s or (o.stride() == s.stride() and _dense(o)) else torch.empty_like(s)
                for o, s in zip(outs, src)]
+        _check_copied([o for o, d in zip(outs, dst) if o is not d])
     with _on_device(tensors[0].device):
         norm, ws = _norm_buffers(codes, tensors[0].device)
         L.sla_clip_norm(len(src), L.tensor_list(src, codes, dst), kind, max_norm, norm, ws)

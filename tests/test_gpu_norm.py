@@ -182,3 +182,26 @@ def test_writing_counts_as_a_change():
     sla.clip_by_global_norm([x], 1.0, out=[x])
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         torch.autograd.grad(y, w)
+
+
+def test_outputs_written_by_way_of_a_copy_are_checked_first():
+    """A gradient that two parameters share, or that is expanded, is refused before any
+    other gradient is scaled, also where it is not dense."""
+    wide = torch.ones(4, 6, device=DEV)
+    for grads in ([wide[:, :3]] * 2, [torch.ones(1, device=DEV).expand(5)], [wide[::2, :3]], [wide[:0, :3]] * 2):
+        params = [torch.zeros(7, device=DEV, requires_grad=True)] + \
+            [torch.zeros(g.shape, device=DEV, requires_grad=True) for g in grads]
+        params[0].grad = torch.full((7,), 5.0, device=DEV)
+        for p, g in zip(params[1:], grads):
+            p.grad = g
+        bad = len(grads) > 1 and grads[0].numel() > 0 or 0 in grads[0].stride()
+        if bad:
+            with pytest.raises(ValueError, match="twice|expanded"):
+                sla.clip_grad_norm_(params, 1.0)
+            assert torch.equal(params[0].grad, torch.full((7,), 5.0, device=DEV)) and torch.equal(wide, torch.ones_like(wide))
+        else:
+            want = torch.sqrt(sum((p.grad.double() ** 2).sum() for p in params))
+            norm = sla.clip_grad_norm_(params, 1.0)
+            assert abs(float(norm) - float(want)) <= 1e-6 * float(want)
+            assert torch.allclose(params[0].grad, torch.full((7,), 5.0 / float(want), device=DEV), rtol=1e-6)
+            wide.fill_(1.0)
