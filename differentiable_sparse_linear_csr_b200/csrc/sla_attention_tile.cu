@@ -1145,8 +1145,11 @@ __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__
 }
 
 // By A's rows: dq, and ds of every entry if asked for.
+// With values two blocks an SM from 64 elements a warp on: three would spill (graph of
+// 100 k rows, 8 heads of 64: 207 us against 224; of 32, 122 against 166; of 48, 220
+// against 199).
 template <typename T, int D, int KH, bool VALS, bool PACK>
-__global__ void __launch_bounds__(kTileThreads, D * KH <= 64 && !(PACK && VALS) ? 3 : 2)
+__global__ void __launch_bounds__(kTileThreads, D * KH <= (VALS ? 48 : 64) && !(PACK && VALS) ? 3 : 2)
 tile_bwd_rows_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
     using R = Ring<D, KH, false>;
     extern __shared__ __align__(128) char smem[];
