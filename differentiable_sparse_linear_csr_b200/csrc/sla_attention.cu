@@ -161,8 +161,8 @@ sla_status build_items(AttnPlan *p, unsigned *len, int seg_len, int64_t fill, in
 // share of the work, are not split, nor tiles up to kWhole columns: a short part
 // spends more on its partial result than on its entries.  Measured, forward pass:
 //   tiles, 24 an SM against 8: 300 rows over 1500 columns, 64 systems and heads,
-//   107 -> 116 us and a join of 26; 513 rows of 256 entries, 2 key heads of 128
-//   elements, 26 -> 30 us;
+//   112 -> 116 us and a join of 22; 513 rows of 256 entries, 2 key heads of 128
+//   elements, 23 -> 28 us;
 //   rows, float32, 8, 64 and 128 an SM: 30000 rows of 20 entries and one of 20000, 8
 //   heads of 32, 1150, 205 and 137 us; 64 full rows over 4096 columns, 292, 60 and 45 us;
 //   rows whole up to 5 shares against 4: 513 rows of 256 entries, 8 heads of 32, 66
@@ -299,8 +299,8 @@ void free_attn_plans(Csr *h) {
 // the item are walked STEP at a time with their loads issued together.
 // Bound by the gathers (2 * dim elements an entry and head, mostly from L1 and L2)
 // and, for short rows, by the instructions around them.  128 systems of a 32 x 32
-// grid, 4 heads of 32 float32 elements (67 MB a tensor): forward 97 us, dq and the
-// stored (p, ds) 140 us, dk and dv 96 us, 2.8 to 3.0 TB/s of the bytes that cannot
+// grid, 4 heads of 32 float32 elements (67 MB a tensor): forward 98 us, dq and the
+// stored (p, ds) 150 us, dk and dv 96 us, 2.7 to 3.0 TB/s of the bytes that cannot
 // be left out.
 namespace {
 
@@ -874,8 +874,8 @@ sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {
 }
 
 // Entries in flight: 4 or 5, whichever leaves fewer places empty on a row of mean
-// length (a 5-point row in one step instead of two: the 128 systems above take 97,
-// 140 and 96 us with 5, 112, 153 and 103 with 4); 2 where the registers hold no
+// length (a 5-point row in one step instead of two: the 128 systems above take 98,
+// 150 and 96 us with 5, 112, 166 and 102 with 4); 2 where the registers hold no
 // more.
 template <typename T, int VEC, int L, int NV>
 sla_status launch_rows(int what, const AttnArgs &a, cudaStream_t s) {

@@ -5,8 +5,7 @@
 // rows of a mesh or graph share columns, so a k or v row is fetched once for the
 // tile instead of once an entry, and the scores of all 16 x 16 pairs are a
 // matrix product; pairs that are not stored are masked by the chunk's row bits.
-// Most of that product is thrown away (a 5-point grid uses 5 of 34 columns a
-// row), which costs nothing: the gathers bound the kernel.
+// Most of that product is thrown away (a 5-point grid uses 5 of 50 columns a row).
 //
 // Each warp copies the chunk's rows into its own ring of shared-memory stages
 // (cp.async, a few chunks ahead: the loads' latency is what the kernels wait for)
@@ -29,13 +28,15 @@
 // keys share must leave no trace in dq (keys with a common offset of 16: dq off by
 // 5e-3 with one part), and D = dout . o is subtracted from numbers of its size.
 //
-// What bounds it is neither the memory nor the tensor pipe (15 to 20 % active) but
-// the instructions of the masked softmax, the reads of shared memory and the waits
-// between them, with 12 warps an SM.  Measured: 1024 x 1024 grid, 4 heads of 32
-// bfloat16 elements, forward 500 us (2.1 TB/s of the bytes that cannot be left out;
-// the row kernels take 733); graph of 100 k rows and 1.2 M entries, 8 heads of 64:
-// forward 185 us, dq and ds 193, dk and dv 219, 2.7 to 3.3 TB/s (row kernels 528,
-// 696, 495).
+// What bounds it is neither the memory (a quarter of the DRAM rate) nor the tensor
+// pipe (23 to 36 % active) but chains of dependent instructions, the masked softmax
+// of all 256 pairs between two products and reads of shared memory, with 8 to 12
+// warps an SM to cover them: issue slots 45 to 53 % busy, most waits for results of
+// a fixed latency, then for loads.  Measured: 1024 x 1024 grid, 4 heads of 32
+// bfloat16 elements, forward 524 us (2.1 TB/s of the bytes that cannot be left out;
+// the row kernels take 772); graph of 100 k rows and 1.2 M entries, 8 heads of 64:
+// forward 202 us, dq and ds 208, dk and dv 246, 2.5 to 3.0 TB/s (row kernels 334,
+// 458, 406).
 //
 // Masked pairs have weight 0, but 0 times an infinity or a NaN is a NaN.  A column
 // that every row leaves out (values of -inf: padding, which may hold anything) is
@@ -606,7 +607,7 @@ template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.as
 
 // A warp's ring of stages: two gathered tensors of HEADS heads, 16 rows each,
 // and with STAT four numbers a column and head.  The padded pitch beats pieces
-// permuted in an unpadded row (508 against 546 us on the 1024 x 1024 grid): no
+// permuted in an unpadded row (by 7 % on the 1024 x 1024 grid): no
 // address arithmetic at a read.  Three stages where 12 warps' rings (8 with STAT) fit an SM.
 template <int D, int HEADS, bool STAT>
 struct Ring {
@@ -854,8 +855,8 @@ __device__ __forceinline__ unsigned my_share(unsigned total, unsigned &first, un
 
 // KH key heads a warp; with one, the query heads of the tile share it.
 // Blocks an SM, here and below: 3 while the sums and the own rows leave room in 168
-// registers, else 2.  (1024 x 1024 grid, 2 heads of 32 a warp: 526 us cold with 3,
-// 612 with 2, 528 with 4 and spills, and dq of the graph 232 -> 380 us with 4.)
+// registers, else 2.  (1024 x 1024 grid, 2 heads of 32 a warp: 524 us with 3, 597
+// with 2, 536 with 4 and spills; forward of the graph 202, 222 and 297.)
 template <typename T, int D, int KH, bool VALS, bool PACK>
 __global__ void __launch_bounds__(kTileThreads, D * KH <= 64 && !(PACK && VALS) ? 3 : 2)
 tile_forward_kernel(const __grid_constant__ AttnArgs a, unsigned total) {
@@ -1110,7 +1111,7 @@ __device__ __noinline__ void slow_bwd_rows(const AttnArgs &a, const TileWork &w)
 // in the unit of relative(), -inf where the row has no weight.  A weight's derivative
 // p (dp - D) is then exp(s - m) (dp / l - D / l), one multiply-add as without l.
 // G lanes a row and head, 8 elements each.  Bound by memory: 100 k rows, 8 heads of
-// 64, 307 MB in 50 us (6.1 TB/s).
+// 64, 326 MB in 54 to 60 us (5.4 to 6.0 TB/s).
 template <typename T, int G>
 __global__ void __launch_bounds__(256) tile_delta_kernel(const __grid_constant__ AttnArgs a, int64_t count, float unit) {
     const int64_t x = (blockIdx.x * (int64_t)256 + threadIdx.x) / G;
@@ -1360,7 +1361,7 @@ __device__ __noinline__ void slow_bwd_cols(const AttnArgs &a, const TileWork &w,
 // By A^T's rows: dk (DK) and dv (DV) of 16 columns of A for KH key heads, the
 // query heads that share one following each other.  Wide heads take two launches:
 // both sums and both own operands would not fit the registers, and 3 blocks an SM
-// would spill (219 us with 2 on the graph above).  The values come in
+// would spill (246 us with 2, 396 with 3 on the graph above).  The values come in
 // A^T's order (tile_values_kernel).
 template <typename T, int D, int KH, bool DK, bool DV, bool VALS, bool PACK>
 __global__ void __launch_bounds__(kTileThreads, 2)
@@ -1623,8 +1624,8 @@ sla_status launch_delta(const AttnArgs &a, cudaStream_t s) {
 }
 
 // Key heads a warp: as many as fill 128 bytes of a gathered row, if every query
-// head has its own and their number allows (1024 x 1024 grid, heads of 32: 526 us
-// with two, 654 with one, cold).
+// head has its own and their number allows (1024 x 1024 grid, heads of 32: 524 us
+// with two, 655 with one).
 template <typename T, int D, bool VALS>
 sla_status launch_tile_heads(int what, const AttnArgs &a, cudaStream_t s) {
     if constexpr (D <= 32) {

@@ -288,12 +288,12 @@ int num_sms() {
     return n;
 }
 
-// Chunks that one block takes as fast as two launches would, or faster (clipping 1, 2,
-// 4 and 8 chunks of float32: 2.2, 2.9, 4.6 and 7.3 us against 4.0 to 4.4; a call's
-// launch on the host 4 us less).
+// Chunks that one block takes alone.  Clipping 1, 2, 4 and 8 chunks of float32: 2.2, 2.9,
+// 4.6 and 7.3 us against 4.0 to 4.4 for two launches.  At 4 chunks the device loses 0.2
+// to 0.6 us, and the host saves a launch of about 4.
 constexpr int kSmallChunks = 4;
 
-// Pass 1 over the list, tables of N tensors at a time; then the norm alone, or
+// Pass 1 over the list, tables of kTable tensors at a time; then the norm alone, or
 // pass 2.  Partial results: at most kMaxPartials a table.
 template <int KIND>
 sla_status run_norm(const sla_tensor *list, int n, bool clip, double max_norm, void *norm, int f64, double *part,
